@@ -47,6 +47,16 @@ class kvb_model_spec(ctypes.Structure):
 _SPEC_P = ctypes.POINTER(kvb_model_spec)
 
 
+class kvb_cache8(ctypes.Structure):
+    _fields_ = [("page_tokens", ctypes.c_int32), ("n_pages", ctypes.c_int64), ("k", _P), ("v", _P), ("k_scale", _P),
+                ("v_scale", _P)]
+
+
+class kvb_seqs(ctypes.Structure):
+    _fields_ = [("n_seq", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("max_tokens", ctypes.c_int32),
+                ("max_kv", ctypes.c_int32), ("page_table", _P), ("seq_off", _P), ("seq_pos", _P), ("kv_len", _P)]
+
+
 class kvb_kernel_time(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 32), ("launches", ctypes.c_int64), ("total_ms", ctypes.c_double)]
 
@@ -77,6 +87,12 @@ SIGNATURES = {
     "kvb_ridge_solve": (ctypes.c_int, [_P, _P, _I32P, _I32P, ctypes.c_double, ctypes.c_int, _P, _P, _P, _P, _P]),
     "kvb_attention_cosine": (ctypes.c_int, [_P, ctypes.c_int, _P, ctypes.c_int32, _P, ctypes.c_int64, _P, _P, _P,
                                             _P, _P, ctypes.c_int64, _P, _P]),
+    "kvb_cache8_write": (ctypes.c_int, [_P, _P, _P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int, _P, _P,
+                                        ctypes.c_int64, _P]),
+    "kvb_cache8_read": (ctypes.c_int, [_P, _P, _P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int, _P, _P,
+                                       ctypes.c_int64, _P]),
+    "kvb_cache8_attention": (ctypes.c_int, [_P, _P, _P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int, _P,
+                                            ctypes.c_int32, ctypes.c_int64, ctypes.c_double, _P, _P, _P]),
 }
 
 _lib = None
@@ -341,3 +357,105 @@ def kvb_attention_cosine(ctx: Ctx, q, q_pos, k_a, v_a, k_b, v_b, kv_pos, cos_out
     _check(load_library().kvb_attention_cosine(
         ctx.handle, _dtype_of(q), _dev(q), int(q.shape[1]), _dev(q_pos), int(q.shape[2]), _dev(k_a), _dev(v_a),
         _dev(k_b), _dev(v_b), _dev(kv_pos), int(k_a.shape[2]), _dev(cos_out), _stream(stream)))
+
+
+# ------------------------------------------------------------------ paged 8-bit cache
+
+class Cache8:
+    """The four tensors of a paged 8-bit cache (see kvb_cache8 in include/kvb.h).
+
+    k, v [L_t][n_pages][H][page_tokens][d], one byte an element (float8_e4m3fn or
+    uint8); k_scale, v_scale float32 [L_t][n_pages][H], powers of two.
+    """
+
+    def __init__(self, ctx: Ctx, k, v, k_scale, v_scale):
+        import torch
+        L, n_pages, H, page, d = k.shape
+        if (L, H, d) != (ctx.L_t, ctx.H, ctx.d):
+            raise ValueError(f"cache8 codes must be [{ctx.L_t}][n_pages][{ctx.H}][page_tokens][{ctx.d}], got "
+                             f"{list(k.shape)}")
+        for t in (k, v):
+            if t.shape != k.shape or t.dtype not in (torch.float8_e4m3fn, torch.uint8):
+                raise ValueError("cache8 codes must be two float8_e4m3fn or uint8 tensors of one shape")
+        for t in (k_scale, v_scale):
+            if tuple(t.shape) != (L, n_pages, H) or t.dtype != torch.float32:
+                raise ValueError(f"cache8 scales must be float32 [{L}][{n_pages}][{H}]")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.n_pages, self.page_tokens = int(n_pages), int(page)
+        self.struct = kvb_cache8(self.page_tokens, self.n_pages, _dev(k), _dev(v), _dev(k_scale), _dev(v_scale))
+        self.ref = ctypes.addressof(self.struct)
+
+
+def kvb_cache8_create(ctx: Ctx, n_pages: int, page_tokens: int = 64) -> Cache8:
+    """Allocate a cache of n_pages pages for every target layer on the context's device."""
+    import torch
+    dev = torch.device("cuda", ctx.device)
+    shape = (ctx.L_t, int(n_pages), ctx.H, int(page_tokens), ctx.d)
+    code = lambda: torch.empty(shape, dtype=torch.float8_e4m3fn, device=dev)
+    scale = lambda: torch.empty(shape[:3], dtype=torch.float32, device=dev)
+    return Cache8(ctx, code(), code(), scale(), scale())
+
+
+class Seqs:
+    """The sequences of a call, packed on its token axis (see kvb_seqs in include/kvb.h).
+
+    page_table int32 [n_seq][max_pages], seq_off int32 [n_seq + 1], seq_pos int32
+    [n_seq] and kv_len int32 [n_seq] or None, on the device.  The kernels read the
+    tensors, so a captured call sees what they hold when it is replayed.
+    """
+
+    def __init__(self, page_table, seq_off, seq_pos, max_tokens: int, max_kv: int = 0, kv_len=None):
+        import torch
+        n = int(page_table.shape[0])
+        want = {"page_table": (page_table, (n, int(page_table.shape[1]))), "seq_off": (seq_off, (n + 1,)),
+                "seq_pos": (seq_pos, (n,))}
+        if kv_len is not None:
+            want["kv_len"] = (kv_len, (n,))
+        for name, (t, shape) in want.items():
+            if t.dtype != torch.int32 or tuple(t.shape) != shape:
+                raise ValueError(f"{name} must be int32 {list(shape)}, got {t.dtype} {list(t.shape)}")
+        self.tensors = (page_table, seq_off, seq_pos, kv_len)
+        self.struct = kvb_seqs(n, int(page_table.shape[1]), int(max_tokens), int(max_kv), _dev(page_table),
+                               _dev(seq_off), _dev(seq_pos), _dev(kv_len))
+        self.ref = ctypes.addressof(self.struct)
+
+
+def _same_shape(name, t, shape, dtype):
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+
+
+def _cache8_rw(call, ctx: Ctx, cache: Cache8, seqs: Seqs, k, v, l_begin, stream):
+    if k.dim() != 4 or k.shape[1] != ctx.H or k.shape[3] != ctx.d:
+        raise ValueError(f"k must be [n_layers][{ctx.H}][T][{ctx.d}], got {list(k.shape)}")
+    _same_shape("v", v, k.shape, k.dtype)
+    _check(call(ctx.handle, cache.ref, seqs.ref, l_begin, k.shape[0], _dtype_of(k), _dev(k), _dev(v), k.shape[2],
+                _stream(stream)))
+
+
+def kvb_cache8_write(ctx: Ctx, cache: Cache8, seqs: Seqs, k, v, l_begin: int = 0, stream=None):
+    """Quantise the tokens k, v [n_layers][H][T][d] (bf16 or fp32) into layers l_begin .. of the cache."""
+    _cache8_rw(load_library().kvb_cache8_write, ctx, cache, seqs, k, v, l_begin, stream)
+
+
+def kvb_cache8_read(ctx: Ctx, cache: Cache8, seqs: Seqs, k, v, l_begin: int = 0, stream=None):
+    """Read the sequences' tokens back into k, v [n_layers][H][T][d] (bf16 or fp32)."""
+    _cache8_rw(load_library().kvb_cache8_read, ctx, cache, seqs, k, v, l_begin, stream)
+
+
+def kvb_cache8_attention(ctx: Ctx, cache: Cache8, seqs: Seqs, q, out, lse=None, l_begin: int = 0, scale: float = 0.0,
+                         stream=None):
+    """out [n_layers][Hq][T][d] = attention of the queries q over the cache; lse float32 [n_layers][Hq][T] or None.
+
+    Token i of a sequence is at position seq_pos + i and sees the cache positions up
+    to its own (and below kv_len where that is given).  scale 0 is 1/sqrt(d).
+    """
+    if q.dim() != 4 or q.shape[3] != ctx.d:
+        raise ValueError(f"q must be [n_layers][Hq][T][{ctx.d}], got {list(q.shape)}")
+    _same_shape("out", out, q.shape, q.dtype)
+    if lse is not None:
+        import torch
+        _same_shape("lse", lse, q.shape[:3], torch.float32)
+    _check(load_library().kvb_cache8_attention(
+        ctx.handle, cache.ref, seqs.ref, l_begin, q.shape[0], _dtype_of(q), _dev(q), q.shape[1], q.shape[2], scale,
+        _dev(out), _dev(lse), _stream(stream)))

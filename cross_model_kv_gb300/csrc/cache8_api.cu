@@ -1,0 +1,176 @@
+// Entry points of the paged 8-bit cache: argument checks, workspace, launches.
+#include <cmath>
+
+#include "cache8.h"
+#include "kvb_host.h"
+
+using namespace kvb;
+
+namespace {
+
+// What the three calls check alike; fills the kernels' views.
+kvb_status check_call(kvb_ctx* c, const kvb_cache8* cache, const kvb_seqs* seqs, int32_t l_begin, int32_t n_layers,
+                      kvb_dtype dtype, int64_t T, const char* what, c8::Cache* cv, c8::Seqs* sv) {
+    const std::string w(what);
+    if (!c) return fail(KVB_ERR_INVALID_ARG, "ctx is NULL");
+    if (!cache || !seqs) return fail(KVB_ERR_INVALID_ARG, w + ": cache or seqs is NULL");
+    if (dtype != KVB_F32 && dtype != KVB_BF16) return fail(KVB_ERR_UNSUPPORTED, "dtype must be KVB_F32 or KVB_BF16");
+    if (c->d != 16 && c->d != 32 && c->d != 64 && c->d != 128)
+        return fail(KVB_ERR_UNSUPPORTED, w + " supports head_dim 16, 32, 64 or 128");
+    const int pt = cache->page_tokens;
+    if (pt != 16 && pt != 32 && pt != 64 && pt != 128)
+        return fail(KVB_ERR_UNSUPPORTED, w + ": page_tokens must be 16, 32, 64 or 128");
+    if (cache->n_pages < 0 || cache->n_pages > 0x7fffffffLL) return fail(KVB_ERR_INVALID_ARG, w + ": bad n_pages");
+    if (l_begin < 0 || n_layers < 0 || l_begin > c->L_t - n_layers)
+        return fail(KVB_ERR_INVALID_ARG, w + ": layers outside [0, L_tgt)");
+    if (T < 0) return fail(KVB_ERR_INVALID_ARG, "T < 0");
+    if (T > 0x7fffffffLL) return fail(KVB_ERR_UNSUPPORTED, "T above 2^31-1");
+    if (seqs->n_seq < 0 || seqs->max_pages < 0 || seqs->max_tokens < 0 || seqs->max_kv < 0)
+        return fail(KVB_ERR_INVALID_ARG, w + ": negative size in seqs");
+    if (seqs->max_tokens > T) return fail(KVB_ERR_INVALID_ARG, w + ": max_tokens above T");
+    kvb_status st;
+    if ((st = take_device_error(c)) != KVB_OK) return st;
+    if (T > 0 && seqs->n_seq > 0 && n_layers > 0 && seqs->max_tokens > 0) {
+        if ((st = check_device_ptrs({cache->k, cache->v, cache->k_scale, cache->v_scale}, what)) != KVB_OK) return st;
+        for (const int32_t* p : {seqs->page_table, seqs->seq_off, seqs->seq_pos}) {
+            if (!p) return fail(KVB_ERR_INVALID_ARG, w + ": null device pointer in seqs");
+            if (reinterpret_cast<uintptr_t>(p) & 3u)
+                return fail(KVB_ERR_INVALID_ARG, w + ": device pointer in seqs not 4-byte aligned");
+        }
+        if (reinterpret_cast<uintptr_t>(seqs->kv_len) & 3u)
+            return fail(KVB_ERR_INVALID_ARG, w + ": device pointer in seqs not 4-byte aligned");
+    }
+    cv->code[0] = static_cast<uint8_t*>(cache->k);
+    cv->code[1] = static_cast<uint8_t*>(cache->v);
+    cv->scale[0] = cache->k_scale;
+    cv->scale[1] = cache->v_scale;
+    cv->n_pages = cache->n_pages;
+    cv->H = c->H;
+    cv->d = c->d;
+    cv->d_log2 = c->d == 16 ? 4 : c->d == 32 ? 5 : c->d == 64 ? 6 : 7;
+    cv->page = pt;
+    cv->page_log2 = pt == 16 ? 4 : pt == 32 ? 5 : pt == 64 ? 6 : 7;
+    cv->l_begin = l_begin;
+    cv->n_layers = n_layers;
+    sv->page_table = seqs->page_table;
+    sv->off = seqs->seq_off;
+    sv->pos = seqs->seq_pos;
+    sv->kv_len = seqs->kv_len;
+    sv->n_seq = seqs->n_seq;
+    sv->max_pages = seqs->max_pages;
+    sv->max_tokens = seqs->max_tokens;
+    const int64_t room = static_cast<int64_t>(seqs->max_pages) * pt;
+    const int64_t kv = seqs->max_kv > 0 && seqs->max_kv < room ? seqs->max_kv : room;
+    if (kv > 0x7fffff00LL) return fail(KVB_ERR_UNSUPPORTED, w + ": more than 2^31 cache positions in a sequence");
+    sv->max_kv = static_cast<int>(kv);
+    sv->T = T;
+    return KVB_OK;
+}
+
+bool empty(const c8::Cache& c, const c8::Seqs& q) {
+    return q.T == 0 || q.n_seq == 0 || c.n_layers == 0 || q.max_tokens == 0;
+}
+
+c8::Err call_err(const kvb_ctx* c) { return c8::Err{c->err_dev, c->err_mirror, c->timeout_ns}; }
+
+// Blocks of a read or write: (K or V, layer, head, sequence, page that its tokens can touch).
+bool too_many_blocks(const c8::Cache& c, const c8::Seqs& q) {
+    const double items = (static_cast<double>(q.max_tokens) + c.page - 2) / c.page + 1;
+    return items * q.n_seq * c.H * c.n_layers * 2 > 2147483647.0;
+}
+
+// Counters (zeroed once; every call leaves them at zero) followed by the partial outputs.
+kvb_status ensure_attn_ws(kvb_ctx* c, const c8::AttnPlan& p, cudaStream_t s) {
+    const size_t need = p.counter_bytes + p.partial_bytes;
+    if (need <= c->attn_ws_bytes && p.counter_bytes <= c->attn_ws_counters) return KVB_OK;
+    cudaError_t e;
+    if (c->attn_ws) {
+        if ((e = cudaDeviceSynchronize()) != cudaSuccess) return cuda_fail(e, "sync before growing the attention workspace");
+        cudaFree(c->attn_ws);
+        c->attn_ws = nullptr;
+        c->attn_ws_bytes = c->attn_ws_counters = 0;
+    }
+    // room for counters of larger calls to come, so that a batch that grows by a sequence does not reallocate
+    const size_t counters = p.counter_bytes < 65536 ? 65536 : 2 * p.counter_bytes;
+    const size_t bytes = counters + p.partial_bytes + p.partial_bytes / 4;
+    if ((e = cudaMalloc(&c->attn_ws, bytes)) != cudaSuccess) return cuda_fail(e, "cudaMalloc attention workspace");
+    if ((e = cudaMemset(c->attn_ws, 0, counters)) != cudaSuccess || (e = cudaStreamSynchronize(0)) != cudaSuccess)
+        return cuda_fail(e, "zeroing the attention workspace");
+    c->attn_ws_bytes = bytes;
+    c->attn_ws_counters = counters;
+    return KVB_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+kvb_status kvb_cache8_write(kvb_ctx* c, const kvb_cache8* cache, const kvb_seqs* seqs, int32_t l_begin,
+                            int32_t n_layers, kvb_dtype dtype, const void* k, const void* v, int64_t T, void* stream) {
+    g_last_error.clear();
+    c8::Cache cv{};
+    c8::Seqs sv{};
+    kvb_status st = check_call(c, cache, seqs, l_begin, n_layers, dtype, T, "kvb_cache8_write", &cv, &sv);
+    if (st != KVB_OK) return st;
+    if (empty(cv, sv)) return KVB_OK;
+    if ((st = check_device_ptrs({k, v}, "kvb_cache8_write")) != KVB_OK) return st;
+    if (too_many_blocks(cv, sv)) return fail(KVB_ERR_UNSUPPORTED, "kvb_cache8_write: more than 2^31-1 blocks in one call");
+    DeviceGuard g(c->device);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    ProfScope ps(c, s, "cache8_write");
+    const cudaError_t e = c8::launch_write(cv, sv, dtype, k, v, call_err(c), s);
+    return e == cudaSuccess ? KVB_OK : cuda_fail(e, "cache8 write launch");
+}
+
+kvb_status kvb_cache8_read(kvb_ctx* c, const kvb_cache8* cache, const kvb_seqs* seqs, int32_t l_begin,
+                           int32_t n_layers, kvb_dtype dtype, void* k, void* v, int64_t T, void* stream) {
+    g_last_error.clear();
+    c8::Cache cv{};
+    c8::Seqs sv{};
+    kvb_status st = check_call(c, cache, seqs, l_begin, n_layers, dtype, T, "kvb_cache8_read", &cv, &sv);
+    if (st != KVB_OK) return st;
+    if (empty(cv, sv)) return KVB_OK;
+    if ((st = check_device_ptrs({k, v}, "kvb_cache8_read")) != KVB_OK) return st;
+    if (too_many_blocks(cv, sv)) return fail(KVB_ERR_UNSUPPORTED, "kvb_cache8_read: more than 2^31-1 blocks in one call");
+    DeviceGuard g(c->device);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    ProfScope ps(c, s, "cache8_read");
+    const cudaError_t e = c8::launch_read(cv, sv, dtype, k, v, call_err(c), s);
+    return e == cudaSuccess ? KVB_OK : cuda_fail(e, "cache8 read launch");
+}
+
+kvb_status kvb_cache8_attention(kvb_ctx* c, const kvb_cache8* cache, const kvb_seqs* seqs, int32_t l_begin,
+                                int32_t n_layers, kvb_dtype dtype, const void* q, int32_t n_q_heads, int64_t T,
+                                double scale, void* out, float* lse, void* stream) {
+    g_last_error.clear();
+    c8::AttnArgs a{};
+    kvb_status st = check_call(c, cache, seqs, l_begin, n_layers, dtype, T, "kvb_cache8_attention", &a.c, &a.q);
+    if (st != KVB_OK) return st;
+    if (n_q_heads < c->H || n_q_heads % c->H)
+        return fail(KVB_ERR_INVALID_ARG, "n_q_heads must be a positive multiple of the KV heads");
+    if (!(scale >= 0.0) || !std::isfinite(scale)) return fail(KVB_ERR_INVALID_ARG, "scale must be finite and >= 0");
+    if (empty(a.c, a.q)) return KVB_OK;
+    if ((st = check_device_ptrs({q, out}, "kvb_cache8_attention")) != KVB_OK) return st;
+    if (reinterpret_cast<uintptr_t>(lse) & 3u)
+        return fail(KVB_ERR_INVALID_ARG, "kvb_cache8_attention: lse not 4-byte aligned");
+    DeviceGuard g(c->device);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    a.dtype = dtype;
+    a.query = q;
+    a.out = out;
+    a.lse = lse;
+    a.g = n_q_heads / c->H;
+    a.scale_log2 = static_cast<float>((scale > 0.0 ? scale : 1.0 / std::sqrt(static_cast<double>(c->d))) * 1.4426950408889634);
+    a.err = call_err(c);
+    const c8::AttnPlan p = c8::plan_attention(a.c, a.q, dtype, a.g, c->num_sms);
+    if (static_cast<int64_t>(p.row_blocks) * c->H > 65535 || static_cast<int64_t>(a.q.n_seq) * n_layers > 65535)
+        return fail(KVB_ERR_UNSUPPORTED, "kvb_cache8_attention: too many query rows, sequences or layers in one call");
+    if ((st = ensure_attn_ws(c, p, s)) != KVB_OK) return st;
+    a.counters = static_cast<int*>(c->attn_ws);
+    a.partial = reinterpret_cast<float*>(static_cast<char*>(c->attn_ws) + c->attn_ws_counters);
+    ProfScope ps(c, s, "cache8_attention");
+    const cudaError_t e = c8::launch_attention(a, p, s);
+    return e == cudaSuccess ? KVB_OK : cuda_fail(e, "cache8 attention launch");
+}
+
+}  // extern "C"

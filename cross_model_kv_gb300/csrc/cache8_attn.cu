@@ -1,0 +1,569 @@
+// Attention over the paged 8-bit cache: few query rows over many keys.
+//
+// For the g * n query rows of a (layer, sequence, KV head):
+//     s_rj = scale * q_r . k_j,  p_rj = 2^(s_rj log2(e) - m_r),
+//     o_r = sum_j p_rj v_j / sum_j p_rj.
+// Decoding reads every code once for 4 d g flops per 2 d bytes (16 flop/byte
+// at g = 8), far below the machine's ratio, so HBM bounds it and the layout
+// serves the loads: a warp takes 16 keys at a time straight from global memory
+// to registers, in the fragment order of mma.m16n8k16, with the keys as the
+// M rows.  Both contractions let their index be permuted freely:
+//   S^T = K Q^T  M = 16 keys, K = 16 dims, N = 8 query rows.  Lane (r, c) =
+//                (lane / 4, lane % 4) holds d/4 consecutive codes of keys r and
+//                r + 8; k step t takes its bytes 4t .. 4t+3, and Q is laid out to match.
+//   O^T = V^T P^T  M = 16 dims, K = 16 keys.  Lane (r, c) holds d/8 consecutive
+//                codes of keys 2c, 2c+1, 2c+8, 2c+9; a byte permute pairs two
+//                keys' codes of one dim, which is an A register after the
+//                conversion.  P^T comes from S^T by an 8 x 8 transpose in registers.
+// e4m3 converts to fp16 exactly.  A query row is scaled by a power of two to
+// at most 2^14 and enters as fp16 (bf16 rows: exact to 2^-28 of the row's
+// largest) or as an fp16 pair (fp32 rows); products and sums are fp32.
+//
+// Numerators carry the values' scale in the exponent: w_rj = 2^(s_rj log2(e) +
+// e_v(j) - mv_r) is what multiplies the codes, and the denominator sums
+// 2^(s_rj log2(e) - m_r); each has its own reference, so a page's scale, large
+// or small, costs neither range nor bits.  References are raised only when a
+// tile exceeds them by 2^8 (one vote per tile); weights are biased by 2^7, so fp16
+// holds them from 2^15 down to 2^-24 (2^-31 of the reference).
+//
+// Keys are split into chunks over CTAs where there are few rows; the last CTA
+// of a unit to arrive joins the chunks in order, so results do not depend on timing.
+#include "cache8.h"
+
+namespace kvb {
+namespace c8 {
+
+namespace {
+
+constexpr int NWARPS = 4;
+constexpr int NT = NWARPS * 32;
+constexpr int MAX_PAGES = 512;    // pages of one chunk, listed in shared memory
+constexpr float BIAS = 7.f;       // weights are taken against 2^-7 of the reference
+constexpr float MARGIN = 8.f;     // a reference is raised past this much
+constexpr float NO_REF = -3.0e38f;
+
+struct Params {
+    Cache c;
+    Seqs q;
+    const void* query;
+    void* out;
+    float* lse;
+    int g, row_blocks, chunk, splits;
+    float scale_log2;
+    int* counters;
+    float* partial;   // [unit][split][rows][d]
+    float4* part_stat;  // [unit][split][rows]: references and sum
+    Err err;
+};
+
+__device__ __forceinline__ float ex2(float x) {  // relative error about 2^-22
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Parts of one row's result, each with its references: first every part's
+// reference(), then every part's add().  st = (m, mv, sum, -).  A part that saw
+// nothing has NO_REF references and adds zeros; a NaN reaches the result.
+struct Joined {
+    float m = NO_REF, mv = NO_REF, sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    __device__ __forceinline__ void reference(const float4& st) {
+        m = fmaxf(m, st.x);
+        mv = fmaxf(mv, st.y);
+    }
+    __device__ __forceinline__ void add(const float4& st, const float4& o) {
+        const float f = ex2(st.y - mv);
+        sum = fmaf(ex2(st.x - m), st.z, sum);
+        acc.x = fmaf(f, o.x, acc.x);
+        acc.y = fmaf(f, o.y, acc.y);
+        acc.z = fmaf(f, o.z, acc.z);
+        acc.w = fmaf(f, o.w, acc.w);
+    }
+    // acc / sum * 2^(mv - m), the power in two halves: it may pass the range of one float
+    __device__ __forceinline__ float4 output() const {
+        const float half = ex2(0.5f * (mv - m)), f = sum == 0.f ? 0.f : half / sum;
+        return make_float4(acc.x * f * half, acc.y * f * half, acc.z * f * half, acc.w * f * half);
+    }
+    __device__ __forceinline__ float lse() const {
+        return sum == 0.f ? -INFINITY : (m - BIAS + log2f(sum)) * 0.693147180559945f;
+    }
+};
+
+// W consecutive 32-bit words (B bytes), read once: not kept in L1.
+template <int B>
+__device__ __forceinline__ void load_codes(const uint8_t* p, uint32_t* w) {
+    if constexpr (B == 32) {
+        asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                     : "l"(p));
+    } else if constexpr (B == 16) {
+        asm volatile("ld.global.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "l"(p));
+    } else if constexpr (B == 8) {
+        asm volatile("ld.global.L1::no_allocate.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+    } else if constexpr (B == 4) {
+        asm volatile("ld.global.b32 %0, [%1];" : "=r"(w[0]) : "l"(p));
+    } else {
+        uint16_t h;
+        asm volatile("ld.global.b16 %0, [%1];" : "=h"(h) : "l"(p));
+        w[0] = h;
+    }
+}
+
+// n consecutive query elements as fp32.
+__device__ __forceinline__ float2 load2(const __nv_bfloat16* p) {
+    const uint32_t u = __ldg(reinterpret_cast<const uint32_t*>(p));
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+__device__ __forceinline__ float2 load2(const float* p) { return __ldg(reinterpret_cast<const float2*>(p)); }
+__device__ __forceinline__ void store_out(__nv_bfloat16* p, float4 v) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+}
+__device__ __forceinline__ void store_out(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+
+template <typename T, int D, int NB>
+struct Shape8 {
+    static constexpr int PARTS = sizeof(T) == 4 ? 2 : 1;  // fp16 parts of a query element and of a weight
+    static constexpr int ROWS = 8 * NB;
+    static constexpr int KS = D / 16;                     // k steps of S, and M tiles of O
+    // per warp: its outputs, references and sums; then the page list of the chunk
+    static constexpr int Q_WORDS = PARTS * NB * KS * 2 * 32;
+    static constexpr size_t smem() {
+        return sizeof(float) * (NWARPS * ROWS * D + NWARPS * ROWS * 4) + 4 * Q_WORDS + MAX_PAGES * 12;
+    }
+};
+
+template <typename T, int D, int NB>
+__global__ void __launch_bounds__(NT) decode_kernel(const __grid_constant__ Params P) {
+    using S8 = Shape8<T, D, NB>;
+    constexpr int PARTS = S8::PARTS, ROWS = S8::ROWS, KS = S8::KS;
+    constexpr int KB = D / 4, VB = D / 8;                    // bytes of a lane: of a key row, of a value row
+    constexpr int KW = KB / 4, VW = VB >= 4 ? VB / 4 : 1;    // words
+    extern __shared__ float4 sm4[];
+    float* so = reinterpret_cast<float*>(sm4);               // [NWARPS][ROWS][D]
+    float4* stat = reinterpret_cast<float4*>(so + NWARPS * ROWS * D);  // [NWARPS][ROWS] references and sum
+    float* sqs = reinterpret_cast<float*>(stat);             // [ROWS] factors of the query rows, before that
+    uint32_t* sq = reinterpret_cast<uint32_t*>(stat + NWARPS * ROWS);  // query fragments
+    int* s_page = reinterpret_cast<int*>(sq + S8::Q_WORDS);
+    float* s_ks = reinterpret_cast<float*>(s_page + MAX_PAGES);  // key scale
+    float* s_ev = s_ks + MAX_PAGES;                              // exponent of the value scale
+    __shared__ int s_last;
+
+    const int split = blockIdx.x;
+    const int64_t unit = blockIdx.y + static_cast<int64_t>(blockIdx.z) * gridDim.y;
+    const int h = blockIdx.y % P.c.H;
+    const int rb = blockIdx.y / P.c.H;
+    const int s = blockIdx.z % P.q.n_seq;
+    const int l = blockIdx.z / P.q.n_seq;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int r = lane >> 2, c = lane & 3;
+
+    const SeqView sv = seq_view(P.q, s, P.err);
+    const int64_t rows = static_cast<int64_t>(sv.n) * P.g;
+    const int64_t row0 = static_cast<int64_t>(rb) * ROWS;
+    if (row0 >= rows) return;
+    // row = token * g + head of the group: rows of a block are close in position
+    const int nrows = static_cast<int>(min(static_cast<int64_t>(ROWS), rows - row0));
+    int64_t kv = P.q.kv_len ? static_cast<int64_t>(__ldg(P.q.kv_len + s)) : static_cast<int64_t>(sv.pos) + sv.n;
+    const int64_t room = min(static_cast<int64_t>(P.q.max_kv), static_cast<int64_t>(P.q.max_pages) << P.c.page_log2);
+    if (kv > room) {
+        if (threadIdx.x == 0) err_set(P.err, DEV_ERR_BAD_SEQ);
+        kv = room;
+    }
+    const int64_t pos_hi = sv.pos + (row0 + nrows - 1) / P.g;  // position of the block's last row
+    const int pos_lo = sv.pos + static_cast<int>(row0 / P.g);
+    const int kv_end = static_cast<int>(max(static_cast<int64_t>(0), min(kv, pos_hi + 1)));
+    const int active = max(1, (kv_end + P.chunk - 1) / P.chunk);
+    if (split >= active) return;
+    const int k0 = split * P.chunk, k1 = min(kv_end, k0 + P.chunk);
+
+    // the chunk's pages and scales
+    const int page0 = k0 >> P.c.page_log2;
+    const int npages = k1 > k0 ? ((k1 - 1) >> P.c.page_log2) - page0 + 1 : 0;
+    const int64_t layer = static_cast<int64_t>(P.c.l_begin) + l;
+    for (int i = threadIdx.x; i < npages; i += NT) {
+        int pid = __ldg(P.q.page_table + static_cast<int64_t>(s) * P.q.max_pages + page0 + i);
+        if (pid < 0 || pid >= P.c.n_pages) {
+            err_set(P.err, DEV_ERR_BAD_SEQ);
+            pid = -1;
+        }
+        s_page[i] = pid;
+        const int64_t b = (layer * P.c.n_pages + pid) * P.c.H + h;
+        s_ks[i] = pid < 0 ? 1.f : __ldg(P.c.scale[0] + b);
+        s_ev[i] = pid < 0 ? 0.f : static_cast<float>(exponent_of(__ldg(P.c.scale[1] + b)));
+    }
+
+    // query fragments (every warp needs all of them: row block b is laid out by warp b % NWARPS)
+    const T* query = static_cast<const T*>(P.query);
+    const int64_t hq0 = (static_cast<int64_t>(l) * P.c.H + h) * P.g;
+    for (int b = warp; b < NB; b += NWARPS) {
+        const int row = 8 * b + r;
+        float q[KB];
+        float amax = 0.f;
+        if (row < nrows) {
+            const int64_t gr = row0 + row;
+            const int64_t i = gr / P.g;
+            const T* p = query + ((hq0 + (gr - i * P.g)) * P.q.T + sv.tok0 + i) * D + c * KB;
+#pragma unroll
+            for (int e = 0; e < KB; e += 2) {
+                const float2 x = load2(p + e);
+                q[e] = x.x;
+                q[e + 1] = x.y;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < KB; ++e) q[e] = 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < KB; ++e) amax = fmaxf(amax, fabsf(q[e]));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        const int eq = max((__float_as_int(amax) >> 23) - 127, -100) - 13;  // amax 2^-eq in [2^13, 2^14)
+        const float inv = pow2(-eq);
+        if (c == 0) sqs[row] = pow2(eq) * P.scale_log2;
+#pragma unroll
+        for (int t = 0; t < KS; ++t)
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                const float a = q[4 * t + 2 * w] * inv, z = q[4 * t + 2 * w + 1] * inv;
+                const uint32_t hi = pack_half2(a, z);
+                sq[((b * KS + t) * 2 + w) * 32 + lane] = hi;
+                if constexpr (PARTS == 2) {
+                    const float2 f = float2_of(hi);
+                    sq[NB * KS * 64 + ((b * KS + t) * 2 + w) * 32 + lane] = pack_half2(a - f.x, z - f.y);
+                }
+            }
+    }
+    __syncthreads();
+    float qs[NB][2];  // log2(e) * scale * 2^eq of query rows 2c, 2c+1
+    int qpos[NB][2];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int row = 8 * b + 2 * c + j;
+            qs[b][j] = sqs[row];
+            qpos[b][j] = row < nrows ? sv.pos + static_cast<int>((row0 + row) / P.g) : INT32_MIN;
+        }
+    uint32_t qf[NB * PARTS == 1 ? KS : 1][2];  // in registers where one fragment set serves
+    if constexpr (NB * PARTS == 1) {
+#pragma unroll
+        for (int t = 0; t < KS; ++t)
+#pragma unroll
+            for (int w = 0; w < 2; ++w) qf[t][w] = sq[(t * 2 + w) * 32 + lane];
+    }
+    __syncthreads();  // sqs is free
+
+    float o[NB][KS][4];
+    float m[NB][2], mv[NB][2], sum[NB][2];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+#pragma unroll
+        for (int i = 0; i < KS; ++i) o[b][i][0] = o[b][i][1] = o[b][i][2] = o[b][i][3] = 0.f;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            m[b][j] = mv[b][j] = NO_REF;
+            sum[b][j] = 0.f;
+        }
+    }
+
+    const int64_t slab = layer * P.c.n_pages * P.c.H + h;  // block of page 0
+    uint32_t kw[2][KW], vw[4][VW];
+    auto load_k = [&](int j) {
+        const int pi = (j >> P.c.page_log2) - page0;
+        if (s_page[pi] < 0) {  // every key of the page is masked
+#pragma unroll
+            for (int x = 0; x < KW; ++x) kw[0][x] = kw[1][x] = 0;
+            return;
+        }
+        const int64_t blk = slab + static_cast<int64_t>(s_page[pi]) * P.c.H;
+        const uint8_t* p = P.c.code[0] + ((blk << P.c.page_log2) + (j & (P.c.page - 1))) * D;
+        load_codes<KB>(p + r * D + c * KB, kw[0]);
+        load_codes<KB>(p + (r + 8) * D + c * KB, kw[1]);
+    };
+    auto load_v = [&](int j) {
+        const int pi = (j >> P.c.page_log2) - page0;
+        if (s_page[pi] < 0) {
+#pragma unroll
+            for (int x = 0; x < VW; ++x) vw[0][x] = vw[1][x] = vw[2][x] = vw[3][x] = 0;
+            return;
+        }
+        const int64_t blk = slab + static_cast<int64_t>(s_page[pi]) * P.c.H;
+        const uint8_t* p = P.c.code[1] + ((blk << P.c.page_log2) + (j & (P.c.page - 1))) * D + r * VB;
+        load_codes<VB>(p + (2 * c) * D, vw[0]);
+        load_codes<VB>(p + (2 * c + 1) * D, vw[1]);
+        load_codes<VB>(p + (2 * c + 8) * D, vw[2]);
+        load_codes<VB>(p + (2 * c + 9) * D, vw[3]);
+    };
+    int j = k0 + 16 * warp;
+    if (j < k1) {
+        load_k(j);
+        load_v(j);
+    }
+    for (; j < k1; j += 16 * NWARPS) {
+        const int jn = j + 16 * NWARPS;
+        const int pi = (j >> P.c.page_log2) - page0;
+        const bool bad = s_page[pi] < 0;
+        const float ks = s_ks[pi], ev = s_ev[pi];
+        // S^T = K Q^T
+        float sc[NB][4];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) sc[b][0] = sc[b][1] = sc[b][2] = sc[b][3] = 0.f;
+#pragma unroll
+        for (int t = 0; t < KS; ++t) {
+            const uint32_t a0 = half2_of_lo(kw[0][t]), a2 = half2_of_hi(kw[0][t]);
+            const uint32_t a1 = half2_of_lo(kw[1][t]), a3 = half2_of_hi(kw[1][t]);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                if constexpr (NB * PARTS == 1) {
+                    mma16816(sc[b], a0, a1, a2, a3, qf[t][0], qf[t][1]);
+                } else {
+#pragma unroll
+                    for (int p = 0; p < PARTS; ++p) {
+                        const uint32_t* f = sq + ((p * NB + b) * KS + t) * 64 + lane;
+                        mma16816(sc[b], a0, a1, a2, a3, f[0], f[32]);
+                    }
+                }
+            }
+        }
+        if (jn < k1) load_k(jn);
+        // scores in base 2, masked; keys r, r + 8 and query rows 2c, 2c + 1 of each row block
+        const bool whole = !bad && j + 16 <= k1 && j + 15 <= pos_lo;
+        bool raise = false;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                float x = sc[b][u] * (ks * qs[b][u & 1]);
+                if (!whole) {
+                    const int key = j + r + 8 * (u >> 1);
+                    if (bad || key >= k1 || key > qpos[b][u & 1]) x = -INFINITY;
+                }
+                sc[b][u] = x;
+                raise |= x > m[b][u & 1] + MARGIN || x + ev > mv[b][u & 1] + MARGIN;
+            }
+        if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    float top = fmaxf(sc[b][q], sc[b][q + 2]);
+#pragma unroll
+                    for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+                    const float mn = fmaxf(m[b][q], top), mvn = fmaxf(mv[b][q], top + ev);
+                    sum[b][q] *= ex2(m[b][q] - mn);
+                    const float f = ex2(mv[b][q] - mvn);
+                    m[b][q] = mn;
+                    mv[b][q] = mvn;
+#pragma unroll
+                    for (int i = 0; i < KS; ++i) {
+                        o[b][i][q] *= f;
+                        o[b][i][q + 2] *= f;
+                    }
+                }
+        }
+        uint32_t pt[NB][PARTS][2];
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                float w[2];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const float x = sc[b][2 * hf + q];
+                    sum[b][q] += ex2(x - (m[b][q] - BIAS));
+                    w[q] = ex2(x + ev - (mv[b][q] - BIAS));
+                }
+                const uint32_t hi = pack_half2(w[0], w[1]);
+                pt[b][0][hf] = transpose8x8(hi);
+                if constexpr (PARTS == 2) {
+                    const float2 f = float2_of(hi);
+                    pt[b][PARTS - 1][hf] = transpose8x8(pack_half2(w[0] - f.x, w[1] - f.y));
+                }
+            }
+        if (j + 16 > k1) {  // slots past the last visible key may hold anything
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (j + 2 * c + (u & 1) + 8 * (u >> 1) >= k1) {
+#pragma unroll
+                    for (int x = 0; x < VW; ++x) vw[u][x] = 0;
+                }
+        }
+        // O^T += V^T P^T; M tile i: dims r * d/8 + 2i and + 2i + 1
+#pragma unroll
+        for (int x = 0; x < VW; ++x) {
+            const uint32_t e0 = __byte_perm(vw[0][x], vw[1][x], 0x5140), e1 = __byte_perm(vw[0][x], vw[1][x], 0x7362);
+            const uint32_t f0 = __byte_perm(vw[2][x], vw[3][x], 0x5140), f1 = __byte_perm(vw[2][x], vw[3][x], 0x7362);
+#pragma unroll
+            for (int y = 0; y < (VB >= 4 ? 2 : 1); ++y) {
+                const uint32_t e = y ? e1 : e0, f = y ? f1 : f0;
+                const uint32_t a0 = half2_of_lo(e), a1 = half2_of_hi(e), a2 = half2_of_lo(f), a3 = half2_of_hi(f);
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int p = 0; p < PARTS; ++p) mma16816(o[b][2 * x + y], a0, a1, a2, a3, pt[b][p][0], pt[b][p][1]);
+            }
+        }
+        if (jn < k1) load_v(jn);
+    }
+
+    // join the warps: outputs in units of 2^mv, sums in units of 2^m (both with the bias)
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            float t = sum[b][q];
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) t += __shfl_xor_sync(0xffffffffu, t, x);
+            const int row = 8 * b + 2 * c + q;
+            if (r == 0) stat[warp * ROWS + row] = make_float4(m[b][q], mv[b][q], t, 0.f);
+            float* dst = so + (warp * ROWS + row) * D + r * VB;
+#pragma unroll
+            for (int i = 0; i < KS; ++i) *reinterpret_cast<float2*>(dst + 2 * i) = make_float2(o[b][i][q], o[b][i][q + 2]);
+        }
+    __syncthreads();
+
+    T* out = static_cast<T*>(P.out);
+    auto row_of = [&](int row) {  // index of a row in [n_layers][Hq][T]
+        const int64_t gr = row0 + row, i = gr / P.g;
+        return (hq0 + (gr - i * P.g)) * P.q.T + sv.tok0 + i;
+    };
+    const int64_t part0 = (unit * P.splits + split) * ROWS;
+    for (int e = threadIdx.x; e < nrows * (D / 4); e += NT) {
+        const int row = e / (D / 4), d4 = e % (D / 4);
+        Joined z;
+#pragma unroll
+        for (int w = 0; w < NWARPS; ++w) z.reference(stat[w * ROWS + row]);
+#pragma unroll
+        for (int w = 0; w < NWARPS; ++w)
+            z.add(stat[w * ROWS + row], reinterpret_cast<const float4*>(so + (w * ROWS + row) * D)[d4]);
+        if (active == 1) {
+            store_out(out + row_of(row) * D + 4 * d4, z.output());
+            if (d4 == 0 && P.lse) P.lse[row_of(row)] = z.lse();
+        } else {
+            reinterpret_cast<float4*>(P.partial + (part0 + row) * D)[d4] = z.acc;
+            if (d4 == 0) P.part_stat[part0 + row] = make_float4(z.m, z.mv, z.sum, 0.f);
+        }
+    }
+    if (active == 1) return;
+
+    // the last chunk to arrive joins them, in order
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        const int n = atomicAdd(P.counters + unit, 1);
+        s_last = n == active - 1;
+        if (s_last) P.counters[unit] = 0;
+    }
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+    const int64_t u0 = unit * P.splits * ROWS;
+    for (int e = threadIdx.x; e < nrows * (D / 4); e += NT) {
+        const int row = e / (D / 4), d4 = e % (D / 4);
+        Joined z;
+        for (int i = 0; i < active; ++i) z.reference(__ldcg(P.part_stat + u0 + i * ROWS + row));
+#pragma unroll 4
+        for (int i = 0; i < active; ++i)
+            z.add(__ldcg(P.part_stat + u0 + i * ROWS + row),
+                  __ldcg(reinterpret_cast<const float4*>(P.partial + (u0 + i * ROWS + row) * D) + d4));
+        store_out(out + row_of(row) * D + 4 * d4, z.output());
+        if (d4 == 0 && P.lse) P.lse[row_of(row)] = z.lse();
+    }
+}
+
+template <typename T, int D, int NB>
+cudaError_t launch_decode(const Params& P, cudaStream_t s) {
+    constexpr size_t smem = Shape8<T, D, NB>::smem();
+    cudaError_t e = cudaFuncSetAttribute(decode_kernel<T, D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    dim3 grid(P.splits, P.c.H * P.row_blocks, P.q.n_seq * P.c.n_layers);
+    decode_kernel<T, D, NB><<<grid, NT, smem, s>>>(P);
+    return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t launch_rows(const Params& P, int rows, cudaStream_t s) {
+    switch (rows) {
+        case 8: return launch_decode<T, D, 1>(P, s);
+        case 16: return launch_decode<T, D, 2>(P, s);
+        default: return launch_decode<T, D, 4>(P, s);
+    }
+}
+
+template <typename T>
+cudaError_t launch_dim(const Params& P, int rows, cudaStream_t s) {
+    switch (P.c.d) {
+        case 16: return launch_rows<T, 16>(P, rows, s);
+        case 32: return launch_rows<T, 32>(P, rows, s);
+        case 64: return launch_rows<T, 64>(P, rows, s);
+        default: return launch_rows<T, 128>(P, rows, s);
+    }
+}
+
+}  // namespace
+
+AttnPlan plan_attention(const Cache& c, const Seqs& q, kvb_dtype dtype, int g, int num_sms) {
+    AttnPlan p{};
+    const int64_t most = static_cast<int64_t>(q.max_tokens) * g;  // rows of one sequence and head
+    p.rows = most <= 8 ? 8 : (most <= 16 ? 16 : 32);
+    p.row_blocks = static_cast<int>((most + p.rows - 1) / p.rows);
+    p.units = static_cast<int64_t>(c.n_layers) * q.n_seq * c.H * p.row_blocks;
+    // four CTAs fit an SM: cut the keys so that there are about four waves of them where
+    // there is that much work, into no fewer than 64 keys (one step of the four warps)
+    const double keys = static_cast<double>(q.max_kv) * static_cast<double>(p.units);
+    double chunk = keys / (num_sms * 16.0);
+    const double most_chunk = static_cast<double>(MAX_PAGES / 2) * c.page < 2048.0 ? MAX_PAGES / 2 * c.page : 2048.0;
+    if (chunk > most_chunk) chunk = most_chunk;
+    if (chunk < 64) chunk = 64;
+    p.chunk = (static_cast<int>(chunk) + 127) / 128 * 128;
+    if (chunk <= 64) p.chunk = 64;
+    p.splits = static_cast<int>((static_cast<int64_t>(q.max_kv) + p.chunk - 1) / p.chunk);
+    if (p.splits < 1) p.splits = 1;
+    p.counter_bytes = (static_cast<size_t>(p.units) * sizeof(int) + 255) / 256 * 256;
+    p.partial_bytes = p.splits > 1 ? static_cast<size_t>(p.units) * p.splits * p.rows * (c.d + 4) * sizeof(float) : 0;
+    return p;
+}
+
+cudaError_t launch_attention(const AttnArgs& a, const AttnPlan& p, cudaStream_t s) {
+    Params P{};
+    P.c = a.c;
+    P.q = a.q;
+    P.query = a.query;
+    P.out = a.out;
+    P.lse = a.lse;
+    P.g = a.g;
+    P.row_blocks = p.row_blocks;
+    P.chunk = p.chunk;
+    P.splits = p.splits;
+    P.scale_log2 = a.scale_log2;
+    P.counters = a.counters;
+    P.partial = a.partial;
+    P.part_stat = reinterpret_cast<float4*>(a.partial + static_cast<size_t>(p.units) * p.splits * p.rows * a.c.d);
+    P.err = a.err;
+    return a.dtype == KVB_BF16 ? launch_dim<__nv_bfloat16>(P, p.rows, s) : launch_dim<float>(P, p.rows, s);
+}
+
+}  // namespace c8
+}  // namespace kvb

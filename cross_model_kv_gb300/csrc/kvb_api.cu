@@ -76,6 +76,11 @@ kvb_status take_device_error(kvb_ctx* c) {
         return fail(KVB_ERR_TIMEOUT, "a bounded device wait gave up in an earlier kernel on this context");
     if (code == DEV_ERR_BOUNDS)
         return fail(KVB_ERR_CUDA, "an index check of the checked build failed in an earlier kernel on this context");
+    if (code == DEV_ERR_BAD_SEQ)
+        return fail(KVB_ERR_INVALID_ARG,
+                    "a sequence or page outside what its call described was seen by an earlier kernel on this context");
+    if (code == DEV_ERR_NONFINITE)
+        return fail(KVB_ERR_NUMERIC, "a value that is not finite was stored as 0 by an earlier kernel on this context");
     return fail(KVB_ERR_INVALID_ARG, "a position outside [0, max_pos) was seen by an earlier kernel on this context");
 }
 
@@ -99,18 +104,6 @@ kvb_status ensure_scratch(kvb_ctx* c, size_t bytes) {
     c->scratch_bytes = bytes;
     return KVB_OK;
 }
-
-struct DeviceGuard {
-    int prev = -1;
-    explicit DeviceGuard(int dev) {
-        if (cudaGetDevice(&prev) != cudaSuccess) prev = -1;
-        if (prev != dev) cudaSetDevice(dev);
-    }
-    ~DeviceGuard() {
-        int cur = -1;
-        if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
-    }
-};
 
 }  // namespace kvb
 
@@ -199,6 +192,7 @@ kvb_status kvb_ctx_destroy(kvb_ctx* c) {
     cudaFree(c->scratch);
     cudaFree(c->err_dev);
     cudaFree(c->strip_ctr);
+    cudaFree(c->attn_ws);
     if (c->err_mirror) cudaFreeHost(c->err_mirror);
     for (auto& r : c->prof) {
         cudaEventDestroy(r.start);

@@ -21,6 +21,9 @@ struct kvb_ctx {
     int* err_dev = nullptr;    // error word written by kernels
     int* strip_ctr = nullptr;  // [4]: next / finished chunk of the strip fused into the map kernel, next map tile
     int* err_mirror = nullptr; // pinned host copy, refreshed after each call
+    void* attn_ws = nullptr;   // 8-bit cache attention: arrival counters (kept at 0 between calls), then partials
+    size_t attn_ws_bytes = 0;
+    size_t attn_ws_counters = 0;  // how many counters the workspace starts with
     // kernel timing (kvb_profile_enable / kvb_profile_read)
     struct ProfRec {
         const char* name;
@@ -45,6 +48,19 @@ kvb_status check_selection(const kvb_ctx* c, const int32_t* sel, const char* nam
 kvb_status take_device_error(kvb_ctx* c);
 void mirror_device_error(kvb_ctx* c, cudaStream_t s);
 DevErr dev_err(const kvb_ctx* c);
+
+// Make `dev` current for the scope.
+struct DeviceGuard {
+    int prev = -1;
+    explicit DeviceGuard(int dev) {
+        if (cudaGetDevice(&prev) != cudaSuccess) prev = -1;
+        if (prev != dev) cudaSetDevice(dev);
+    }
+    ~DeviceGuard() {
+        int cur = -1;
+        if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
+    }
+};
 
 // Bracket one launch with events when profiling is on (no-op otherwise).
 struct ProfScope {

@@ -82,7 +82,14 @@ struct DevErr {
     uint64_t timeout_ns;  // limit of every spin-wait
 };
 
-enum : int { DEV_ERR_NONE = 0, DEV_ERR_BAD_POS = 1, DEV_ERR_TIMEOUT = 7, DEV_ERR_BOUNDS = 9 };
+enum : int {
+    DEV_ERR_NONE = 0,
+    DEV_ERR_BAD_POS = 1,
+    DEV_ERR_BAD_SEQ = 2,    // 8-bit cache: a sequence or page outside what the call described
+    DEV_ERR_NONFINITE = 5,  // 8-bit cache: a value to be stored was not finite
+    DEV_ERR_TIMEOUT = 7,
+    DEV_ERR_BOUNDS = 9
+};
 
 __device__ __forceinline__ void dev_err_set(const DevErr& e, int code) {
     if (e.word) atomicCAS(e.word, 0, code);

@@ -318,6 +318,99 @@ kvb_status kvb_attention_cosine(kvb_ctx* ctx, kvb_dtype dtype, const void* q, in
                                 const void* k_b, const void* v_b, const int32_t* kv_pos, int64_t T,
                                 float* cos_out, void* stream);
 
+/*
+ * Paged 8-bit cache of the target model: a mapped cache kept in half the bytes
+ * of bf16, grown by the tokens that the target decodes and attended over.
+ *
+ * Codes are e4m3 bytes in pages of page_tokens tokens; the (layer, page, head)
+ * block of page_tokens * d codes has one scale for K and one for V, a power of
+ * two 2^e with -117 <= e <= 119, and a code c stands for c * 2^e.  With such a
+ * scale x * 2^-e is exact before the one rounding to e4m3, a code re-rounded
+ * under a larger scale changes only if it becomes subnormal, and c * 2^e is
+ * exact in bf16.
+ *   k, v             device [L_tgt][n_pages][H][page_tokens][d] bytes, 16-byte aligned
+ *   k_scale, v_scale device float32 [L_tgt][n_pages][H]
+ * page_tokens is 16, 32, 64 or 128 and d (the context's) 16, 32, 64 or 128.
+ * The caller owns the four buffers; they need no initial value, since only
+ * slots that kvb_cache8_write has written are read.
+ */
+typedef struct {
+    int32_t page_tokens;
+    int64_t n_pages;
+    void* k;
+    void* v;
+    float* k_scale;
+    float* v_scale;
+} kvb_cache8;
+
+/*
+ * The sequences of a call, packed on its token axis of T tokens: sequence s
+ * owns tokens seq_off[s] .. seq_off[s+1]-1, the first of them at position
+ * seq_pos[s] of the sequence, and page_table[s][p] is the page of its positions
+ * p*page_tokens .. (p+1)*page_tokens-1.  All arrays are int32 on the device.
+ *   max_tokens  the most tokens that one sequence owns
+ *   kv_len      [n_seq], or NULL for seq_pos[s] + its tokens: cache positions
+ *               that kvb_cache8_attention may read (the other calls ignore it)
+ *   max_kv      the largest kv_len, or 0 for max_pages * page_tokens
+ * max_tokens and max_kv size the launches.  Sequences that run past max_tokens,
+ * T, max_kv or their row of the page table, and pages outside [0, n_pages), are
+ * found by the kernels: KVB_ERR_INVALID_ARG is recorded on the context, and
+ * what would have been read counts as absent.  One call writes to a page from
+ * one sequence only; any number of sequences may read it.
+ */
+typedef struct {
+    int32_t n_seq;
+    int32_t max_pages;
+    int32_t max_tokens;
+    int32_t max_kv;
+    const int32_t* page_table;
+    const int32_t* seq_off;
+    const int32_t* seq_pos;
+    const int32_t* kv_len;
+} kvb_seqs;
+
+/*
+ * Quantise tokens into layers [l_begin, l_begin + n_layers) of the cache.
+ *   k, v  device [n_layers][H][T][d] in dtype, keys with the target's RoPE
+ *         (the layout of kvb_map_apply's outputs); positions must be >= 0
+ * Per block: e_new is the smallest e with max|x| <= 448 * 2^e over the block's
+ * new values; a block whose first slot is written takes it (what the page held
+ * is forgotten), any other block takes max(e_old, e_new) and, where that is
+ * above e_old, its slots before the new tokens are rounded again under the new
+ * scale.  Rounding is to nearest even, saturating at 448 * 2^119.  A value that
+ * is not finite is stored as 0 and recorded as KVB_ERR_NUMERIC on the context.
+ */
+kvb_status kvb_cache8_write(kvb_ctx* ctx, const kvb_cache8* cache, const kvb_seqs* seqs, int32_t l_begin,
+                            int32_t n_layers, kvb_dtype dtype, const void* k, const void* v, int64_t T, void* stream);
+
+/*
+ * Read tokens back: k, v device [n_layers][H][T][d] in dtype, every token that
+ * a sequence owns written in full (0 where its page is bad).  Exact in both types.
+ */
+kvb_status kvb_cache8_read(kvb_ctx* ctx, const kvb_cache8* cache, const kvb_seqs* seqs, int32_t l_begin,
+                           int32_t n_layers, kvb_dtype dtype, void* k, void* v, int64_t T, void* stream);
+
+/*
+ * Attention of a call's tokens over the cache:
+ *     out_i = sum over visible j of softmax_j(scale * q_i . k_j) v_j,
+ *     lse_i = log sum over visible j of exp(scale * q_i . k_j),
+ * for token i of a sequence at position p = seq_pos[s] + i; position j is
+ * visible iff j <= p and j < kv_len[s].  Query head hq reads KV head
+ * hq / (n_q_heads / H).  A row that sees nothing is 0 with lse -infinity.
+ *   q, out  device [n_layers][n_q_heads][T][d] in dtype
+ *   lse     device float32 [n_layers][n_q_heads][T], or NULL
+ *   scale   > 0, or 0 for 1/sqrt(d)
+ * seq_pos may be negative here.  To attend over the call's own tokens too, write
+ * them first.  Scores, softmax and sums are fp32; queries enter the products
+ * exactly (bf16) or as an fp16 pair (fp32: 22 bits), probabilities as fp16
+ * (bf16) or an fp16 pair (fp32).  Workspace (partial outputs where keys are
+ * split) belongs to the context and grows on demand, which synchronises: make
+ * a call of the largest size before capturing a stream.
+ */
+kvb_status kvb_cache8_attention(kvb_ctx* ctx, const kvb_cache8* cache, const kvb_seqs* seqs, int32_t l_begin,
+                                int32_t n_layers, kvb_dtype dtype, const void* q, int32_t n_q_heads, int64_t T,
+                                double scale, void* out, float* lse, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
