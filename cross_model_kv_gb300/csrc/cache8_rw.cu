@@ -10,8 +10,8 @@ namespace c8 {
 
 namespace {
 
-constexpr int NT = 256;       // threads per CTA
-constexpr int MAX_CHUNKS = 8;  // 8-element chunks that one thread holds
+constexpr int NT = 256;    // threads per CTA (512 where a block needs them all)
+constexpr int CHUNKS = 4;  // 8-element chunks that one thread holds: 16 registers of bf16, 32 of fp32
 
 struct RwParams {
     Cache c;
@@ -41,27 +41,44 @@ __device__ __forceinline__ Item item_of(const RwParams& P, int64_t idx) {
     return it;
 }
 
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&o)[8]) {
-    const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p));
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// Eight elements as they lie in memory, and as fp32 with those that are not finite as 0.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<__nv_bfloat16> {
+    uint4 u;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = __ldcs(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void get(float (&o)[8]) const {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        o[2 * i] = __uint_as_float(w[i] << 16);
-        o[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        for (int i = 0; i < 4; ++i) {
+            o[2 * i] = __uint_as_float(w[i] << 16);
+            o[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
     }
-}
-__device__ __forceinline__ void load8(const float* p, float (&o)[8]) {
-    const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
-    const float4 b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-    o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w;
-    o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
-}
+};
+template <>
+struct Raw8<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p) {
+        a = __ldcs(reinterpret_cast<const float4*>(p));
+        b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+    }
+    __device__ __forceinline__ void get(float (&o)[8]) const {
+        o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w;
+        o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
+    }
+};
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) < __int_as_float(0x7f800000); }
 
-// One block per group of GS threads: its new values are held in registers
-// between the maximum and the rounding, so they are read once.
+// One block per group of GS threads: its new values stay in registers, as they
+// lay in memory, between the maximum and the rounding, so they are read once and
+// enough CTAs are resident to keep HBM busy (holding them as fp32, eight chunks
+// a thread, left two CTAs an SM and 3.1 TB/s).
 template <typename T, int GS>
-__global__ void __launch_bounds__(NT) write_kernel(const __grid_constant__ RwParams P) {
-    const int64_t idx = static_cast<int64_t>(blockIdx.x) * (NT / GS) + threadIdx.x / GS;
+__global__ void __launch_bounds__(GS > NT ? GS : NT) write_kernel(const __grid_constant__ RwParams P) {
+    constexpr int PER = GS > NT ? 1 : NT / GS;
+    const int64_t idx = static_cast<int64_t>(blockIdx.x) * PER + threadIdx.x / GS;
     const int t = threadIdx.x % GS;
     if (idx >= P.total) return;  // whole groups leave together, here and below
     const Item it = item_of(P, idx);
@@ -87,22 +104,21 @@ __global__ void __launch_bounds__(NT) write_kernel(const __grid_constant__ RwPar
     const T* src = static_cast<const T*>(P.src[it.kv]) + ((head * P.q.T + tok) << P.c.d_log2);
     const int n8 = (m << P.c.d_log2) >> 3;
 
-    float x[MAX_CHUNKS][8];
+    Raw8<T> raw[CHUNKS];
     float amax = 0.f;
     bool bad = false;
 #pragma unroll
-    for (int c = 0; c < MAX_CHUNKS; ++c)
-        if (c * GS + t < n8) load8(src + 8 * (c * GS + t), x[c]);
+    for (int c = 0; c < CHUNKS; ++c)
+        if (c * GS + t < n8) raw[c].load(src + 8 * (c * GS + t));
 #pragma unroll
-    for (int c = 0; c < MAX_CHUNKS; ++c)
+    for (int c = 0; c < CHUNKS; ++c)
         if (c * GS + t < n8) {
+            float x[8];
+            raw[c].get(x);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                if (!(fabsf(x[c][i]) < __int_as_float(0x7f800000))) {
-                    bad = true;
-                    x[c][i] = 0.f;
-                }
-                amax = fmaxf(amax, fabsf(x[c][i]));
+                bad |= !finite(x[i]);
+                amax = fmaxf(amax, finite(x[i]) ? fabsf(x[i]) : 0.f);
             }
         }
     if (bad) err_set(P.err, DEV_ERR_NONFINITE);
@@ -115,11 +131,12 @@ __global__ void __launch_bounds__(NT) write_kernel(const __grid_constant__ RwPar
     int e_old = E_MIN;
     if (lo > 0) e_old = min(max(exponent_of(*scale), E_MIN), E_MAX);
     if constexpr (GS > 32) {
-        __shared__ int tops[NT / 32];
-        if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
-        __syncthreads();  // also: every thread has read the old scale
+        __shared__ int tops[PER][GS / 32];
+        const int group = threadIdx.x / GS;
+        if ((t & 31) == 0) tops[group][t >> 5] = top;
+        named_bar_sync(1 + group, GS);  // also: every thread has read the old scale
 #pragma unroll
-        for (int w = 0; w < NT / 32; ++w) top = max(top, tops[w]);
+        for (int w = 0; w < GS / 32; ++w) top = max(top, tops[group][w]);
     } else {
         __syncwarp();
     }
@@ -127,11 +144,15 @@ __global__ void __launch_bounds__(NT) write_kernel(const __grid_constant__ RwPar
     if (t == 0) *scale = pow2(e);
     const float inv = pow2(-e);
 #pragma unroll
-    for (int c = 0; c < MAX_CHUNKS; ++c)
+    for (int c = 0; c < CHUNKS; ++c)
         if (c * GS + t < n8) {
+            float x[8];
+            raw[c].get(x);
             uint32_t w[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = e4m3x2(x[c][2 * i] * inv, x[c][2 * i + 1] * inv);
+            for (int i = 0; i < 8; ++i) x[i] = finite(x[i]) ? x[i] * inv : 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = e4m3x2(x[2 * i], x[2 * i + 1]);
             *reinterpret_cast<uint2*>(codes + (lo << P.c.d_log2) + 8 * (c * GS + t)) =
                 make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
         }
@@ -212,10 +233,13 @@ int items_of(const Cache& c, const Seqs& q) {
     return static_cast<int>((static_cast<int64_t>(q.max_tokens) + c.page - 2) / c.page + 1);
 }
 
-// A warp for each block where a block gets at most 2048 new values (a few
-// tokens: more blocks in flight), a CTA otherwise.
-bool small_blocks(const Cache& c, const Seqs& q) {
-    return static_cast<int64_t>(q.max_tokens < c.page ? q.max_tokens : c.page) * c.d <= 32 * 8 * MAX_CHUNKS;
+// Threads for a block: enough to hold the most new values that a block can get, four
+// chunks each, so that a few tokens take a warp a block and a whole page a CTA.
+int group_size(const Cache& c, const Seqs& q) {
+    const int values = (q.max_tokens < c.page ? q.max_tokens : c.page) * c.d;
+    int gs = 32;
+    while (gs * CHUNKS * 8 < values) gs *= 2;
+    return gs;  // at most 512: 128 tokens of 128
 }
 
 RwParams params(const Cache& c, const Seqs& q, const Err& err) {
@@ -228,6 +252,33 @@ RwParams params(const Cache& c, const Seqs& q, const Err& err) {
     return P;
 }
 
+template <typename T, int GS>
+cudaError_t launch_write_gs(const RwParams& P, cudaStream_t s) {
+    constexpr int PER = GS > NT ? 1 : NT / GS;
+    write_kernel<T, GS><<<static_cast<unsigned>((P.total + PER - 1) / PER), GS > NT ? GS : NT, 0, s>>>(P);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_write_t(const RwParams& P, int gs, cudaStream_t s) {
+    switch (gs) {
+        case 32: return launch_write_gs<T, 32>(P, s);
+        case 64: return launch_write_gs<T, 64>(P, s);
+        case 128: return launch_write_gs<T, 128>(P, s);
+        case 256: return launch_write_gs<T, 256>(P, s);
+        default: return launch_write_gs<T, 512>(P, s);
+    }
+}
+
+template <typename T>
+cudaError_t launch_read_t(const RwParams& P, int gs, cudaStream_t s) {
+    const int per = gs == 32 ? NT / 32 : 1;
+    const unsigned grid = static_cast<unsigned>((P.total + per - 1) / per);
+    if (gs == 32) read_kernel<T, 32><<<grid, NT, 0, s>>>(P);
+    else read_kernel<T, NT><<<grid, NT, 0, s>>>(P);
+    return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_write(const Cache& c, const Seqs& q, kvb_dtype dtype, const void* k, const void* v, const Err& err,
@@ -235,18 +286,8 @@ cudaError_t launch_write(const Cache& c, const Seqs& q, kvb_dtype dtype, const v
     RwParams P = params(c, q, err);
     P.src[0] = k;
     P.src[1] = v;
-    const bool small = small_blocks(c, q);
-    const int per = small ? NT / 32 : 1;
-    if (P.total > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    const unsigned grid = static_cast<unsigned>((P.total + per - 1) / per);
-    if (dtype == KVB_BF16) {
-        if (small) write_kernel<__nv_bfloat16, 32><<<grid, NT, 0, s>>>(P);
-        else write_kernel<__nv_bfloat16, NT><<<grid, NT, 0, s>>>(P);
-    } else {
-        if (small) write_kernel<float, 32><<<grid, NT, 0, s>>>(P);
-        else write_kernel<float, NT><<<grid, NT, 0, s>>>(P);
-    }
-    return cudaGetLastError();
+    return dtype == KVB_BF16 ? launch_write_t<__nv_bfloat16>(P, group_size(c, q), s)
+                             : launch_write_t<float>(P, group_size(c, q), s);
 }
 
 cudaError_t launch_read(const Cache& c, const Seqs& q, kvb_dtype dtype, void* k, void* v, const Err& err,
@@ -254,18 +295,8 @@ cudaError_t launch_read(const Cache& c, const Seqs& q, kvb_dtype dtype, void* k,
     RwParams P = params(c, q, err);
     P.dst[0] = k;
     P.dst[1] = v;
-    const bool small = small_blocks(c, q);
-    const int per = small ? NT / 32 : 1;
-    if (P.total > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    const unsigned grid = static_cast<unsigned>((P.total + per - 1) / per);
-    if (dtype == KVB_BF16) {
-        if (small) read_kernel<__nv_bfloat16, 32><<<grid, NT, 0, s>>>(P);
-        else read_kernel<__nv_bfloat16, NT><<<grid, NT, 0, s>>>(P);
-    } else {
-        if (small) read_kernel<float, 32><<<grid, NT, 0, s>>>(P);
-        else read_kernel<float, NT><<<grid, NT, 0, s>>>(P);
-    }
-    return cudaGetLastError();
+    return dtype == KVB_BF16 ? launch_read_t<__nv_bfloat16>(P, group_size(c, q), s)
+                             : launch_read_t<float>(P, group_size(c, q), s);
 }
 
 }  // namespace c8
