@@ -47,28 +47,31 @@ cudaError_t launch_write(const Cache& c, const Seqs& q, kvb_dtype dtype, const v
 cudaError_t launch_read(const Cache& c, const Seqs& q, kvb_dtype dtype, void* k, void* v, const Err& err,
                         cudaStream_t s);
 
-struct AttnArgs {
+struct AttnParams {
     Cache c;
     Seqs q;
-    kvb_dtype dtype;
     const void* query;  // [n_layers][Hq][T][d]
     void* out;
     float* lse;  // or null
     int g;       // query heads of a KV head
-    float scale_log2;  // scale * log2(e)
-    int* counters;     // [units], 0 before and after
-    float* partial;    // [units][splits][rows][d] outputs, then [units][splits][rows][4] references and sums
+    int row_blocks, chunk, splits;
+    float scale_log2;   // scale * log2(e)
+    int* counters;      // [units], 0 before and after a call
+    float* partial;     // [units][splits][rows][d] outputs in units of 2^mv
+    float4* part_stat;  // [units][splits][rows] (m, mv, sum, -)
     Err err;
 };
 
 // How a call is cut: blocks of `rows` query rows, keys in `splits` chunks of `chunk`.
 struct AttnPlan {
+    bool tensor;  // the tcgen05 kernel
     int rows, row_blocks, chunk, splits;
     int64_t units;  // (layer, sequence, head, row block)
     size_t counter_bytes, partial_bytes;
 };
 AttnPlan plan_attention(const Cache& c, const Seqs& q, kvb_dtype dtype, int g, int num_sms);
-cudaError_t launch_attention(const AttnArgs& a, const AttnPlan& p, cudaStream_t s);
+cudaError_t launch_decode(const AttnParams& P, kvb_dtype dtype, int rows, cudaStream_t s);
+cudaError_t launch_prefill(const AttnParams& P, cudaStream_t s);  // bf16, d 128, 256 rows a block
 
 #ifdef __CUDACC__
 

@@ -143,7 +143,7 @@ kvb_status kvb_cache8_attention(kvb_ctx* c, const kvb_cache8* cache, const kvb_s
                                 int32_t n_layers, kvb_dtype dtype, const void* q, int32_t n_q_heads, int64_t T,
                                 double scale, void* out, float* lse, void* stream) {
     g_last_error.clear();
-    c8::AttnArgs a{};
+    c8::AttnParams a{};
     kvb_status st = check_call(c, cache, seqs, l_begin, n_layers, dtype, T, "kvb_cache8_attention", &a.c, &a.q);
     if (st != KVB_OK) return st;
     if (n_q_heads < c->H || n_q_heads % c->H)
@@ -155,7 +155,6 @@ kvb_status kvb_cache8_attention(kvb_ctx* c, const kvb_cache8* cache, const kvb_s
         return fail(KVB_ERR_INVALID_ARG, "kvb_cache8_attention: lse not 4-byte aligned");
     DeviceGuard g(c->device);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    a.dtype = dtype;
     a.query = q;
     a.out = out;
     a.lse = lse;
@@ -168,8 +167,12 @@ kvb_status kvb_cache8_attention(kvb_ctx* c, const kvb_cache8* cache, const kvb_s
     if ((st = ensure_attn_ws(c, p, s)) != KVB_OK) return st;
     a.counters = static_cast<int*>(c->attn_ws);
     a.partial = reinterpret_cast<float*>(static_cast<char*>(c->attn_ws) + c->attn_ws_counters);
-    ProfScope ps(c, s, "cache8_attention");
-    const cudaError_t e = c8::launch_attention(a, p, s);
+    a.part_stat = reinterpret_cast<float4*>(a.partial + static_cast<size_t>(p.units) * p.splits * p.rows * c->d);
+    a.row_blocks = p.row_blocks;
+    a.chunk = p.chunk;
+    a.splits = p.splits;
+    ProfScope ps(c, s, p.tensor ? "cache8_attention_tcgen05" : "cache8_attention");
+    const cudaError_t e = p.tensor ? c8::launch_prefill(a, s) : c8::launch_decode(a, dtype, p.rows, s);
     return e == cudaSuccess ? KVB_OK : cuda_fail(e, "cache8 attention launch");
 }
 

@@ -28,7 +28,7 @@
 //
 // Keys are split into chunks over CTAs where there are few rows; the last CTA
 // of a unit to arrive joins the chunks in order, so results do not depend on timing.
-#include "cache8.h"
+#include "cache8_attn.cuh"
 
 namespace kvb {
 namespace c8 {
@@ -38,29 +38,6 @@ namespace {
 constexpr int NWARPS = 4;
 constexpr int NT = NWARPS * 32;
 constexpr int MAX_PAGES = 512;    // pages of one chunk, listed in shared memory
-constexpr float BIAS = 7.f;       // weights are taken against 2^-7 of the reference
-constexpr float MARGIN = 8.f;     // a reference is raised past this much
-constexpr float NO_REF = -3.0e38f;
-
-struct Params {
-    Cache c;
-    Seqs q;
-    const void* query;
-    void* out;
-    float* lse;
-    int g, row_blocks, chunk, splits;
-    float scale_log2;
-    int* counters;
-    float* partial;   // [unit][split][rows][d]
-    float4* part_stat;  // [unit][split][rows]: references and sum
-    Err err;
-};
-
-__device__ __forceinline__ float ex2(float x) {  // relative error about 2^-22
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -74,39 +51,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
-
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// Parts of one row's result, each with its references: first every part's
-// reference(), then every part's add().  st = (m, mv, sum, -).  A part that saw
-// nothing has NO_REF references and adds zeros; a NaN reaches the result.
-struct Joined {
-    float m = NO_REF, mv = NO_REF, sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    __device__ __forceinline__ void reference(const float4& st) {
-        m = fmaxf(m, st.x);
-        mv = fmaxf(mv, st.y);
-    }
-    __device__ __forceinline__ void add(const float4& st, const float4& o) {
-        const float f = ex2(st.y - mv);
-        sum = fmaf(ex2(st.x - m), st.z, sum);
-        acc.x = fmaf(f, o.x, acc.x);
-        acc.y = fmaf(f, o.y, acc.y);
-        acc.z = fmaf(f, o.z, acc.z);
-        acc.w = fmaf(f, o.w, acc.w);
-    }
-    // acc / sum * 2^(mv - m), the power in two halves: it may pass the range of one float
-    __device__ __forceinline__ float4 output() const {
-        const float half = ex2(0.5f * (mv - m)), f = sum == 0.f ? 0.f : half / sum;
-        return make_float4(acc.x * f * half, acc.y * f * half, acc.z * f * half, acc.w * f * half);
-    }
-    __device__ __forceinline__ float lse() const {
-        return sum == 0.f ? -INFINITY : (m - BIAS + log2f(sum)) * 0.693147180559945f;
-    }
-};
 
 // W consecutive 32-bit words (B bytes), read once: not kept in L1.
 template <int B>
@@ -136,11 +80,6 @@ __device__ __forceinline__ float2 load2(const __nv_bfloat16* p) {
     return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
 }
 __device__ __forceinline__ float2 load2(const float* p) { return __ldg(reinterpret_cast<const float2*>(p)); }
-__device__ __forceinline__ void store_out(__nv_bfloat16* p, float4 v) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-}
-__device__ __forceinline__ void store_out(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
-
 template <typename T, int D, int NB>
 struct Shape8 {
     static constexpr int PARTS = sizeof(T) == 4 ? 2 : 1;  // fp16 parts of a query element and of a weight
@@ -154,7 +93,7 @@ struct Shape8 {
 };
 
 template <typename T, int D, int NB>
-__global__ void __launch_bounds__(NT) decode_kernel(const __grid_constant__ Params P) {
+__global__ void __launch_bounds__(NT) decode_kernel(const __grid_constant__ AttnParams P) {
     using S8 = Shape8<T, D, NB>;
     constexpr int PARTS = S8::PARTS, ROWS = S8::ROWS, KS = S8::KS;
     constexpr int KB = D / 4, VB = D / 8;                    // bytes of a lane: of a key row, of a value row
@@ -178,24 +117,10 @@ __global__ void __launch_bounds__(NT) decode_kernel(const __grid_constant__ Para
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = lane >> 2, c = lane & 3;
 
-    const SeqView sv = seq_view(P.q, s, P.err);
-    const int64_t rows = static_cast<int64_t>(sv.n) * P.g;
-    const int64_t row0 = static_cast<int64_t>(rb) * ROWS;
-    if (row0 >= rows) return;
-    // row = token * g + head of the group: rows of a block are close in position
-    const int nrows = static_cast<int>(min(static_cast<int64_t>(ROWS), rows - row0));
-    int64_t kv = P.q.kv_len ? static_cast<int64_t>(__ldg(P.q.kv_len + s)) : static_cast<int64_t>(sv.pos) + sv.n;
-    const int64_t room = min(static_cast<int64_t>(P.q.max_kv), static_cast<int64_t>(P.q.max_pages) << P.c.page_log2);
-    if (kv > room) {
-        if (threadIdx.x == 0) err_set(P.err, DEV_ERR_BAD_SEQ);
-        kv = room;
-    }
-    const int64_t pos_hi = sv.pos + (row0 + nrows - 1) / P.g;  // position of the block's last row
-    const int pos_lo = sv.pos + static_cast<int>(row0 / P.g);
-    const int kv_end = static_cast<int>(max(static_cast<int64_t>(0), min(kv, pos_hi + 1)));
-    const int active = max(1, (kv_end + P.chunk - 1) / P.chunk);
-    if (split >= active) return;
-    const int k0 = split * P.chunk, k1 = min(kv_end, k0 + P.chunk);
+    RowBlock B;
+    if (!row_block(P, s, rb, ROWS, split, B)) return;
+    const int k0 = B.k0, k1 = B.k1, nrows = B.nrows;
+    const int64_t row0 = B.row0;
 
     // the chunk's pages and scales
     const int page0 = k0 >> P.c.page_log2;
@@ -223,7 +148,7 @@ __global__ void __launch_bounds__(NT) decode_kernel(const __grid_constant__ Para
         if (row < nrows) {
             const int64_t gr = row0 + row;
             const int64_t i = gr / P.g;
-            const T* p = query + ((hq0 + (gr - i * P.g)) * P.q.T + sv.tok0 + i) * D + c * KB;
+            const T* p = query + ((hq0 + (gr - i * P.g)) * P.q.T + B.tok0 + i) * D + c * KB;
 #pragma unroll
             for (int e = 0; e < KB; e += 2) {
                 const float2 x = load2(p + e);
@@ -263,7 +188,7 @@ __global__ void __launch_bounds__(NT) decode_kernel(const __grid_constant__ Para
         for (int j = 0; j < 2; ++j) {
             const int row = 8 * b + 2 * c + j;
             qs[b][j] = sqs[row];
-            qpos[b][j] = row < nrows ? sv.pos + static_cast<int>((row0 + row) / P.g) : INT32_MIN;
+            qpos[b][j] = row < nrows ? B.pos + static_cast<int>((row0 + row) / P.g) : INT32_MIN;
         }
     uint32_t qf[NB * PARTS == 1 ? KS : 1][2];  // in registers where one fragment set serves
     if constexpr (NB * PARTS == 1) {
@@ -348,7 +273,7 @@ __global__ void __launch_bounds__(NT) decode_kernel(const __grid_constant__ Para
         }
         if (jn < k1) load_k(jn);
         // scores in base 2, masked; keys r, r + 8 and query rows 2c, 2c + 1 of each row block
-        const bool whole = !bad && j + 16 <= k1 && j + 15 <= pos_lo;
+        const bool whole = !bad && j + 16 <= k1 && j + 15 <= B.pos_lo;
         bool raise = false;
 #pragma unroll
         for (int b = 0; b < NB; ++b)
@@ -444,10 +369,7 @@ __global__ void __launch_bounds__(NT) decode_kernel(const __grid_constant__ Para
     __syncthreads();
 
     T* out = static_cast<T*>(P.out);
-    auto row_of = [&](int row) {  // index of a row in [n_layers][Hq][T]
-        const int64_t gr = row0 + row, i = gr / P.g;
-        return (hq0 + (gr - i * P.g)) * P.q.T + sv.tok0 + i;
-    };
+    auto row_of = [&](int row) { return B.row_of(P, hq0, row); };
     const int64_t part0 = (unit * P.splits + split) * ROWS;
     for (int e = threadIdx.x; e < nrows * (D / 4); e += NT) {
         const int row = e / (D / 4), d4 = e % (D / 4);
@@ -457,7 +379,7 @@ __global__ void __launch_bounds__(NT) decode_kernel(const __grid_constant__ Para
 #pragma unroll
         for (int w = 0; w < NWARPS; ++w)
             z.add(stat[w * ROWS + row], reinterpret_cast<const float4*>(so + (w * ROWS + row) * D)[d4]);
-        if (active == 1) {
+        if (B.active == 1) {
             store_out(out + row_of(row) * D + 4 * d4, z.output());
             if (d4 == 0 && P.lse) P.lse[row_of(row)] = z.lse();
         } else {
@@ -465,35 +387,11 @@ __global__ void __launch_bounds__(NT) decode_kernel(const __grid_constant__ Para
             if (d4 == 0) P.part_stat[part0 + row] = make_float4(z.m, z.mv, z.sum, 0.f);
         }
     }
-    if (active == 1) return;
-
-    // the last chunk to arrive joins them, in order
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        const int n = atomicAdd(P.counters + unit, 1);
-        s_last = n == active - 1;
-        if (s_last) P.counters[unit] = 0;
-    }
-    __syncthreads();
-    if (!s_last) return;
-    __threadfence();
-    const int64_t u0 = unit * P.splits * ROWS;
-    for (int e = threadIdx.x; e < nrows * (D / 4); e += NT) {
-        const int row = e / (D / 4), d4 = e % (D / 4);
-        Joined z;
-        for (int i = 0; i < active; ++i) z.reference(__ldcg(P.part_stat + u0 + i * ROWS + row));
-#pragma unroll 4
-        for (int i = 0; i < active; ++i)
-            z.add(__ldcg(P.part_stat + u0 + i * ROWS + row),
-                  __ldcg(reinterpret_cast<const float4*>(P.partial + (u0 + i * ROWS + row) * D) + d4));
-        store_out(out + row_of(row) * D + 4 * d4, z.output());
-        if (d4 == 0 && P.lse) P.lse[row_of(row)] = z.lse();
-    }
+    if (B.active > 1) join_splits<T, D, ROWS, NT>(P, B, unit, hq0, &s_last);
 }
 
 template <typename T, int D, int NB>
-cudaError_t launch_decode(const Params& P, cudaStream_t s) {
+cudaError_t launch_shape(const AttnParams& P, cudaStream_t s) {
     constexpr size_t smem = Shape8<T, D, NB>::smem();
     cudaError_t e = cudaFuncSetAttribute(decode_kernel<T, D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(smem));
@@ -504,16 +402,16 @@ cudaError_t launch_decode(const Params& P, cudaStream_t s) {
 }
 
 template <typename T, int D>
-cudaError_t launch_rows(const Params& P, int rows, cudaStream_t s) {
+cudaError_t launch_rows(const AttnParams& P, int rows, cudaStream_t s) {
     switch (rows) {
-        case 8: return launch_decode<T, D, 1>(P, s);
-        case 16: return launch_decode<T, D, 2>(P, s);
-        default: return launch_decode<T, D, 4>(P, s);
+        case 8: return launch_shape<T, D, 1>(P, s);
+        case 16: return launch_shape<T, D, 2>(P, s);
+        default: return launch_shape<T, D, 4>(P, s);
     }
 }
 
 template <typename T>
-cudaError_t launch_dim(const Params& P, int rows, cudaStream_t s) {
+cudaError_t launch_dim(const AttnParams& P, int rows, cudaStream_t s) {
     switch (P.c.d) {
         case 16: return launch_rows<T, 16>(P, rows, s);
         case 32: return launch_rows<T, 32>(P, rows, s);
@@ -527,42 +425,43 @@ cudaError_t launch_dim(const Params& P, int rows, cudaStream_t s) {
 AttnPlan plan_attention(const Cache& c, const Seqs& q, kvb_dtype dtype, int g, int num_sms) {
     AttnPlan p{};
     const int64_t most = static_cast<int64_t>(q.max_tokens) * g;  // rows of one sequence and head
-    p.rows = most <= 8 ? 8 : (most <= 16 ? 16 : 32);
+    const double max_kv = q.max_kv > 0 ? q.max_kv : 1;
+    p.tensor = dtype == KVB_BF16 && c.d == 128 && most > 64;
+    p.rows = p.tensor ? 256 : most <= 8 ? 8 : most <= 16 ? 16 : 32;
     p.row_blocks = static_cast<int>((most + p.rows - 1) / p.rows);
     p.units = static_cast<int64_t>(c.n_layers) * q.n_seq * c.H * p.row_blocks;
-    // four CTAs fit an SM: cut the keys so that there are about four waves of them where
-    // there is that much work, into no fewer than 64 keys (one step of the four warps)
-    const double keys = static_cast<double>(q.max_kv) * static_cast<double>(p.units);
-    double chunk = keys / (num_sms * 16.0);
-    const double most_chunk = static_cast<double>(MAX_PAGES / 2) * c.page < 2048.0 ? MAX_PAGES / 2 * c.page : 2048.0;
-    if (chunk > most_chunk) chunk = most_chunk;
-    if (chunk < 64) chunk = 64;
-    p.chunk = (static_cast<int>(chunk) + 127) / 128 * 128;
-    if (chunk <= 64) p.chunk = 64;
-    p.splits = static_cast<int>((static_cast<int64_t>(q.max_kv) + p.chunk - 1) / p.chunk);
-    if (p.splits < 1) p.splits = 1;
+    if (p.tensor) {
+        // one CTA an SM: the number of chunks that fills the waves best, a CTA costing
+        // about six steps of 128 keys beside its keys (set-up, output)
+        const int64_t steps = (static_cast<int64_t>(max_kv) + 127) / 128;
+        double best = 0;
+        int64_t per = steps;
+        for (int64_t n = 1; n <= 16 && n <= steps; ++n) {
+            const int64_t k = (steps + n - 1) / n;
+            const double waves = static_cast<double>((p.units * n + num_sms - 1) / num_sms);
+            const double cost = waves * static_cast<double>(k + (n > 1 ? 8 : 6));
+            if (n == 1 || cost < best) {
+                best = cost;
+                per = k;
+            }
+        }
+        p.chunk = static_cast<int>(per * 128);
+    } else {
+        // four CTAs fit an SM: cut the keys so that there are about four waves of them where
+        // there is that much work, into no fewer than 64 keys (one step of the four warps)
+        const double most_chunk = MAX_PAGES / 2 * c.page < 2048 ? MAX_PAGES / 2 * c.page : 2048;
+        double chunk = max_kv * static_cast<double>(p.units) / (num_sms * 16.0);
+        if (chunk > most_chunk) chunk = most_chunk;
+        p.chunk = chunk <= 64 ? 64 : (static_cast<int>(chunk) + 127) / 128 * 128;
+    }
+    p.splits = static_cast<int>((static_cast<int64_t>(max_kv) + p.chunk - 1) / p.chunk);
     p.counter_bytes = (static_cast<size_t>(p.units) * sizeof(int) + 255) / 256 * 256;
     p.partial_bytes = p.splits > 1 ? static_cast<size_t>(p.units) * p.splits * p.rows * (c.d + 4) * sizeof(float) : 0;
     return p;
 }
 
-cudaError_t launch_attention(const AttnArgs& a, const AttnPlan& p, cudaStream_t s) {
-    Params P{};
-    P.c = a.c;
-    P.q = a.q;
-    P.query = a.query;
-    P.out = a.out;
-    P.lse = a.lse;
-    P.g = a.g;
-    P.row_blocks = p.row_blocks;
-    P.chunk = p.chunk;
-    P.splits = p.splits;
-    P.scale_log2 = a.scale_log2;
-    P.counters = a.counters;
-    P.partial = a.partial;
-    P.part_stat = reinterpret_cast<float4*>(a.partial + static_cast<size_t>(p.units) * p.splits * p.rows * a.c.d);
-    P.err = a.err;
-    return a.dtype == KVB_BF16 ? launch_dim<__nv_bfloat16>(P, p.rows, s) : launch_dim<float>(P, p.rows, s);
+cudaError_t launch_decode(const AttnParams& P, kvb_dtype dtype, int rows, cudaStream_t s) {
+    return dtype == KVB_BF16 ? launch_dim<__nv_bfloat16>(P, rows, s) : launch_dim<float>(P, rows, s);
 }
 
 }  // namespace c8

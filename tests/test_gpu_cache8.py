@@ -585,3 +585,81 @@ def test_refusals(kvb):
     with pytest.raises(ValueError):
         kvb.Seqs(P.dtab, i32([0, 1]).long(), i32([0]), max_tokens=1)
     kvb.kvb_ctx_check(P.ctx)
+
+
+# ------------------------------------------------------------------ many rows on the tensor cores
+
+@pytest.mark.parametrize("page,H,g,n,lens", [(64, 1, 8, [100, 33, 0], [1500, 40, 10]), (16, 2, 4, [257, 64, 1], [900, 64, 300]),
+                                             (128, 1, 16, [70, 20, 16], [700, 129, 16]), (32, 2, 1, [513, 128, 65], [513, 640, 65])])
+def test_prompt_over_a_cached_prefix(kvb, page, H, g, n, lens):
+    P = Pool(kvb, 1, H, 128, page, 3, max(lens), seed=page + g)
+    P.fill(lens)
+    q = torch.from_numpy(1.5 * P.rng.standard_normal((1, H * g, sum(n), 128))).to(BF).cuda()
+    pos = np.asarray(lens) - n
+    out, lse = attend(P, q, offsets(n), pos)
+    kvb.kvb_ctx_check(P.ctx)
+    check_attention(P, q, offsets(n), pos, out, lse)
+    o2, z2 = attend(P, q, offsets(n), pos)
+    assert torch.equal(out, o2) and torch.equal(lse, z2)
+
+
+def test_prompt_with_rising_maxima_and_rows_that_see_nothing(kvb):
+    P = Pool(kvb, 1, 1, 128, 32, 2, 1200)
+    P.lens = np.asarray([1200, 1200])
+    ramp = np.concatenate([np.linspace(0, 30, 800), np.linspace(30, -20, 400)])
+    k = 0.3 * P.rng.standard_normal((1, 1, 2400, 128))
+    k[0, 0, :, 0] += np.concatenate([ramp, ramp[::-1]])
+    P.write([0, 1200, 2400], [0, 0], BF, x=[k, P.rng.standard_normal((1, 1, 2400, 128))])
+    q = P.rng.standard_normal((1, 2, 160, 128))
+    q[..., 0] = np.linspace(-20, 20, 320).reshape(1, 2, 160)
+    q = torch.from_numpy(q).to(BF).cuda()
+    for pos, kv_len in (([1100, 1120], None), ([-30, 0], None), ([1100, 900], [1000, 0])):
+        out, lse = attend(P, q, [0, 80, 160], pos, kv_len=None if kv_len is None else i32(kv_len))
+        kvb.kvb_ctx_check(P.ctx)
+        check_attention(P, q, [0, 80, 160], np.asarray(pos), out, lse, kv_len=kv_len)
+
+
+def test_prompt_with_page_scales_far_apart(kvb):
+    # as test_page_scales_far_apart, on the tensor-core kernel: 160 rows of head_dim 128
+    d, page, kv, n = 128, 16, 288, 80
+    P = Pool(kvb, 1, 1, d, page, 1, kv)
+    blocks = P.rng.permutation(np.repeat([0, 90, -90, 5, 60, -60, 1, -1, 3], 2))
+    v = P.rng.standard_normal((1, 1, kv, d)) * 2.0 ** np.repeat(blocks, page)[None, None, :, None]
+    k = 0.02 * P.rng.standard_normal((1, 1, kv, d))
+    k[0, 0, :, 0] += -4.0 * np.repeat(blocks, page) / 8
+    P.write([0, kv], [0], F32, x=[k, v])
+    q = P.rng.standard_normal((1, 2, n, d))
+    q[..., 0] = np.linspace(-12, 12, 2 * n).reshape(1, 2, n)
+    q = torch.from_numpy(q).to(BF).cuda()
+    out, lse = attend(P, q, [0, n], [kv - n])
+    kvb.kvb_ctx_check(P.ctx)
+    o, z, A, B = P.ref.attention(to_host64(q), P.table, [0, n], [kv - n])
+    ds = (d / 16 + 4) * 2.0 ** -23 * B[..., None]
+    tol = A * (2 * (ds + 2.0 ** -21) + 40 * 2.0 ** -23 + 2.0 ** -11 + kv * 2.0 ** -31) + np.abs(o) * 2.0 ** -8
+    assert (np.abs(to_host64(out) - o) <= tol).all()
+    assert (np.abs(to_host64(lse) - z) <= ds[..., 0] + 2.0 ** -18 + 2.0 ** -22 * np.abs(z)).all()
+
+
+def test_prompt_over_bad_pages_reports_and_sees_the_others(kvb):
+    P = Pool(kvb, 1, 2, 128, 64, 2, 500)
+    P.fill([500, 500])
+    q = torch.from_numpy(P.rng.standard_normal((1, 8, 60, 128))).to(BF).cuda()
+    good, _ = attend(P, q, [0, 30, 60], [470, 470])
+    kvb.kvb_ctx_check(P.ctx)
+    bad = P.dtab.clone()
+    bad[1, 2] = P.cache.n_pages + 5
+    bad[1, 5] = -7
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:3], device="cuda")
+    s = kvb.Seqs(bad, i32([0, 30, 60]), i32([470, 470]), max_tokens=30)
+    kvb.kvb_cache8_attention(P.ctx, P.cache, s, q, out, lse)
+    assert status_of(kvb, lambda: kvb.kvb_ctx_check(P.ctx)) == INVALID_ARG
+    assert torch.equal(out[:, :, :30], good[:, :, :30])
+    # the same pages as if their keys were not there: a sequence without those positions
+    keep = [p for p in range(8) if p not in (2, 5)]
+    few = i32(np.stack([P.table[1][keep]]))
+    o2, z2 = torch.empty_like(q[:, :, 30:].contiguous()), torch.empty((1, 8, 30), device="cuda")
+    s2 = kvb.Seqs(few, i32([0, 30]), i32([470 - 128]), max_tokens=30)
+    kvb.kvb_cache8_attention(P.ctx, P.cache, s2, q[:, :, 30:].contiguous(), o2, z2)
+    kvb.kvb_ctx_check(P.ctx)
+    assert torch.allclose(out[:, :, 30:].float(), o2.float(), rtol=2.0 ** -7, atol=2.0 ** -9)
+    assert torch.allclose(lse[:, :, 30:], z2, rtol=0, atol=2.0 ** -16)
