@@ -93,17 +93,22 @@ struct Joined {
 };
 
 // After a chunk's partial results are written: the last CTA of the unit to
-// arrive joins the chunks, in order.  Called by all NTHREADS threads.
-template <typename T, int D, int ROWS, int NTHREADS>
+// arrive joins the chunks, in order.  Called by the CTA's first NTHREADS threads
+// (SOME: there are others, so they meet at named barrier 1).
+template <typename T, int D, int ROWS, int NTHREADS, bool SOME = false>
 __device__ __forceinline__ void join_splits(const AttnParams& P, const RowBlock& B, int64_t unit, int64_t hq0, int* s_last) {
+    auto meet = [] {
+        if constexpr (SOME) named_bar_sync(1, NTHREADS);
+        else __syncthreads();
+    };
     __threadfence();
-    __syncthreads();
+    meet();
     if (threadIdx.x == 0) {
         const int n = atomicAdd(P.counters + unit, 1);
         *s_last = n == B.active - 1;
         if (n == B.active - 1) P.counters[unit] = 0;
     }
-    __syncthreads();
+    meet();
     if (!*s_last) return;
     __threadfence();
     const int64_t u0 = unit * P.splits * ROWS;

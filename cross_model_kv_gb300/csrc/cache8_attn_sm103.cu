@@ -5,22 +5,26 @@
 // product of the rows (tokens x query heads of a KV head) with the keys is large
 // enough to be bound by the tensor cores.  One CTA takes 256 rows as two tiles
 // of 128 and walks the keys 128 at a time:
-//   warps 8..11   read the codes (prefetched into registers a tile ahead),
+//   warps 8..15   read the codes (prefetched into registers a tile ahead),
 //                 convert them to fp16 (exact) and lay them out as operands, keys
 //                 and values alike: 128-byte swizzle, key rows, K-major for S and
 //                 MN-major for O; also the scales of the tile's 16-key groups;
-//   warp 12       one thread issues S_x = Q_x K^T (SS) and O_x += P_x V (P from TMEM)
-//                 for the tiles x = 0, 1 in turn, so that one tile's softmax runs
-//                 under the other's products;
-//   warps 0..3, 4..7  softmax of tile 0, 1, a row a thread: S from TMEM twice (the
-//                 maximum, then the weights), P as fp16 over the S just read, the
-//                 sum in fp32; O is rescaled in TMEM on the rare raise.
-// TMEM: S_x at 128 x, O_x at 256 + 128 x.  P_x lies in S_x's columns, so S_x of
-// the next tile is issued when O_x += P_x V has completed.
+//   warps 16, 17  one thread each issues S_x = Q_x K^T (SS) and O_x += P_x V (P from
+//                 TMEM) for tile x: one tile's softmax and waits run under the
+//                 other's products;
+//   warps 0..3, 4..7  softmax of tile 0, 1, a row a thread, 64 keys a step: scores
+//                 from TMEM to registers, P as fp16 over them, the sum in fp32; O is
+//                 rescaled in TMEM on the rare raise.
+// TMEM: score buffer b of tile x at 128 x + 64 b, O_x at 256 + 128 x.  P takes its
+// scores' columns, so a buffer's next scores are issued when O_x += P V has
+// completed; meanwhile the softmax works on the other buffer (one buffer of 128
+// keys left it waiting 2500 of 5800 cycles for each 128 keys).
 // The weights carry the value scale, w = 2^(s + e_v - mv); a 16-key group's sum goes
 // into the denominator with the factor 2^(mv - m - e_v), or is taken from
 // exponentials of its own where that factor could leave fp32's range.
 // Every wait is bounded.
+#include <cfloat>
+
 #include "cache8_attn.cuh"
 
 namespace kvb {
@@ -29,11 +33,16 @@ namespace c8 {
 namespace {
 
 constexpr int TR = 128;  // rows of a tile
-constexpr int TK = 128;  // keys of a step
+constexpr int TK = 128;  // keys of an operand tile
+constexpr int SK = 64;   // keys of a step (two score buffers a tile in TMEM)
 constexpr int HD = 128;
 constexpr int ATOM = 128 * 128;  // bytes of 128 rows x 64 fp16
 constexpr int TILE = 2 * ATOM;
-constexpr int NUM_THREADS = 416;
+constexpr int NUM_THREADS = 640;
+constexpr int CONV = 256;  // threads that convert
+// Registers a thread: 96 at launch, then by role.  256 * 144 + 256 * 72 + 128 * 40 = 60416 of
+// the launch's 640 * 96 = 61440.
+constexpr int REGS_SOFTMAX = 144, REGS_CONVERT = 72, REGS_MMA = 40;
 constexpr int INFO_RING = 4;  // scales are written at most three tiles before the slowest softmax reads them
 constexpr int SMEM_BYTES = 6 * TILE + 1024 + 1024;
 constexpr uint64_t DRAIN_NS = 200ull * 1000 * 1000;
@@ -41,12 +50,12 @@ constexpr uint64_t DRAIN_NS = 200ull * 1000 * 1000;
 __device__ __forceinline__ uint32_t sw_off(int r, int c) {  // 16-byte chunk c (0..15) of row r
     return static_cast<uint32_t>((c >> 3) * ATOM + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
-__device__ __forceinline__ uint64_t desc_k(const uint8_t* tile, int kk) {
-    return sdesc_k_sw128(smem_u32(tile) + (kk >> 2) * ATOM + (kk & 3) * 32);
-}
-__device__ __forceinline__ uint64_t desc_v(const uint8_t* tile, int kk) {
-    return sdesc_mn_sw128(smem_u32(tile) + kk * 16 * 128, ATOM);
-}
+// Operand descriptors of a tile (step 0) and the distance to step kk, in the
+// descriptor's 16-byte units: the issuing thread adds a constant for each product.
+__device__ __forceinline__ uint64_t desc_k(const uint8_t* tile) { return sdesc_k_sw128(smem_u32(tile)); }
+__device__ __forceinline__ uint64_t desc_v(const uint8_t* tile) { return sdesc_mn_sw128(smem_u32(tile), ATOM); }
+constexpr uint32_t step_k(int kk) { return ((kk >> 2) * ATOM + (kk & 3) * 32) >> 4; }
+constexpr uint32_t step_v(int kk) { return (kk * 16 * 128) >> 4; }
 constexpr uint32_t idesc_f16_f32(uint32_t M, uint32_t N) {
     return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
@@ -59,6 +68,62 @@ __device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void regs_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// 32 lanes x 32 bits, 32 consecutive columns per thread (no wait).
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,"
+        "%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, w;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+// 16 bytes, or zeros where !pred: a predicated load, so that a thread's loads are
+// all in flight together (behind branches they went one by one: 940 us, not 590, at
+// 1024 tokens over 16K with the conversion left out).
+__device__ __forceinline__ uint4 load16_if(const void* p, bool pred) {
+    uint4 v;
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+        "mov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
+        "@q ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+        : "l"(p), "r"(static_cast<uint32_t>(pred)));
+    return v;
 }
 
 struct TileInfo {
@@ -76,16 +141,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
     uint64_t* k_empty = bar + 2;   // [2]
     uint64_t* v_full = bar + 4;    // [2]
     uint64_t* v_empty = bar + 6;   // [2]
-    uint64_t* s_full = bar + 8;    // [2] tile x
-    uint64_t* p_full = bar + 10;   // [2]
-    uint64_t* pv_done = bar + 12;  // [2]
-    uint64_t* q_full = bar + 14;
-    uint64_t* drain = bar + 15;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 16);
+    uint64_t* s_full = bar + 8;    // [tile x][buffer]
+    uint64_t* p_full = bar + 12;   // [tile x][buffer]
+    uint64_t* pv_done = bar + 16;  // [tile x]
+    uint64_t* drain = bar + 18;    // [tile x]
+    uint64_t* q_full = bar + 20;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 21);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int* s_last = reinterpret_cast<int*>(tmem_slot + 2);
-    uint64_t* info_full = bar + 18;  // [INFO_RING]
-    TileInfo* info = reinterpret_cast<TileInfo*>(bar + 18 + INFO_RING);
+    uint64_t* info_full = bar + 24;  // [INFO_RING]
+    TileInfo* info = reinterpret_cast<TileInfo*>(bar + 24 + INFO_RING);
 
     const int split = blockIdx.x;
     const int64_t unit = blockIdx.y + static_cast<int64_t>(blockIdx.z) * gridDim.y;
@@ -97,28 +162,30 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
 
     RowBlock B;
     if (!row_block(P, s, rb, 2 * TR, split, B)) return;
-    const int ntiles = (B.k1 - B.k0 + TK - 1) / TK;
+    const int ntiles = (B.k1 - B.k0 + TK - 1) / TK, nsteps = (B.k1 - B.k0 + SK - 1) / SK;
     const int64_t layer = static_cast<int64_t>(P.c.l_begin) + l;
     const int64_t hq0 = (static_cast<int64_t>(l) * P.c.H + h) * P.g;
     const DevErr derr{P.err.word, P.err.timeout_ns};
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&k_full[i], 128);
-            mbar_init(&k_empty[i], 1);
-            mbar_init(&v_full[i], 128);
-            mbar_init(&v_empty[i], 1);
-            mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 128);
+            mbar_init(&k_full[i], CONV);
+            mbar_init(&k_empty[i], 2);
+            mbar_init(&v_full[i], CONV);
+            mbar_init(&v_empty[i], 2);
+            mbar_init(&s_full[2 * i], 1);
+            mbar_init(&s_full[2 * i + 1], 1);
+            mbar_init(&p_full[2 * i], 128);
+            mbar_init(&p_full[2 * i + 1], 128);
             mbar_init(&pv_done[i], 1);
+            mbar_init(&drain[i], 1);
         }
         for (int i = 0; i < INFO_RING; ++i) mbar_init(&info_full[i], 8);
         mbar_init(q_full, 256);
-        mbar_init(drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == 12) {
+    if (warp == 16) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
@@ -144,6 +211,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
     const uint32_t tS = tl + 128u * x, tO = tl + 256u + 128u * x;
 
     if (warp < 8) {
+        regs_up<REGS_SOFTMAX>();
         // the row as fp16 under a power of two: largest element in [2^13, 2^14)
         float qs;
         {
@@ -174,48 +242,46 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
             fence_proxy_async_smem();
             mbar_arrive(q_full);
         }
-        const int qpos = valid ? B.pos + static_cast<int>(tok) : INT32_MIN;
-        for (int t = 0; t < ntiles; ++t) {
-            ok = wait_all(&info_full[t & (INFO_RING - 1)], (t / INFO_RING) & 1) && wait_all(&s_full[x], t & 1);
+        // keys below `see` are visible to this row
+        const int see = valid ? min(B.k1, B.pos + static_cast<int>(tok) + 1) : 0;
+        for (int u = 0; u < nsteps; ++u) {
+            const int t = u >> 1, hf = u & 1;
+            if (hf == 0) ok = wait_all(&info_full[t & (INFO_RING - 1)], (t / INFO_RING) & 1);
+            ok = ok && wait_all(&s_full[2 * x + hf], t & 1);
             if (!ok) break;
             tc_fence_after();
+            const uint32_t cS = tS + SK * hf;
+            uint32_t sv[SK];
+            tmem_ld32(cS, sv);
+            tmem_ld32(cS + 32, sv + 32);
             const TileInfo& I = info[t & (INFO_RING - 1)];
-            // visible keys of this row are a prefix of the tile
-            const int j0 = B.k0 + t * TK;
-            const int nvis = static_cast<int>(min(static_cast<int64_t>(min(B.k1, qpos == INT32_MAX ? B.k1 : qpos + 1)) - j0,
-                                                  static_cast<int64_t>(TK)));
-            bool whole = nvis == TK;
+            const float4 ks4 = *reinterpret_cast<const float4*>(I.ks + 4 * hf), ev4 = *reinterpret_cast<const float4*>(I.ev + 4 * hf);
+            const float ev[4] = {ev4.x, ev4.y, ev4.z, ev4.w};
+            const float k[4] = {fmaxf(ks4.x * qs, FLT_MIN), fmaxf(ks4.y * qs, FLT_MIN), fmaxf(ks4.z * qs, FLT_MIN),
+                                fmaxf(ks4.w * qs, FLT_MIN)};
+            // visible keys of this row are a prefix of the step's
+            const int nvis = min(see - (B.k0 + u * SK), SK);
+            const bool whole = nvis == SK && ks4.x != 0.f && ks4.y != 0.f && ks4.z != 0.f && ks4.w != 0.f;
+            tmem_ld_wait();
+            if (!__all_sync(0xffffffffu, whole)) {
+                const float seen[4] = {ks4.x, ks4.y, ks4.z, ks4.w};
 #pragma unroll
-            for (int gq = 0; gq < 8; ++gq) whole &= I.ks[gq] != 0.f;
-            whole = __all_sync(0xffffffffu, whole);
-            // pass 1: the maxima of s and of s + e_v
-            float ms = -INFINITY, mvs = -INFINITY;
-#pragma unroll 1
-            for (int c0 = 0; c0 < TK; c0 += 32) {
-                uint32_t sv[2][16];
-                tmem_ld16(tS + c0, sv[0]);
-                tmem_ld16(tS + c0 + 16, sv[1]);
-                tmem_ld_wait();
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const int gq = (c0 >> 4) + c;
-                    float top = -INFINITY;
-                    if (whole) {
-#pragma unroll
-                        for (int u = 0; u < 16; ++u) top = fmaxf(top, __uint_as_float(sv[c][u]));
-                    } else {
-#pragma unroll
-                        for (int u = 0; u < 16; ++u)
-                            if (16 * gq + u < nvis && I.ks[gq] != 0.f) top = fmaxf(top, __uint_as_float(sv[c][u]));
-                    }
-                    if (top > -INFINITY) {
-                        top *= I.ks[gq] * qs;
-                        ms = fmaxf(ms, top);
-                        mvs = fmaxf(mvs, top + I.ev[gq]);
-                    }
-                }
+                for (int j = 0; j < SK; ++j)
+                    if (j >= nvis || seen[j >> 4] == 0.f) sv[j] = 0xff800000u;  // -inf
             }
-            __syncwarp();
+            // maxima of s and of s + e_v (factors are positive)
+            float ms = -INFINITY, mvs = -INFINITY;
+#pragma unroll
+            for (int gq = 0; gq < 4; ++gq) {
+                float top[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    top[j] = fmaxf(fmaxf(__uint_as_float(sv[16 * gq + 4 * j]), __uint_as_float(sv[16 * gq + 4 * j + 1])),
+                                   fmaxf(__uint_as_float(sv[16 * gq + 4 * j + 2]), __uint_as_float(sv[16 * gq + 4 * j + 3])));
+                const float best = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * k[gq];
+                ms = fmaxf(ms, best);
+                mvs = fmaxf(mvs, best + ev[gq]);
+            }
             const bool raise = ms > m + MARGIN || mvs > mv + MARGIN;
             if (__any_sync(0xffffffffu, raise)) {
                 float f = 1.f;
@@ -226,179 +292,64 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
                     m = mn;
                     mv = mvn;
                 }
-                if (t > 0) {
+                __syncwarp();
+                if (u > 0) {
+                    ok = wait_all(&pv_done[x], (u - 1) & 1);  // O is complete up to the step before
+                    if (!ok) break;
+                    tc_fence_after();
 #pragma unroll 1
                     for (int c0 = 0; c0 < HD; c0 += 16) {
                         uint32_t o[16];
                         tmem_ld16(tO + c0, o);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * f);
+                        for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
                         tmem_st16(tO + c0, o);
                     }
                     tmem_st_wait();
                 }
             }
-            // pass 2: the weights, over the scores just read
-#pragma unroll 1
-            for (int c0 = 0; c0 < TK; c0 += 32) {
-                uint32_t sv[2][16];
-                tmem_ld16(tS + c0, sv[0]);
-                tmem_ld16(tS + c0 + 16, sv[1]);
-                tmem_ld_wait();
+            // the weights; P takes the columns of the scores
+            float factor = 0.f;
+#pragma unroll
+            for (int g2 = 0; g2 < 2; ++g2) {
                 uint32_t pw[16];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const int gq = (c0 >> 4) + c;
-                    const float k = I.ks[gq] * qs, ev = I.ev[gq], b = ev - mv + BIAS;
-                    float w[16];
-                    if (whole) {
+                    const int gq = 2 * g2 + c;
+                    const float b = ev[gq] - mv + BIAS, e = mv - m - ev[gq];
+                    float2 w[8];
 #pragma unroll
-                        for (int u = 0; u < 16; ++u) w[u] = ex2(fmaf(__uint_as_float(sv[c][u]), k, b));
-                    } else {
-#pragma unroll
-                        for (int u = 0; u < 16; ++u)
-                            w[u] = 16 * gq + u < nvis && k != 0.f ? ex2(fmaf(__uint_as_float(sv[c][u]), k, b)) : 0.f;
+                    for (int j = 0; j < 8; ++j) {
+                        const float2 a = make_float2(__uint_as_float(sv[16 * gq + 2 * j]), __uint_as_float(sv[16 * gq + 2 * j + 1]));
+                        w[j] = fma2(a, make_float2(k[gq], k[gq]), make_float2(b, b));
+                        w[j] = make_float2(ex2(w[j].x), ex2(w[j].y));
+                        pw[8 * c + j] = pack_half2(w[j].x, w[j].y);
                     }
-                    float p = 0.f;
-                    const float e = mv - m - ev;
-                    if (fabsf(e) < 60.f) {
+                    if (gq == 0 || ev[gq] != ev[gq - 1]) factor = ex2(e);
+                    float2 p = add2(add2(add2(w[0], w[1]), add2(w[2], w[3])), add2(add2(w[4], w[5]), add2(w[6], w[7])));
+                    float p1 = (p.x + p.y) * factor;
+                    if (fabsf(e) > 60.f) {
+                        p1 = 0.f;
 #pragma unroll
-                        for (int u = 0; u < 16; ++u) p += w[u];
-                        p *= ex2(e);
-                    } else {
-#pragma unroll
-                        for (int u = 0; u < 16; ++u)
-                            if (16 * gq + u < nvis && k != 0.f) p += ex2(fmaf(__uint_as_float(sv[c][u]), k, BIAS - m));
+                        for (int j = 0; j < 16; ++j)
+                            p1 += ex2(fmaf(__uint_as_float(sv[16 * gq + j]), k[gq], BIAS - m));
                     }
-                    sum += p;
-#pragma unroll
-                    for (int u = 0; u < 8; ++u) pw[8 * c + u] = pack_half2(w[2 * u], w[2 * u + 1]);
+                    sum += p1;
                 }
-                __syncwarp();  // the warp-wide store, after branches that lanes take apart
-                tmem_st16(tS + (c0 >> 1), pw);
+                __syncwarp();  // the warp-wide store, after branches that lanes may take apart
+                tmem_st16(cS + 16 * g2, pw);
             }
             tmem_st_wait();
             tc_fence_before();
-            mbar_arrive(&p_full[x]);
+            mbar_arrive(&p_full[2 * x + hf]);
         }
-        ok = ok && (ntiles == 0 || wait_all(&pv_done[x], (ntiles - 1) & 1));
-    } else if (warp < 12) {
-        // ------------------------------------------------------- codes -> fp16 operands
-        const int tid = threadIdx.x - 256;
-        const int r8 = tid >> 3, c16 = tid & 7;  // row within a 16-key group, 16-code column
-        const int* table = P.q.page_table + static_cast<int64_t>(s) * P.q.max_pages;
-        const int pm = P.c.page - 1;
-        uint4 kr[8], vr[8];
-        auto load = [&](int kv, int t, uint4 (&u)[8]) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int j = B.k0 + t * TK + 16 * i;
-                u[i] = make_uint4(0, 0, 0, 0);
-                if (j + r8 < B.k1) {  // slots past the last visible key may hold anything
-                    const int pid = __ldg(table + (j >> P.c.page_log2));
-                    if (pid >= 0 && pid < P.c.n_pages) {
-                        const int64_t blk = (layer * P.c.n_pages + pid) * P.c.H + h;
-                        u[i] = __ldg(reinterpret_cast<const uint4*>(P.c.code[kv] + ((blk << P.c.page_log2) + (j & pm) + r8) * HD) + c16);
-                    }
-                }
-            }
-        };
-        auto store = [&](uint8_t* tile, const uint4 (&u)[8]) {
-            // codes 16 c16 .. +15 are chunks 2 c16 and 2 c16 + 1; lanes of the upper 64 dims
-            // store theirs in the other order, so that eight lanes hit eight bank groups
-            const int flip = c16 >> 2;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint4 a = make_uint4(half2_of_lo(u[i].x), half2_of_hi(u[i].x), half2_of_lo(u[i].y), half2_of_hi(u[i].y));
-                const uint4 b = make_uint4(half2_of_lo(u[i].z), half2_of_hi(u[i].z), half2_of_lo(u[i].w), half2_of_hi(u[i].w));
-                *reinterpret_cast<uint4*>(tile + sw_off(16 * i + r8, 2 * c16 + flip)) = flip ? b : a;
-                *reinterpret_cast<uint4*>(tile + sw_off(16 * i + r8, 2 * c16 + 1 - flip)) = flip ? a : b;
-            }
-        };
-        if (ntiles > 0) {
-            load(0, 0, kr);
-            load(1, 0, vr);
-        }
-        for (int t = 0; t < ntiles; ++t) {
-            const int b = t & 1;
-            float ks = 0.f, ev = 0.f;
-            if (tid < 8) {
-                const int j = B.k0 + t * TK + 16 * tid;
-                if (j < B.k1) {
-                    const int pid = __ldg(table + (j >> P.c.page_log2));
-                    if (pid >= 0 && pid < P.c.n_pages) {
-                        const int64_t blk = (layer * P.c.n_pages + pid) * P.c.H + h;
-                        ks = __ldg(P.c.scale[0] + blk);
-                        ev = static_cast<float>(exponent_of(__ldg(P.c.scale[1] + blk)));
-                    } else {
-                        err_set(P.err, DEV_ERR_BAD_SEQ);
-                    }
-                }
-            }
-            if (!mbar_wait(&k_empty[b], ((t >> 1) & 1) ^ 1, derr, abort_flag)) break;
-            if (tid < 8) {
-                TileInfo& I = info[t & (INFO_RING - 1)];
-                I.ks[tid] = ks;
-                I.ev[tid] = ev;
-                mbar_arrive(&info_full[t & (INFO_RING - 1)]);
-            }
-            store(sK + b * TILE, kr);
-            fence_proxy_async_smem();
-            mbar_arrive(&k_full[b]);
-            if (t + 1 < ntiles) load(0, t + 1, kr);
-            if (!mbar_wait(&v_empty[b], ((t >> 1) & 1) ^ 1, derr, abort_flag)) break;
-            store(sV + b * TILE, vr);
-            fence_proxy_async_smem();
-            mbar_arrive(&v_full[b]);
-            if (t + 1 < ntiles) load(1, t + 1, vr);
-        }
-    } else if (lane == 0 && ntiles > 0) {
-        // ------------------------------------------------------- MMA issuer
-        constexpr uint32_t idesc_s = idesc_f16_f32(TR, TK);
-        constexpr uint32_t idesc_o = idesc_f16_f32(TR, HD) | IDESC_B_MN;
-        auto scores = [&](int xx, int b) {
-#pragma unroll
-            for (int kk = 0; kk < HD / 16; ++kk)
-                umma_bf16(tmem_base + 128u * xx, desc_k(sQ + xx * TILE, kk), desc_k(sK + b * TILE, kk), idesc_s, kk != 0);
-            umma_commit(&s_full[xx]);
-        };
-        bool go = mbar_wait(q_full, 0, derr, abort_flag) && mbar_wait(&k_full[0], 0, derr, abort_flag);
-        if (go) {
-            tc_fence_after();
-            scores(0, 0);
-            scores(1, 0);
-            umma_commit(&k_empty[0]);
-        }
-        for (int t = 0; go && t < ntiles; ++t) {
-            const int b = t & 1, nb = (t + 1) & 1;
-            go = mbar_wait(&v_full[b], (t >> 1) & 1, derr, abort_flag);
-            if (go && t + 1 < ntiles) go = mbar_wait(&k_full[nb], ((t + 1) >> 1) & 1, derr, abort_flag);
-            for (int xx = 0; go && xx < 2; ++xx) {
-                go = mbar_wait(&p_full[xx], t & 1, derr, abort_flag);
-                if (!go) break;
-                tc_fence_after();
-#pragma unroll
-                for (int kk = 0; kk < TK / 16; ++kk)
-                    umma_f16_ts(tmem_base + 256u + 128u * xx, tmem_base + 128u * xx + 8u * kk, desc_v(sV + b * TILE, kk),
-                                idesc_o, (t | kk) != 0);
-                umma_commit(&pv_done[xx]);
-                if (t + 1 < ntiles) {
-                    go = mbar_wait(&pv_done[xx], t & 1, derr, abort_flag);
-                    if (go) scores(xx, nb);
-                }
-            }
-            if (go) {
-                umma_commit(&v_empty[b]);
-                if (t + 1 < ntiles) umma_commit(&k_empty[nb]);
-            }
-        }
-        umma_commit(drain);  // every MMA issued here completes before TMEM is released
-        mbar_wait_drain(drain, 0, DRAIN_NS);
-    }
+        // the last two products: the one before the last may still run, and its phase has the
+        // other parity, so it is waited for first
+        if (nsteps > 1) ok = ok && wait_all(&pv_done[x], (nsteps - 2) & 1);
+        if (nsteps > 0) ok = ok && wait_all(&pv_done[x], (nsteps - 1) & 1);
 
-    // outputs: from TMEM (units of 2^mv, sums of 2^m, both with the bias)
-    if (warp < 8) {
+        // outputs: from TMEM (units of 2^mv, sums of 2^m, both with the bias)
         const bool have = ok && ntiles > 0;
         if (have) tc_fence_after();
         const int64_t part = (unit * P.splits + split) * (2 * TR) + brow;
@@ -432,17 +383,143 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
             if (B.active > 1) P.part_stat[part] = make_float4(m, mv, sum, 0.f);
             else if (P.lse) P.lse[out_row] = sum == 0.f ? -INFINITY : (m - BIAS + log2f(sum)) * 0.693147180559945f;
         }
+        if (B.active > 1) join_splits<__nv_bfloat16, HD, 2 * TR, 256, true>(P, B, unit, hq0, s_last);
+    } else if (warp < 16) {
+        // ------------------------------------------------------- codes -> fp16 operands
+        regs_down<REGS_CONVERT>();
+        const int tid = threadIdx.x - 256;
+        const int r32 = tid >> 3, c16 = tid & 7;  // row within 32 keys, 16-code column
+        const int* table = P.q.page_table + static_cast<int64_t>(s) * P.q.max_pages;
+        const int pm = P.c.page - 1;
+        const int last = max(B.k1 - 1, 0);
+        // this thread's first code in page 0, and bytes from one page's block to the next's
+        const int64_t first = (((layer * P.c.n_pages) * P.c.H + h) << P.c.page_log2) * HD + c16 * 16;
+        const uint8_t* base[2] = {P.c.code[0] + first, P.c.code[1] + first};
+        const uint32_t page_bytes = static_cast<uint32_t>(P.c.H << P.c.page_log2) * HD;
+        uint4 kr[4], vr[4];
+        int pid[4], pid_next[4];  // pages of the tile being loaded and of the one after it
+        auto pages = [&](int t, int (&p)[4]) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p[i] = __ldg(table + (min(B.k0 + t * TK + 32 * i + r32, last) >> P.c.page_log2));
+        };
+        auto load = [&](int kv, int t, uint4 (&u)[4]) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int j = B.k0 + t * TK + 32 * i + r32;
+                // slots past the last visible key may hold anything: not read
+                const bool have = j < B.k1 && pid[i] >= 0 && pid[i] < P.c.n_pages;
+                u[i] = load16_if(base[kv] + static_cast<uint64_t>(static_cast<uint32_t>(pid[i])) * page_bytes + (j & pm) * HD, have);
+            }
+        };
+        auto store = [&](uint8_t* tile, const uint4 (&u)[4]) {
+            // codes 16 c16 .. +15 are chunks 2 c16 and 2 c16 + 1; lanes of the upper 64 dims
+            // store theirs in the other order, so that eight lanes hit eight bank groups
+            const int flip = c16 >> 2;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint4 a = make_uint4(half2_of_lo(u[i].x), half2_of_hi(u[i].x), half2_of_lo(u[i].y), half2_of_hi(u[i].y));
+                const uint4 b = make_uint4(half2_of_lo(u[i].z), half2_of_hi(u[i].z), half2_of_lo(u[i].w), half2_of_hi(u[i].w));
+                *reinterpret_cast<uint4*>(tile + sw_off(32 * i + r32, 2 * c16 + flip)) = flip ? b : a;
+                *reinterpret_cast<uint4*>(tile + sw_off(32 * i + r32, 2 * c16 + 1 - flip)) = flip ? a : b;
+            }
+        };
+        if (ntiles > 0) {
+            pages(0, pid);
+            pages(1, pid_next);
+            load(0, 0, kr);
+            load(1, 0, vr);
+        }
+        for (int t = 0; t < ntiles; ++t) {
+            const int b = t & 1;
+            float ks = 0.f, ev = 0.f;
+            if (tid < 8) {
+                const int j = B.k0 + t * TK + 16 * tid;
+                if (j < B.k1) {
+                    const int pid = __ldg(table + (j >> P.c.page_log2));
+                    if (pid >= 0 && pid < P.c.n_pages) {
+                        const int64_t blk = (layer * P.c.n_pages + pid) * P.c.H + h;
+                        ks = __ldg(P.c.scale[0] + blk);
+                        ev = static_cast<float>(exponent_of(__ldg(P.c.scale[1] + blk)));
+                    } else {
+                        err_set(P.err, DEV_ERR_BAD_SEQ);
+                    }
+                }
+            }
+            if (!mbar_wait(&k_empty[b], ((t >> 1) & 1) ^ 1, derr, abort_flag)) break;
+            if (tid < 8) {
+                TileInfo& I = info[t & (INFO_RING - 1)];
+                I.ks[tid] = ks;
+                I.ev[tid] = ev;
+                mbar_arrive(&info_full[t & (INFO_RING - 1)]);
+            }
+            store(sK + b * TILE, kr);
+            fence_proxy_async_smem();
+            mbar_arrive(&k_full[b]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) pid[i] = pid_next[i];
+            if (t + 1 < ntiles) load(0, t + 1, kr);
+            if (t + 2 < ntiles) pages(t + 2, pid_next);
+            if (!mbar_wait(&v_empty[b], ((t >> 1) & 1) ^ 1, derr, abort_flag)) break;
+            store(sV + b * TILE, vr);
+            fence_proxy_async_smem();
+            mbar_arrive(&v_full[b]);
+            if (t + 1 < ntiles) load(1, t + 1, vr);
+        }
+    } else {
+        // ------------------------------------------------------- MMA issuer
+        regs_down<REGS_MMA>();
+        if (warp < 18 && lane == 0 && ntiles > 0) {
+            const int xx = warp - 16;  // one thread for each tile: one waits while the other's products run
+            constexpr uint32_t idesc_s = idesc_f16_f32(TR, SK);
+            constexpr uint32_t idesc_o = idesc_f16_f32(TR, HD) | IDESC_B_MN;
+            const uint64_t dq = desc_k(sQ + xx * TILE), dk = desc_k(sK), dv = desc_v(sV);
+            const uint32_t cS = tmem_base + 128u * xx, cO = tmem_base + 256u + 128u * xx;
+            auto scores = [&](int u) {  // step u: 64 key rows of tile u / 2
+                const uint64_t k = dk + (((u >> 1) & 1) * TILE + (u & 1) * 64 * 128) / 16;
+#pragma unroll
+                for (int kk = 0; kk < HD / 16; ++kk)
+                    umma_bf16(cS + SK * (u & 1), dq + step_k(kk), k + step_k(kk), idesc_s, kk != 0);
+                umma_commit(&s_full[2 * xx + (u & 1)]);
+            };
+            bool go = mbar_wait(q_full, 0, derr, abort_flag) && mbar_wait(&k_full[0], 0, derr, abort_flag);
+            if (go) {
+                tc_fence_after();
+                scores(0);
+                if (nsteps > 1) scores(1);
+                umma_commit(&k_empty[0]);
+            }
+            for (int u = 0; go && u < nsteps; ++u) {
+                const int t = u >> 1, hf = u & 1;
+                if (hf == 0 && !(go = mbar_wait(&v_full[t & 1], (t >> 1) & 1, derr, abort_flag))) break;
+                if (!(go = mbar_wait(&p_full[2 * xx + hf], t & 1, derr, abort_flag))) break;
+                tc_fence_after();
+                const uint64_t v = dv + ((t & 1) * TILE) / 16 + step_v(4 * hf);
+#pragma unroll
+                for (int kk = 0; kk < SK / 16; ++kk)
+                    umma_f16_ts(cO, cS + SK * hf + 8u * kk, v + step_v(kk), idesc_o, (u | kk) != 0);
+                umma_commit(&pv_done[xx]);
+                if (hf == 1) umma_commit(&v_empty[t & 1]);
+                if (u + 2 < nsteps) {
+                    if (hf == 0 && !(go = mbar_wait(&k_full[(t + 1) & 1], ((t + 1) >> 1) & 1, derr, abort_flag))) break;
+                    if (!(go = mbar_wait(&pv_done[xx], u & 1, derr, abort_flag))) break;  // P lies where S goes
+                    tc_fence_after();
+                    scores(u + 2);
+                    if (hf == 1) umma_commit(&k_empty[(t + 1) & 1]);
+                }
+            }
+            umma_commit(&drain[xx]);  // every MMA issued here completes before TMEM is released
+            mbar_wait_drain(&drain[xx], 0, DRAIN_NS);
+        }
     }
+
     tc_fence_before();
-    __threadfence();
     __syncthreads();
-    if (warp == 12) {
+    if (warp == 16) {
         __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem_base, 512);
     }
     if (threadIdx.x == 0 && *abort_flag) *reinterpret_cast<volatile int*>(P.err.mirror) = DEV_ERR_TIMEOUT;
-    if (B.active > 1) join_splits<__nv_bfloat16, HD, 2 * TR, NUM_THREADS>(P, B, unit, hq0, s_last);
 }
 
 }  // namespace
