@@ -94,11 +94,11 @@ struct Joined {
 
 // After a chunk's partial results are written: the last CTA of the unit to
 // arrive joins the chunks, in order.  Called by the CTA's first NTHREADS threads
-// (SOME: there are others, so they meet at named barrier 1).
+// (SOME: there are others, so they meet at named barrier 9).
 template <typename T, int D, int ROWS, int NTHREADS, bool SOME = false>
 __device__ __forceinline__ void join_splits(const AttnParams& P, const RowBlock& B, int64_t unit, int64_t hq0, int* s_last) {
     auto meet = [] {
-        if constexpr (SOME) named_bar_sync(1, NTHREADS);
+        if constexpr (SOME) named_bar_sync(9, NTHREADS);
         else __syncthreads();
     };
     __threadfence();

@@ -9,9 +9,9 @@
 //                 convert them to fp16 (exact) and lay them out as operands, keys
 //                 and values alike: 128-byte swizzle, key rows, K-major for S and
 //                 MN-major for O; also the scales of the tile's 16-key groups;
-//   warps 16, 17  one thread each issues S_x = Q_x K^T (SS) and O_x += P_x V (P from
-//                 TMEM) for tile x: one tile's softmax and waits run under the
-//                 other's products;
+//   warps 16, 17  one thread each issues S_x = Q_x K^T (SS) for tile x;
+//   warps 18, 19  and O_x += P_x V (P from TMEM): four threads, so that no product
+//                 waits behind a wait of another kind;
 //   warps 0..3, 4..7  softmax of tile 0, 1, a row a thread, 64 keys a step: scores
 //                 from TMEM to registers, P as fp16 over them, the sum in fp32; O is
 //                 rescaled in TMEM on the rare raise.
@@ -143,14 +143,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
     uint64_t* v_empty = bar + 6;   // [2]
     uint64_t* s_full = bar + 8;    // [tile x][buffer]
     uint64_t* p_full = bar + 12;   // [tile x][buffer]
-    uint64_t* pv_done = bar + 16;  // [tile x]
-    uint64_t* drain = bar + 18;    // [tile x]
-    uint64_t* q_full = bar + 20;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 21);
+    uint64_t* pv_done = bar + 16;  // [tile x][buffer]
+    uint64_t* drain = bar + 20;    // [issuer]
+    uint64_t* q_full = bar + 24;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 25);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int* s_last = reinterpret_cast<int*>(tmem_slot + 2);
-    uint64_t* info_full = bar + 24;  // [INFO_RING]
-    TileInfo* info = reinterpret_cast<TileInfo*>(bar + 24 + INFO_RING);
+    uint64_t* info_full = bar + 28;  // [INFO_RING]
+    TileInfo* info = reinterpret_cast<TileInfo*>(bar + 28 + INFO_RING);
 
     const int split = blockIdx.x;
     const int64_t unit = blockIdx.y + static_cast<int64_t>(blockIdx.z) * gridDim.y;
@@ -177,8 +177,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
             mbar_init(&s_full[2 * i + 1], 1);
             mbar_init(&p_full[2 * i], 128);
             mbar_init(&p_full[2 * i + 1], 128);
-            mbar_init(&pv_done[i], 1);
-            mbar_init(&drain[i], 1);
+            mbar_init(&pv_done[2 * i], 1);
+            mbar_init(&pv_done[2 * i + 1], 1);
+            mbar_init(&drain[2 * i], 1);
+            mbar_init(&drain[2 * i + 1], 1);
         }
         for (int i = 0; i < INFO_RING; ++i) mbar_init(&info_full[i], 8);
         mbar_init(q_full, 256);
@@ -294,7 +296,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
                 }
                 __syncwarp();
                 if (u > 0) {
-                    ok = wait_all(&pv_done[x], (u - 1) & 1);  // O is complete up to the step before
+                    ok = wait_all(&pv_done[2 * x + (hf ^ 1)], ((u - 1) >> 1) & 1);  // O is complete up to the step before
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll 1
@@ -344,10 +346,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
             tc_fence_before();
             mbar_arrive(&p_full[2 * x + hf]);
         }
-        // the last two products: the one before the last may still run, and its phase has the
-        // other parity, so it is waited for first
-        if (nsteps > 1) ok = ok && wait_all(&pv_done[x], (nsteps - 2) & 1);
-        if (nsteps > 0) ok = ok && wait_all(&pv_done[x], (nsteps - 1) & 1);
+        if (nsteps > 0) ok = ok && wait_all(&pv_done[2 * x + ((nsteps - 1) & 1)], ((nsteps - 1) >> 1) & 1);
 
         // outputs: from TMEM (units of 2^mv, sums of 2^m, both with the bias)
         const bool have = ok && ntiles > 0;
@@ -468,47 +467,44 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
     } else {
         // ------------------------------------------------------- MMA issuer
         regs_down<REGS_MMA>();
-        if (warp < 18 && lane == 0 && ntiles > 0) {
-            const int xx = warp - 16;  // one thread for each tile: one waits while the other's products run
-            constexpr uint32_t idesc_s = idesc_f16_f32(TR, SK);
-            constexpr uint32_t idesc_o = idesc_f16_f32(TR, HD) | IDESC_B_MN;
-            const uint64_t dq = desc_k(sQ + xx * TILE), dk = desc_k(sK), dv = desc_v(sV);
-            const uint32_t cS = tmem_base + 128u * xx, cO = tmem_base + 256u + 128u * xx;
-            auto scores = [&](int u) {  // step u: 64 key rows of tile u / 2
-                const uint64_t k = dk + (((u >> 1) & 1) * TILE + (u & 1) * 64 * 128) / 16;
-#pragma unroll
-                for (int kk = 0; kk < HD / 16; ++kk)
-                    umma_bf16(cS + SK * (u & 1), dq + step_k(kk), k + step_k(kk), idesc_s, kk != 0);
-                umma_commit(&s_full[2 * xx + (u & 1)]);
-            };
-            bool go = mbar_wait(q_full, 0, derr, abort_flag) && mbar_wait(&k_full[0], 0, derr, abort_flag);
-            if (go) {
-                tc_fence_after();
-                scores(0);
-                if (nsteps > 1) scores(1);
-                umma_commit(&k_empty[0]);
-            }
-            for (int u = 0; go && u < nsteps; ++u) {
-                const int t = u >> 1, hf = u & 1;
-                if (hf == 0 && !(go = mbar_wait(&v_full[t & 1], (t >> 1) & 1, derr, abort_flag))) break;
-                if (!(go = mbar_wait(&p_full[2 * xx + hf], t & 1, derr, abort_flag))) break;
-                tc_fence_after();
-                const uint64_t v = dv + ((t & 1) * TILE) / 16 + step_v(4 * hf);
-#pragma unroll
-                for (int kk = 0; kk < SK / 16; ++kk)
-                    umma_f16_ts(cO, cS + SK * hf + 8u * kk, v + step_v(kk), idesc_o, (u | kk) != 0);
-                umma_commit(&pv_done[xx]);
-                if (hf == 1) umma_commit(&v_empty[t & 1]);
-                if (u + 2 < nsteps) {
-                    if (hf == 0 && !(go = mbar_wait(&k_full[(t + 1) & 1], ((t + 1) >> 1) & 1, derr, abort_flag))) break;
-                    if (!(go = mbar_wait(&pv_done[xx], u & 1, derr, abort_flag))) break;  // P lies where S goes
+        if (lane == 0 && nsteps > 0) {
+            const int xx = warp & 1;
+            const uint32_t cS = tmem_base + 128u * xx;
+            if (warp < 18) {
+                constexpr uint32_t idesc = idesc_f16_f32(TR, SK);
+                const uint64_t q = desc_k(sQ + xx * TILE), k0 = desc_k(sK);
+                bool go = mbar_wait(q_full, 0, derr, abort_flag);
+                for (int u = 0; go && u < nsteps; ++u) {
+                    const int t = u >> 1, hf = u & 1;
+                    if (hf == 0 && !(go = mbar_wait(&k_full[t & 1], (t >> 1) & 1, derr, abort_flag))) break;
+                    // P of step u - 2 lies where these scores go
+                    if (u > 1 && !(go = mbar_wait(&pv_done[2 * xx + hf], (t - 1) & 1, derr, abort_flag))) break;
                     tc_fence_after();
-                    scores(u + 2);
-                    if (hf == 1) umma_commit(&k_empty[(t + 1) & 1]);
+                    const uint64_t k = k0 + ((t & 1) * TILE + hf * 64 * 128) / 16;
+#pragma unroll
+                    for (int kk = 0; kk < HD / 16; ++kk) umma_bf16(cS + SK * hf, q + step_k(kk), k + step_k(kk), idesc, kk != 0);
+                    umma_commit(&s_full[2 * xx + hf]);
+                    if (hf == 1 || u + 1 == nsteps) umma_commit(&k_empty[t & 1]);
+                }
+            } else {
+                constexpr uint32_t idesc = idesc_f16_f32(TR, HD) | IDESC_B_MN;
+                const uint32_t cO = tmem_base + 256u + 128u * xx;
+                const uint64_t v0 = desc_v(sV);
+                for (int u = 0; u < nsteps; ++u) {
+                    const int t = u >> 1, hf = u & 1;
+                    if (hf == 0 && !mbar_wait(&v_full[t & 1], (t >> 1) & 1, derr, abort_flag)) break;
+                    if (!mbar_wait(&p_full[2 * xx + hf], t & 1, derr, abort_flag)) break;
+                    tc_fence_after();
+                    const uint64_t v = v0 + ((t & 1) * TILE) / 16 + step_v(4 * hf);
+#pragma unroll
+                    for (int kk = 0; kk < SK / 16; ++kk)
+                        umma_f16_ts(cO, cS + SK * hf + 8u * kk, v + step_v(kk), idesc, (u | kk) != 0);
+                    umma_commit(&pv_done[2 * xx + hf]);
+                    if (hf == 1) umma_commit(&v_empty[t & 1]);
                 }
             }
-            umma_commit(&drain[xx]);  // every MMA issued here completes before TMEM is released
-            mbar_wait_drain(&drain[xx], 0, DRAIN_NS);
+            umma_commit(&drain[warp - 16]);  // every MMA issued here completes before TMEM is released
+            mbar_wait_drain(&drain[warp - 16], 0, DRAIN_NS);
         }
     }
 
