@@ -26,8 +26,12 @@
 // tile exceeds them by 2^8 (one vote per tile); weights are biased by 2^7, so fp16
 // holds them from 2^15 down to 2^-24 (2^-31 of the reference).
 //
-// Keys are split into chunks over CTAs where there are few rows; the last CTA
-// of a unit to arrive joins the chunks in order, so results do not depend on timing.
+// The keys of all units (layer, sequence, row block, head) form one line of 64-key
+// tiles, which the CTAs that fit the GPU share evenly: unequal lengths cost
+// nothing, and a CTA pays its set-up once for each unit that it meets.  (Chunks of
+// 512 / 2048 keys as CTAs of their own took 588 / 402 us for 32 sequences of 32768
+// keys: about 4.6 us a CTA.)  The last CTA to arrive at a unit that several share
+// joins its pieces in order, so results do not depend on timing.
 #include "cache8_attn.cuh"
 
 namespace kvb {
@@ -37,7 +41,9 @@ namespace {
 
 constexpr int NWARPS = 4;
 constexpr int NT = NWARPS * 32;
-constexpr int MAX_PAGES = 512;    // pages of one chunk, listed in shared memory
+constexpr int TILE_KEYS = 16 * NWARPS;  // one step of the CTA
+constexpr int LIST_PAGES = 256;         // pages listed in shared memory at a time
+constexpr int MIN_TILES = 4;            // a CTA's least share
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -80,6 +86,37 @@ __device__ __forceinline__ float2 load2(const __nv_bfloat16* p) {
     return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
 }
 __device__ __forceinline__ float2 load2(const float* p) { return __ldg(reinterpret_cast<const float2*>(p)); }
+// CTAs to keep on an SM: what the accumulators (D/4 registers a row block) and the
+// 64 bytes of codes in flight leave; the rest of a thread's state may spill, it is
+// not used inside the key loop.
+constexpr int resident_ctas(size_t element, int D, int NB) {
+    return D < 64 ? 4 : D == 64 ? (NB == 1 ? 4 : NB == 2 ? 3 : 2) : NB == 1 ? (element == 4 ? 3 : 4) : 2;
+}
+
+// Inclusive scan / sum over the CTA's threads (scratch: one value a warp).
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* scratch) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, v, x);
+        if (lane >= x) v += o;
+    }
+    __syncthreads();  // scratch is free
+    if (lane == 31) scratch[warp] = v;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) v += scratch[w];
+    return v;
+}
+__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* scratch) {
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
+    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0;
+    for (int w = 0; w < NWARPS; ++w) v += scratch[w];
+    return v;
+}
+
 template <typename T, int D, int NB>
 struct Shape8 {
     static constexpr int PARTS = sizeof(T) == 4 ? 2 : 1;  // fp16 parts of a query element and of a weight
@@ -88,12 +125,12 @@ struct Shape8 {
     // per warp: its outputs, references and sums; then the page list of the chunk
     static constexpr int Q_WORDS = PARTS * NB * KS * 2 * 32;
     static constexpr size_t smem() {
-        return sizeof(float) * (NWARPS * ROWS * D + NWARPS * ROWS * 4) + 4 * Q_WORDS + MAX_PAGES * 12;
+        return sizeof(float) * (NWARPS * ROWS * D + NWARPS * ROWS * 4) + 4 * Q_WORDS + (LIST_PAGES + 1) * 12;
     }
 };
 
 template <typename T, int D, int NB>
-__global__ void __launch_bounds__(NT) decode_kernel(const __grid_constant__ AttnParams P) {
+__global__ void __launch_bounds__(NT, resident_ctas(sizeof(T), D, NB)) decode_kernel(const __grid_constant__ AttnParams P) {
     using S8 = Shape8<T, D, NB>;
     constexpr int PARTS = S8::PARTS, ROWS = S8::ROWS, KS = S8::KS;
     constexpr int KB = D / 4, VB = D / 8;                    // bytes of a lane: of a key row, of a value row
@@ -104,39 +141,85 @@ __global__ void __launch_bounds__(NT) decode_kernel(const __grid_constant__ Attn
     float* sqs = reinterpret_cast<float*>(stat);             // [ROWS] factors of the query rows, before that
     uint32_t* sq = reinterpret_cast<uint32_t*>(stat + NWARPS * ROWS);  // query fragments
     int* s_page = reinterpret_cast<int*>(sq + S8::Q_WORDS);
-    float* s_ks = reinterpret_cast<float*>(s_page + MAX_PAGES);  // key scale
-    float* s_ev = s_ks + MAX_PAGES;                              // exponent of the value scale
-    __shared__ int s_last;
+    float* s_ks = reinterpret_cast<float*>(s_page + LIST_PAGES + 1);  // key scale
+    float* s_ev = s_ks + LIST_PAGES + 1;                              // exponent of the value scale
+    __shared__ int s_last, s_found;
+    __shared__ int64_t s_before, s_total, s_scan[NWARPS];
 
-    const int split = blockIdx.x;
-    const int64_t unit = blockIdx.y + static_cast<int64_t>(blockIdx.z) * gridDim.y;
-    const int h = blockIdx.y % P.c.H;
-    const int rb = blockIdx.y / P.c.H;
-    const int s = blockIdx.z % P.q.n_seq;
-    const int l = blockIdx.z / P.q.n_seq;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = lane >> 2, c = lane & 3;
 
-    RowBlock B;
-    if (!row_block(P, s, rb, ROWS, split, B)) return;
-    const int k0 = B.k0, k1 = B.k1, nrows = B.nrows;
-    const int64_t row0 = B.row0;
-
-    // the chunk's pages and scales
-    const int page0 = k0 >> P.c.page_log2;
-    const int npages = k1 > k0 ? ((k1 - 1) >> P.c.page_log2) - page0 + 1 : 0;
-    const int64_t layer = static_cast<int64_t>(P.c.l_begin) + l;
-    for (int i = threadIdx.x; i < npages; i += NT) {
-        int pid = __ldg(P.q.page_table + static_cast<int64_t>(s) * P.q.max_pages + page0 + i);
-        if (pid < 0 || pid >= P.c.n_pages) {
-            err_set(P.err, DEV_ERR_BAD_SEQ);
-            pid = -1;
+    // tiles of an entry (sequence, row block); every head of every layer has as many
+    const int entries = P.q.n_seq * P.row_blocks;
+    auto entry = [&](int e) { return row_block(P, e / P.row_blocks, e % P.row_blocks, ROWS); };
+    auto tiles_of = [](const RowBlock& B) { return B.nrows == 0 ? 0 : max(1, (B.kv_end + TILE_KEYS - 1) / TILE_KEYS); };
+    // their sum, then this CTA's place in the line
+    const int64_t mine0 = static_cast<int>(threadIdx.x) < entries ? tiles_of(entry(threadIdx.x)) : 0;
+    int64_t per_layer = mine0;
+    for (int e = threadIdx.x + NT; e < entries; e += NT) per_layer += tiles_of(entry(e));
+    per_layer = block_sum(per_layer, s_scan) * P.c.H;
+    const int64_t all = per_layer * P.c.n_layers;
+    const int64_t share = max(static_cast<int64_t>(MIN_TILES), (all + gridDim.x - 1) / gridDim.x);
+    int64_t at = blockIdx.x * share;
+    if (at >= all) return;
+    const int64_t stop = min(all, at + share);
+    int l = static_cast<int>(at / per_layer);
+    int e = -1;
+    int64_t before = 0;  // tiles of the entries before e, times H
+    const int64_t want = at - l * per_layer;
+    for (int e0 = 0; e < 0; e0 += NT) {
+        if (e0 >= entries) return;  // not reached while the call's arrays stay as they are
+        const int ee = e0 + threadIdx.x;
+        const int64_t mine = (e0 == 0 ? mine0 : ee < entries ? tiles_of(entry(ee)) : 0) * P.c.H;
+        const int64_t incl = before + block_scan(mine, s_scan);
+        if (threadIdx.x == 0) s_found = -1;
+        __syncthreads();
+        if (want >= incl - mine && want < incl) {
+            s_found = ee;
+            s_before = incl - mine;
         }
-        s_page[i] = pid;
-        const int64_t b = (layer * P.c.n_pages + pid) * P.c.H + h;
-        s_ks[i] = pid < 0 ? 1.f : __ldg(P.c.scale[0] + b);
-        s_ev[i] = pid < 0 ? 0.f : static_cast<float>(exponent_of(__ldg(P.c.scale[1] + b)));
+        if (threadIdx.x == NT - 1) s_total = incl;
+        __syncthreads();
+        e = s_found;
+        before = e < 0 ? s_total : s_before;
+        __syncthreads();
     }
+    RowBlock B = entry(e);
+    int tiles = tiles_of(B);
+    int64_t in_entry = at - l * per_layer - before;
+    int h = static_cast<int>(in_entry / tiles);
+    int first = static_cast<int>(in_entry - static_cast<int64_t>(h) * tiles);
+
+    // one unit, or a piece of one, after another
+    for (;;) {
+    const int s = e / P.row_blocks;
+    const int last = static_cast<int>(min(static_cast<int64_t>(tiles), first + (stop - at)));  // tiles [first, last)
+    const int k0 = first * TILE_KEYS, k1 = min(B.kv_end, last * TILE_KEYS);
+    const int nrows = B.nrows;
+    const int64_t row0 = B.row0;
+    const int64_t unit = (static_cast<int64_t>(l) * entries + e) * P.c.H + h;
+    const int64_t layer = static_cast<int64_t>(P.c.l_begin) + l;
+
+    // pages and scales of the keys from k on, up to LIST_PAGES pages' worth
+    int page0 = 0;
+    auto list_pages = [&](int k) {
+        page0 = k >> P.c.page_log2;
+        const int end = min(k1, k + (LIST_PAGES << P.c.page_log2));
+        const int npages = end > k ? ((end - 1) >> P.c.page_log2) - page0 + 1 : 0;
+        for (int i = threadIdx.x; i < npages; i += NT) {
+            int pid = __ldg(P.q.page_table + static_cast<int64_t>(s) * P.q.max_pages + page0 + i);
+            if (pid < 0 || pid >= P.c.n_pages) {
+                err_set(P.err, DEV_ERR_BAD_SEQ);
+                pid = -1;
+            }
+            s_page[i] = pid;
+            const int64_t b = (layer * P.c.n_pages + pid) * P.c.H + h;
+            s_ks[i] = pid < 0 ? 1.f : __ldg(P.c.scale[0] + b);
+            s_ev[i] = pid < 0 ? 0.f : static_cast<float>(exponent_of(__ldg(P.c.scale[1] + b)));
+        }
+        return end;
+    };
+    int listed = list_pages(k0);
 
     // query fragments (every warp needs all of them: row block b is laid out by warp b % NWARPS)
     const T* query = static_cast<const T*>(P.query);
@@ -240,13 +323,15 @@ __global__ void __launch_bounds__(NT) decode_kernel(const __grid_constant__ Attn
         load_codes<VB>(p + (2 * c + 8) * D, vw[2]);
         load_codes<VB>(p + (2 * c + 9) * D, vw[3]);
     };
-    int j = k0 + 16 * warp;
-    if (j < k1) {
+    int kc = k0;  // keys [kc, listed) are listed
+    for (;;) {
+    int j = kc + 16 * warp;
+    if (j < listed) {
         load_k(j);
         load_v(j);
     }
-    for (; j < k1; j += 16 * NWARPS) {
-        const int jn = j + 16 * NWARPS;
+    for (; j < listed; j += TILE_KEYS) {
+        const int jn = j + TILE_KEYS;
         const int pi = (j >> P.c.page_log2) - page0;
         const bool bad = s_page[pi] < 0;
         const float ks = s_ks[pi], ev = s_ev[pi];
@@ -271,7 +356,7 @@ __global__ void __launch_bounds__(NT) decode_kernel(const __grid_constant__ Attn
                 }
             }
         }
-        if (jn < k1) load_k(jn);
+        if (jn < listed) load_k(jn);
         // scores in base 2, masked; keys r, r + 8 and query rows 2c, 2c + 1 of each row block
         const bool whole = !bad && j + 16 <= k1 && j + 15 <= B.pos_lo;
         bool raise = false;
@@ -349,7 +434,13 @@ __global__ void __launch_bounds__(NT) decode_kernel(const __grid_constant__ Attn
                     for (int p = 0; p < PARTS; ++p) mma16816(o[b][2 * x + y], a0, a1, a2, a3, pt[b][p][0], pt[b][p][1]);
             }
         }
-        if (jn < k1) load_v(jn);
+        if (jn < listed) load_v(jn);
+    }
+    if (listed >= k1) break;
+    __syncthreads();  // every warp is done with the list
+    kc = listed;
+    listed = list_pages(kc);
+    __syncthreads();
     }
 
     // join the warps: outputs in units of 2^mv, sums in units of 2^m (both with the bias)
@@ -370,16 +461,19 @@ __global__ void __launch_bounds__(NT) decode_kernel(const __grid_constant__ Attn
 
     T* out = static_cast<T*>(P.out);
     auto row_of = [&](int row) { return B.row_of(P, hq0, row); };
-    const int64_t part0 = (unit * P.splits + split) * ROWS;
-    for (int e = threadIdx.x; e < nrows * (D / 4); e += NT) {
-        const int row = e / (D / 4), d4 = e % (D / 4);
+    // the CTAs that share this unit, and this one's slot
+    const int64_t u0 = at - first, c0 = u0 / share;
+    const int pieces = static_cast<int>((u0 + tiles - 1) / share - c0) + 1;
+    const int64_t part0 = (2 * static_cast<int64_t>(blockIdx.x) + (first == 0)) * ROWS;
+    for (int i = threadIdx.x; i < nrows * (D / 4); i += NT) {
+        const int row = i / (D / 4), d4 = i % (D / 4);
         Joined z;
 #pragma unroll
         for (int w = 0; w < NWARPS; ++w) z.reference(stat[w * ROWS + row]);
 #pragma unroll
         for (int w = 0; w < NWARPS; ++w)
             z.add(stat[w * ROWS + row], reinterpret_cast<const float4*>(so + (w * ROWS + row) * D)[d4]);
-        if (B.active == 1) {
+        if (pieces == 1) {
             store_out(out + row_of(row) * D + 4 * d4, z.output());
             if (d4 == 0 && P.lse) P.lse[row_of(row)] = z.lse();
         } else {
@@ -387,37 +481,70 @@ __global__ void __launch_bounds__(NT) decode_kernel(const __grid_constant__ Attn
             if (d4 == 0) P.part_stat[part0 + row] = make_float4(z.m, z.mv, z.sum, 0.f);
         }
     }
-    if (B.active > 1) join_splits<T, D, ROWS, NT>(P, B, unit, hq0, &s_last);
+    if (pieces > 1)
+        join_splits<T, D, ROWS, NT>(P, B, Pieces{pieces, 2 * c0 + 1, 2 * c0 + 2, 2}, unit, hq0, &s_last, so, NWARPS * ROWS * D);
+
+    at += last - first;
+    if (at >= stop) return;
+    first = 0;
+    if (++h == P.c.H) {
+        h = 0;
+        do {
+            if (++e == entries) {
+                e = 0;
+                if (++l == P.c.n_layers) return;  // likewise not reached
+            }
+            B = entry(e);
+            tiles = tiles_of(B);
+        } while (tiles == 0);
+    }
+    __syncthreads();  // shared memory is free for the next unit
+    }
 }
 
+// One instance: CTAs of it that fit an SM (s null), or its launch.
 template <typename T, int D, int NB>
-cudaError_t launch_shape(const AttnParams& P, cudaStream_t s) {
+cudaError_t instance(const AttnParams* P, int ctas, cudaStream_t s, int* fit) {
     constexpr size_t smem = Shape8<T, D, NB>::smem();
+    static int resident = [] {
+        int n = 0;
+        if (cudaFuncSetAttribute(decode_kernel<T, D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) !=
+                cudaSuccess ||
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_kernel<T, D, NB>, NT, smem) != cudaSuccess)
+            return 0;
+        return n;
+    }();
+    if (fit) *fit = resident;
+    if (!P) return cudaSuccess;
     cudaError_t e = cudaFuncSetAttribute(decode_kernel<T, D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    dim3 grid(P.splits, P.c.H * P.row_blocks, P.q.n_seq * P.c.n_layers);
-    decode_kernel<T, D, NB><<<grid, NT, smem, s>>>(P);
+    decode_kernel<T, D, NB><<<ctas, NT, smem, s>>>(*P);
     return cudaGetLastError();
 }
 
 template <typename T, int D>
-cudaError_t launch_rows(const AttnParams& P, int rows, cudaStream_t s) {
+cudaError_t instance_rows(int rows, const AttnParams* P, int ctas, cudaStream_t s, int* fit) {
     switch (rows) {
-        case 8: return launch_shape<T, D, 1>(P, s);
-        case 16: return launch_shape<T, D, 2>(P, s);
-        default: return launch_shape<T, D, 4>(P, s);
+        case 8: return instance<T, D, 1>(P, ctas, s, fit);
+        case 16: return instance<T, D, 2>(P, ctas, s, fit);
+        default: return instance<T, D, 4>(P, ctas, s, fit);
     }
 }
 
 template <typename T>
-cudaError_t launch_dim(const AttnParams& P, int rows, cudaStream_t s) {
-    switch (P.c.d) {
-        case 16: return launch_rows<T, 16>(P, rows, s);
-        case 32: return launch_rows<T, 32>(P, rows, s);
-        case 64: return launch_rows<T, 64>(P, rows, s);
-        default: return launch_rows<T, 128>(P, rows, s);
+cudaError_t instance_dim(int d, int rows, const AttnParams* P, int ctas, cudaStream_t s, int* fit) {
+    switch (d) {
+        case 16: return instance_rows<T, 16>(rows, P, ctas, s, fit);
+        case 32: return instance_rows<T, 32>(rows, P, ctas, s, fit);
+        case 64: return instance_rows<T, 64>(rows, P, ctas, s, fit);
+        default: return instance_rows<T, 128>(rows, P, ctas, s, fit);
     }
+}
+
+cudaError_t pick(kvb_dtype dtype, int d, int rows, const AttnParams* P, int ctas, cudaStream_t s, int* fit) {
+    return dtype == KVB_BF16 ? instance_dim<__nv_bfloat16>(d, rows, P, ctas, s, fit)
+                             : instance_dim<float>(d, rows, P, ctas, s, fit);
 }
 
 }  // namespace
@@ -446,22 +573,25 @@ AttnPlan plan_attention(const Cache& c, const Seqs& q, kvb_dtype dtype, int g, i
             }
         }
         p.chunk = static_cast<int>(per * 128);
+        p.splits = static_cast<int>((static_cast<int64_t>(max_kv) + p.chunk - 1) / p.chunk);
+        p.slots = p.splits > 1 ? p.units * p.splits : 0;
     } else {
-        // four CTAs fit an SM: cut the keys so that there are about four waves of them where
-        // there is that much work, into no fewer than 64 keys (one step of the four warps)
-        const double most_chunk = MAX_PAGES / 2 * c.page < 2048 ? MAX_PAGES / 2 * c.page : 2048;
-        double chunk = max_kv * static_cast<double>(p.units) / (num_sms * 16.0);
-        if (chunk > most_chunk) chunk = most_chunk;
-        p.chunk = chunk <= 64 ? 64 : (static_cast<int>(chunk) + 127) / 128 * 128;
+        // the CTAs that fit the GPU, no more than the keys give MIN_TILES tiles to
+        int fit = 0;
+        pick(dtype, c.d, p.rows, nullptr, 0, nullptr, &fit);
+        const double most_tiles = static_cast<double>(p.units) * ((static_cast<int64_t>(max_kv) + TILE_KEYS - 1) / TILE_KEYS);
+        const double need = (most_tiles + MIN_TILES - 1) / MIN_TILES;
+        p.ctas = num_sms * (fit > 0 ? fit : 1);
+        if (need < p.ctas) p.ctas = static_cast<int>(need) < 1 ? 1 : static_cast<int>(need);
+        p.slots = 2 * static_cast<int64_t>(p.ctas);
     }
-    p.splits = static_cast<int>((static_cast<int64_t>(max_kv) + p.chunk - 1) / p.chunk);
     p.counter_bytes = (static_cast<size_t>(p.units) * sizeof(int) + 255) / 256 * 256;
-    p.partial_bytes = p.splits > 1 ? static_cast<size_t>(p.units) * p.splits * p.rows * (c.d + 4) * sizeof(float) : 0;
+    p.partial_bytes = static_cast<size_t>(p.slots) * p.rows * (c.d + 4) * sizeof(float);
     return p;
 }
 
-cudaError_t launch_decode(const AttnParams& P, kvb_dtype dtype, int rows, cudaStream_t s) {
-    return dtype == KVB_BF16 ? launch_dim<__nv_bfloat16>(P, rows, s) : launch_dim<float>(P, rows, s);
+cudaError_t launch_decode(const AttnParams& P, kvb_dtype dtype, const AttnPlan& p, cudaStream_t s) {
+    return pick(dtype, P.c.d, p.rows, &P, p.ctas, s, nullptr);
 }
 
 }  // namespace c8

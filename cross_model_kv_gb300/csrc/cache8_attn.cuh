@@ -26,13 +26,13 @@ __device__ __forceinline__ void store_out(__nv_bfloat16* p, float4 v) {
 }
 __device__ __forceinline__ void store_out(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
 
-// The rows and keys of one CTA: row = token * g + head of the group, so the rows
-// of a block are close in position; keys [k0, k1) of the last row's visible ones.
+// A block of query rows of one sequence and head: row = token * g + head of the
+// group, so the rows of a block are close in position.
 struct RowBlock {
     int64_t row0;
-    int nrows, tok0, pos;
-    int pos_lo;        // position of the block's first row
-    int k0, k1, active;  // active: chunks that have keys (at least one)
+    int nrows, tok0, pos;  // nrows 0: the sequence has no such rows
+    int pos_lo;            // position of the block's first row
+    int kv_end;            // keys that its last row may see
     // index of a row in [n_layers][Hq][T]
     __device__ __forceinline__ int64_t row_of(const AttnParams& P, int64_t hq0, int row) const {
         const int64_t gr = row0 + row, i = gr / P.g;
@@ -40,29 +40,33 @@ struct RowBlock {
     }
 };
 
-// false where the block has no rows or the chunk no keys.
-__device__ __forceinline__ bool row_block(const AttnParams& P, int s, int rb, int rows, int split, RowBlock& B) {
+__device__ __forceinline__ RowBlock row_block(const AttnParams& P, int s, int rb, int rows) {
+    RowBlock B{};
     const SeqView sv = seq_view(P.q, s, P.err);
     const int64_t total = static_cast<int64_t>(sv.n) * P.g;
     B.row0 = static_cast<int64_t>(rb) * rows;
-    if (B.row0 >= total) return false;
+    if (B.row0 >= total) return B;
     B.nrows = static_cast<int>(min(static_cast<int64_t>(rows), total - B.row0));
     B.tok0 = sv.tok0;
     B.pos = sv.pos;
     int64_t kv = P.q.kv_len ? static_cast<int64_t>(__ldg(P.q.kv_len + s)) : static_cast<int64_t>(sv.pos) + sv.n;
     if (kv > P.q.max_kv) {
-        if (threadIdx.x == 0) err_set(P.err, DEV_ERR_BAD_SEQ);
+        err_set(P.err, DEV_ERR_BAD_SEQ);
         kv = P.q.max_kv;
     }
     const int64_t pos_hi = sv.pos + (B.row0 + B.nrows - 1) / P.g;  // position of the block's last row
     B.pos_lo = sv.pos + static_cast<int>(B.row0 / P.g);
-    const int kv_end = static_cast<int>(max(static_cast<int64_t>(0), min(kv, pos_hi + 1)));
-    B.active = max(1, static_cast<int>((static_cast<int64_t>(kv_end) + P.chunk - 1) / P.chunk));
-    if (split >= B.active) return false;
-    B.k0 = split * P.chunk;
-    B.k1 = static_cast<int>(min(static_cast<int64_t>(kv_end), static_cast<int64_t>(B.k0) + P.chunk));
-    return true;
+    B.kv_end = static_cast<int>(max(static_cast<int64_t>(0), min(kv, pos_hi + 1)));
+    return B;
 }
+
+// The partial results of one unit, in the order of its keys: slot(i), i < n.
+struct Pieces {
+    int n;
+    int64_t first, next;
+    int stride;
+    __device__ __forceinline__ int64_t slot(int i) const { return i == 0 ? first : next + static_cast<int64_t>(i - 1) * stride; }
+};
 
 // Parts of one row's result, each with its references: first every part's
 // reference(), then every part's add().  st = (m, mv, sum, -).  A part that saw
@@ -75,8 +79,10 @@ struct Joined {
         mv = fmaxf(mv, st.y);
     }
     __device__ __forceinline__ void add(const float4& st, const float4& o) {
-        const float f = ex2(st.y - mv);
         sum = fmaf(ex2(st.x - m), st.z, sum);
+        weigh(ex2(st.y - mv), o);
+    }
+    __device__ __forceinline__ void weigh(float f, const float4& o) {
         acc.x = fmaf(f, o.x, acc.x);
         acc.y = fmaf(f, o.y, acc.y);
         acc.z = fmaf(f, o.z, acc.z);
@@ -92,11 +98,15 @@ struct Joined {
     }
 };
 
-// After a chunk's partial results are written: the last CTA of the unit to
-// arrive joins the chunks, in order.  Called by the CTA's first NTHREADS threads
-// (SOME: there are others, so they meet at named barrier 9).
+// After a piece of a unit is written: the last CTA of the unit to arrive joins
+// the pieces, in order.  Called by the CTA's first NTHREADS threads
+// (SOME: there are others, so they meet at named barrier 9); buf: shared memory of
+// `cap` floats, free once they have met.  A warp takes a row's references and sum, the
+// weights of all chunks go to shared memory, then each thread adds its columns with
+// its loads in flight together: 64 pieces one after another took 15 us.
 template <typename T, int D, int ROWS, int NTHREADS, bool SOME = false>
-__device__ __forceinline__ void join_splits(const AttnParams& P, const RowBlock& B, int64_t unit, int64_t hq0, int* s_last) {
+__device__ __forceinline__ void join_splits(const AttnParams& P, const RowBlock& B, const Pieces& pieces, int64_t unit, int64_t hq0, int* s_last,
+                                            float* buf, int cap) {
     auto meet = [] {
         if constexpr (SOME) named_bar_sync(9, NTHREADS);
         else __syncthreads();
@@ -105,23 +115,51 @@ __device__ __forceinline__ void join_splits(const AttnParams& P, const RowBlock&
     meet();
     if (threadIdx.x == 0) {
         const int n = atomicAdd(P.counters + unit, 1);
-        *s_last = n == B.active - 1;
-        if (n == B.active - 1) P.counters[unit] = 0;
+        *s_last = n == pieces.n - 1;
+        if (n == pieces.n - 1) P.counters[unit] = 0;
     }
     meet();
     if (!*s_last) return;
     __threadfence();
-    const int64_t u0 = unit * P.splits * ROWS;
+    const int active = pieces.n, lane = threadIdx.x & 31;
+    float4* ref = reinterpret_cast<float4*>(buf);  // [ROWS] (m, mv, sum, -)
+    float* weight = buf + 4 * ROWS;                // [row][piece]
+    const bool listed = active <= (cap - 4 * ROWS) / ROWS;
+    auto stat = [&](int row, int i) { return __ldcg(P.part_stat + pieces.slot(i) * ROWS + row); };
+    for (int row = threadIdx.x >> 5; row < B.nrows; row += NTHREADS / 32) {
+        float m = NO_REF, mv = NO_REF, sum = 0.f;
+        for (int i = lane; i < active; i += 32) {
+            const float4 st = stat(row, i);
+            m = fmaxf(m, st.x);
+            mv = fmaxf(mv, st.y);
+        }
+#pragma unroll
+        for (int x = 1; x < 32; x <<= 1) {
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+            mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, x));
+        }
+        for (int i = lane; i < active; i += 32) {
+            const float4 st = stat(row, i);
+            sum = fmaf(ex2(st.x - m), st.z, sum);
+            if (listed) weight[row * active + i] = ex2(st.y - mv);
+        }
+#pragma unroll
+        for (int x = 1; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+        if (lane == 0) ref[row] = make_float4(m, mv, sum, 0.f);
+    }
+    meet();
     T* out = static_cast<T*>(P.out);
     for (int e = threadIdx.x; e < B.nrows * (D / 4); e += NTHREADS) {
         const int row = e / (D / 4), d4 = e % (D / 4);
+        const float4 st = ref[row];
         Joined z;
-        for (int i = 0; i < B.active; ++i) z.reference(__ldcg(P.part_stat + u0 + static_cast<int64_t>(i) * ROWS + row));
-#pragma unroll 4
-        for (int i = 0; i < B.active; ++i) {
-            const int64_t p = u0 + static_cast<int64_t>(i) * ROWS + row;
-            z.add(__ldcg(P.part_stat + p), __ldcg(reinterpret_cast<const float4*>(P.partial + p * D) + d4));
-        }
+        z.m = st.x;
+        z.mv = st.y;
+        z.sum = st.z;
+#pragma unroll 8
+        for (int i = 0; i < active; ++i)
+            z.weigh(listed ? weight[row * active + i] : ex2(stat(row, i).y - z.mv), 
+                    __ldcg(reinterpret_cast<const float4*>(P.partial + (pieces.slot(i) * ROWS + row) * D) + d4));
         const int64_t o = B.row_of(P, hq0, row);
         store_out(out + o * D + 4 * d4, z.output());
         if (d4 == 0 && P.lse) P.lse[o] = z.lse();

@@ -160,9 +160,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
     const int l = blockIdx.z / P.q.n_seq;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    RowBlock B;
-    if (!row_block(P, s, rb, 2 * TR, split, B)) return;
-    const int ntiles = (B.k1 - B.k0 + TK - 1) / TK, nsteps = (B.k1 - B.k0 + SK - 1) / SK;
+    const RowBlock B = row_block(P, s, rb, 2 * TR);
+    const int active = max(1, (B.kv_end + P.chunk - 1) / P.chunk);  // chunks that have keys
+    if (B.nrows == 0 || split >= active) return;
+    const int k0 = split * P.chunk, k1 = min(B.kv_end, k0 + P.chunk);
+    const int ntiles = (k1 - k0 + TK - 1) / TK, nsteps = (k1 - k0 + SK - 1) / SK;
+    const int tiles = B.nrows > TR ? 2 : 1;  // the second tile's warps have nothing to do where there is one
     const int64_t layer = static_cast<int64_t>(P.c.l_begin) + l;
     const int64_t hq0 = (static_cast<int64_t>(l) * P.c.H + h) * P.g;
     const DevErr derr{P.err.word, P.err.timeout_ns};
@@ -170,9 +173,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&k_full[i], CONV);
-            mbar_init(&k_empty[i], 2);
+            mbar_init(&k_empty[i], tiles);
             mbar_init(&v_full[i], CONV);
-            mbar_init(&v_empty[i], 2);
+            mbar_init(&v_empty[i], tiles);
             mbar_init(&s_full[2 * i], 1);
             mbar_init(&s_full[2 * i + 1], 1);
             mbar_init(&p_full[2 * i], 128);
@@ -183,7 +186,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
             mbar_init(&drain[2 * i + 1], 1);
         }
         for (int i = 0; i < INFO_RING; ++i) mbar_init(&info_full[i], 8);
-        mbar_init(q_full, 256);
+        mbar_init(q_full, TR * tiles);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -215,8 +218,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
     if (warp < 8) {
         regs_up<REGS_SOFTMAX>();
         // the row as fp16 under a power of two: largest element in [2^13, 2^14)
-        float qs;
-        {
+        float qs = 1.f;
+        if (x < tiles) {
             const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(P.query) + out_row * HD);
             uint4 u[16];
 #pragma unroll
@@ -245,8 +248,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
             mbar_arrive(q_full);
         }
         // keys below `see` are visible to this row
-        const int see = valid ? min(B.k1, B.pos + static_cast<int>(tok) + 1) : 0;
-        for (int u = 0; u < nsteps; ++u) {
+        const int see = valid ? min(k1, B.pos + static_cast<int>(tok) + 1) : 0;
+        for (int u = 0; x < tiles && u < nsteps; ++u) {
             const int t = u >> 1, hf = u & 1;
             if (hf == 0) ok = wait_all(&info_full[t & (INFO_RING - 1)], (t / INFO_RING) & 1);
             ok = ok && wait_all(&s_full[2 * x + hf], t & 1);
@@ -262,7 +265,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
             const float k[4] = {fmaxf(ks4.x * qs, FLT_MIN), fmaxf(ks4.y * qs, FLT_MIN), fmaxf(ks4.z * qs, FLT_MIN),
                                 fmaxf(ks4.w * qs, FLT_MIN)};
             // visible keys of this row are a prefix of the step's
-            const int nvis = min(see - (B.k0 + u * SK), SK);
+            const int nvis = min(see - (k0 + u * SK), SK);
             const bool whole = nvis == SK && ks4.x != 0.f && ks4.y != 0.f && ks4.z != 0.f && ks4.w != 0.f;
             tmem_ld_wait();
             if (!__all_sync(0xffffffffu, whole)) {
@@ -346,10 +349,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
             tc_fence_before();
             mbar_arrive(&p_full[2 * x + hf]);
         }
-        if (nsteps > 0) ok = ok && wait_all(&pv_done[2 * x + ((nsteps - 1) & 1)], ((nsteps - 1) >> 1) & 1);
+        if (x < tiles && nsteps > 0) ok = ok && wait_all(&pv_done[2 * x + ((nsteps - 1) & 1)], ((nsteps - 1) >> 1) & 1);
 
         // outputs: from TMEM (units of 2^mv, sums of 2^m, both with the bias)
-        const bool have = ok && ntiles > 0;
+        const bool have = x < tiles && ok && nsteps > 0;
         if (have) tc_fence_after();
         const int64_t part = (unit * P.splits + split) * (2 * TR) + brow;
         const float half = ex2(0.5f * (mv - m)), f = sum == 0.f ? 0.f : half / sum;
@@ -363,7 +366,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
 #pragma unroll
                 for (int u = 0; u < 16; ++u) o[u] = 0u;
             }
-            if (valid && B.active == 1) {
+            if (valid && active == 1) {
                 uint32_t w[8];
 #pragma unroll
                 for (int u = 0; u < 8; ++u)
@@ -379,10 +382,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
             __syncwarp();
         }
         if (valid) {
-            if (B.active > 1) P.part_stat[part] = make_float4(m, mv, sum, 0.f);
+            if (active > 1) P.part_stat[part] = make_float4(m, mv, sum, 0.f);
             else if (P.lse) P.lse[out_row] = sum == 0.f ? -INFINITY : (m - BIAS + log2f(sum)) * 0.693147180559945f;
         }
-        if (B.active > 1) join_splits<__nv_bfloat16, HD, 2 * TR, 256, true>(P, B, unit, hq0, s_last);
+        if (active > 1) join_splits<__nv_bfloat16, HD, 2 * TR, 256, true>(P, B, Pieces{active, unit * P.splits, unit * P.splits + 1, 1}, unit, hq0, s_last, reinterpret_cast<float*>(sQ), 2 * TILE / 4);
     } else if (warp < 16) {
         // ------------------------------------------------------- codes -> fp16 operands
         regs_down<REGS_CONVERT>();
@@ -390,7 +393,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
         const int r32 = tid >> 3, c16 = tid & 7;  // row within 32 keys, 16-code column
         const int* table = P.q.page_table + static_cast<int64_t>(s) * P.q.max_pages;
         const int pm = P.c.page - 1;
-        const int last = max(B.k1 - 1, 0);
+        const int last = max(k1 - 1, 0);
         // this thread's first code in page 0, and bytes from one page's block to the next's
         const int64_t first = (((layer * P.c.n_pages) * P.c.H + h) << P.c.page_log2) * HD + c16 * 16;
         const uint8_t* base[2] = {P.c.code[0] + first, P.c.code[1] + first};
@@ -399,14 +402,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
         int pid[4], pid_next[4];  // pages of the tile being loaded and of the one after it
         auto pages = [&](int t, int (&p)[4]) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) p[i] = __ldg(table + (min(B.k0 + t * TK + 32 * i + r32, last) >> P.c.page_log2));
+            for (int i = 0; i < 4; ++i) p[i] = __ldg(table + (min(k0 + t * TK + 32 * i + r32, last) >> P.c.page_log2));
         };
         auto load = [&](int kv, int t, uint4 (&u)[4]) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int j = B.k0 + t * TK + 32 * i + r32;
+                const int j = k0 + t * TK + 32 * i + r32;
                 // slots past the last visible key may hold anything: not read
-                const bool have = j < B.k1 && pid[i] >= 0 && pid[i] < P.c.n_pages;
+                const bool have = j < k1 && pid[i] >= 0 && pid[i] < P.c.n_pages;
                 u[i] = load16_if(base[kv] + static_cast<uint64_t>(static_cast<uint32_t>(pid[i])) * page_bytes + (j & pm) * HD, have);
             }
         };
@@ -432,8 +435,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
             const int b = t & 1;
             float ks = 0.f, ev = 0.f;
             if (tid < 8) {
-                const int j = B.k0 + t * TK + 16 * tid;
-                if (j < B.k1) {
+                const int j = k0 + t * TK + 16 * tid;
+                if (j < k1) {
                     const int pid = __ldg(table + (j >> P.c.page_log2));
                     if (pid >= 0 && pid < P.c.n_pages) {
                         const int64_t blk = (layer * P.c.n_pages + pid) * P.c.H + h;
@@ -467,8 +470,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
     } else {
         // ------------------------------------------------------- MMA issuer
         regs_down<REGS_MMA>();
-        if (lane == 0 && nsteps > 0) {
-            const int xx = warp & 1;
+        const int xx = warp & 1;
+        if (lane == 0 && nsteps > 0 && xx < tiles) {
             const uint32_t cS = tmem_base + 128u * xx;
             if (warp < 18) {
                 constexpr uint32_t idesc = idesc_f16_f32(TR, SK);

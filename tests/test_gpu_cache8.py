@@ -566,7 +566,7 @@ def test_refusals(kvb):
         assert f(P.ctx.handle, P.cache.ref, s.ref, 0, 2, 0, None, p(k), 1, None) == INVALID_ARG
         assert f(P.ctx.handle, P.cache.ref, s.ref, 0, 3, 0, p(k), p(k), 1, None) == INVALID_ARG
         assert f(P.ctx.handle, P.cache.ref, ref(seqs(n_seq=2 ** 31 - 1)), 0, 2, 0, p(k), p(k), 1, None) == UNSUPPORTED
-    assert att(seqs=ref(seqs(n_seq=40000))) == UNSUPPORTED  # sequences x layers above the grid
+    assert att(seqs=ref(seqs(n_seq=2 ** 31 - 1))) == UNSUPPORTED  # sequences x layers x heads above 2^31-1
     bad_d = kvb.kvb_ctx_create(spec(1, 1, 96, 1e6), spec(1, 1, 96, 1e6), 1, 64)
     assert lib.kvb_cache8_write(bad_d.handle, P.cache.ref, s.ref, 0, 1, 0, p(k), p(k), 1, None) == UNSUPPORTED
     # the binding's own
