@@ -55,7 +55,6 @@ struct AttnParams {
     float* lse;  // or null
     int g;       // query heads of a KV head
     int row_blocks;
-    int chunk, splits;  // tcgen05 kernel: keys of a chunk, chunks
     float scale_log2;   // scale * log2(e)
     int* counters;      // [units], 0 before and after a call
     float* partial;     // [slots][rows][d] outputs in units of 2^mv
@@ -67,15 +66,14 @@ struct AttnParams {
 struct AttnPlan {
     bool tensor;  // the tcgen05 kernel
     int rows, row_blocks;
-    int ctas;           // of the CUDA-core-fed kernel, which share the keys evenly
-    int chunk, splits;  // of the tcgen05 kernel
-    int64_t units;      // (layer, sequence, row block, head)
-    int64_t slots;      // partial results
+    int ctas;
+    int64_t units;  // (layer, sequence, row block, head)
+    int64_t slots;  // partial results: two a CTA
     size_t counter_bytes, partial_bytes;
 };
 AttnPlan plan_attention(const Cache& c, const Seqs& q, kvb_dtype dtype, int g, int num_sms);
 cudaError_t launch_decode(const AttnParams& P, kvb_dtype dtype, const AttnPlan& p, cudaStream_t s);
-cudaError_t launch_prefill(const AttnParams& P, cudaStream_t s);  // bf16, d 128, 256 rows a block
+cudaError_t launch_prefill(const AttnParams& P, const AttnPlan& p, cudaStream_t s);  // bf16, d 128
 
 #ifdef __CUDACC__
 

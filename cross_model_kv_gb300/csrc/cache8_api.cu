@@ -162,18 +162,15 @@ kvb_status kvb_cache8_attention(kvb_ctx* c, const kvb_cache8* cache, const kvb_s
     a.scale_log2 = static_cast<float>((scale > 0.0 ? scale : 1.0 / std::sqrt(static_cast<double>(c->d))) * 1.4426950408889634);
     a.err = call_err(c);
     const c8::AttnPlan p = c8::plan_attention(a.c, a.q, dtype, a.g, c->num_sms);
-    if (p.units > 0x7fffffffLL || (p.tensor && (static_cast<int64_t>(p.row_blocks) * c->H > 65535 ||
-                                                static_cast<int64_t>(a.q.n_seq) * n_layers > 65535)))
+    if (p.units > 0x7fffffffLL)
         return fail(KVB_ERR_UNSUPPORTED, "kvb_cache8_attention: too many query rows, sequences or layers in one call");
     if ((st = ensure_attn_ws(c, p, s)) != KVB_OK) return st;
     a.counters = static_cast<int*>(c->attn_ws);
     a.partial = reinterpret_cast<float*>(static_cast<char*>(c->attn_ws) + c->attn_ws_counters);
     a.part_stat = reinterpret_cast<float4*>(a.partial + static_cast<size_t>(p.slots) * p.rows * c->d);
     a.row_blocks = p.row_blocks;
-    a.chunk = p.chunk;
-    a.splits = p.splits;
     ProfScope ps(c, s, p.tensor ? "cache8_attention_tcgen05" : "cache8_attention");
-    const cudaError_t e = p.tensor ? c8::launch_prefill(a, s) : c8::launch_decode(a, dtype, p, s);
+    const cudaError_t e = p.tensor ? c8::launch_prefill(a, p, s) : c8::launch_decode(a, dtype, p, s);
     return e == cudaSuccess ? KVB_OK : cuda_fail(e, "cache8 attention launch");
 }
 

@@ -43,7 +43,6 @@ constexpr int NWARPS = 4;
 constexpr int NT = NWARPS * 32;
 constexpr int TILE_KEYS = 16 * NWARPS;  // one step of the CTA
 constexpr int LIST_PAGES = 256;         // pages listed in shared memory at a time
-constexpr int MIN_TILES = 4;            // a CTA's least share
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -93,30 +92,6 @@ constexpr int resident_ctas(size_t element, int D, int NB) {
     return D < 64 ? 4 : D == 64 ? (NB == 1 ? 4 : NB == 2 ? 3 : 2) : NB == 1 ? (element == 4 ? 3 : 4) : 2;
 }
 
-// Inclusive scan / sum over the CTA's threads (scratch: one value a warp).
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* scratch) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-    for (int x = 1; x < 32; x <<= 1) {
-        const int64_t o = __shfl_up_sync(0xffffffffu, v, x);
-        if (lane >= x) v += o;
-    }
-    __syncthreads();  // scratch is free
-    if (lane == 31) scratch[warp] = v;
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) v += scratch[w];
-    return v;
-}
-__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* scratch) {
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
-    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = 0;
-    for (int w = 0; w < NWARPS; ++w) v += scratch[w];
-    return v;
-}
-
 template <typename T, int D, int NB>
 struct Shape8 {
     static constexpr int PARTS = sizeof(T) == 4 ? 2 : 1;  // fp16 parts of a query element and of a weight
@@ -143,52 +118,20 @@ __global__ void __launch_bounds__(NT, resident_ctas(sizeof(T), D, NB)) decode_ke
     int* s_page = reinterpret_cast<int*>(sq + S8::Q_WORDS);
     float* s_ks = reinterpret_cast<float*>(s_page + LIST_PAGES + 1);  // key scale
     float* s_ev = s_ks + LIST_PAGES + 1;                              // exponent of the value scale
-    __shared__ int s_last, s_found;
-    __shared__ int64_t s_before, s_total, s_scan[NWARPS];
+    __shared__ int s_last;
+    __shared__ LineStart s_start;
+    __shared__ int64_t s_scan[NWARPS];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = lane >> 2, c = lane & 3;
 
-    // tiles of an entry (sequence, row block); every head of every layer has as many
+    int64_t at, stop, share;
+    int l, e, h, first;
+    if (!line_start<ROWS, TILE_KEYS, NT>(P, s_scan, &s_start, at, stop, share, l, e, h, first)) return;
     const int entries = P.q.n_seq * P.row_blocks;
     auto entry = [&](int e) { return row_block(P, e / P.row_blocks, e % P.row_blocks, ROWS); };
-    auto tiles_of = [](const RowBlock& B) { return B.nrows == 0 ? 0 : max(1, (B.kv_end + TILE_KEYS - 1) / TILE_KEYS); };
-    // their sum, then this CTA's place in the line
-    const int64_t mine0 = static_cast<int>(threadIdx.x) < entries ? tiles_of(entry(threadIdx.x)) : 0;
-    int64_t per_layer = mine0;
-    for (int e = threadIdx.x + NT; e < entries; e += NT) per_layer += tiles_of(entry(e));
-    per_layer = block_sum(per_layer, s_scan) * P.c.H;
-    const int64_t all = per_layer * P.c.n_layers;
-    const int64_t share = max(static_cast<int64_t>(MIN_TILES), (all + gridDim.x - 1) / gridDim.x);
-    int64_t at = blockIdx.x * share;
-    if (at >= all) return;
-    const int64_t stop = min(all, at + share);
-    int l = static_cast<int>(at / per_layer);
-    int e = -1;
-    int64_t before = 0;  // tiles of the entries before e, times H
-    const int64_t want = at - l * per_layer;
-    for (int e0 = 0; e < 0; e0 += NT) {
-        if (e0 >= entries) return;  // not reached while the call's arrays stay as they are
-        const int ee = e0 + threadIdx.x;
-        const int64_t mine = (e0 == 0 ? mine0 : ee < entries ? tiles_of(entry(ee)) : 0) * P.c.H;
-        const int64_t incl = before + block_scan(mine, s_scan);
-        if (threadIdx.x == 0) s_found = -1;
-        __syncthreads();
-        if (want >= incl - mine && want < incl) {
-            s_found = ee;
-            s_before = incl - mine;
-        }
-        if (threadIdx.x == NT - 1) s_total = incl;
-        __syncthreads();
-        e = s_found;
-        before = e < 0 ? s_total : s_before;
-        __syncthreads();
-    }
     RowBlock B = entry(e);
-    int tiles = tiles_of(B);
-    int64_t in_entry = at - l * per_layer - before;
-    int h = static_cast<int>(in_entry / tiles);
-    int first = static_cast<int>(in_entry - static_cast<int64_t>(h) * tiles);
+    int tiles = unit_tiles<TILE_KEYS>(B);
 
     // one unit, or a piece of one, after another
     for (;;) {
@@ -495,7 +438,7 @@ __global__ void __launch_bounds__(NT, resident_ctas(sizeof(T), D, NB)) decode_ke
                 if (++l == P.c.n_layers) return;  // likewise not reached
             }
             B = entry(e);
-            tiles = tiles_of(B);
+            tiles = unit_tiles<TILE_KEYS>(B);
         } while (tiles == 0);
     }
     __syncthreads();  // shared memory is free for the next unit
@@ -554,37 +497,18 @@ AttnPlan plan_attention(const Cache& c, const Seqs& q, kvb_dtype dtype, int g, i
     const int64_t most = static_cast<int64_t>(q.max_tokens) * g;  // rows of one sequence and head
     const double max_kv = q.max_kv > 0 ? q.max_kv : 1;
     p.tensor = dtype == KVB_BF16 && c.d == 128 && most > 64;
-    p.rows = p.tensor ? 256 : most <= 8 ? 8 : most <= 16 ? 16 : 32;
+    p.rows = p.tensor ? PREFILL_ROWS : most <= 8 ? 8 : most <= 16 ? 16 : 32;
     p.row_blocks = static_cast<int>((most + p.rows - 1) / p.rows);
     p.units = static_cast<int64_t>(c.n_layers) * q.n_seq * c.H * p.row_blocks;
-    if (p.tensor) {
-        // one CTA an SM: the number of chunks that fills the waves best, a CTA costing
-        // about six steps of 128 keys beside its keys (set-up, output)
-        const int64_t steps = (static_cast<int64_t>(max_kv) + 127) / 128;
-        double best = 0;
-        int64_t per = steps;
-        for (int64_t n = 1; n <= 16 && n <= steps; ++n) {
-            const int64_t k = (steps + n - 1) / n;
-            const double waves = static_cast<double>((p.units * n + num_sms - 1) / num_sms);
-            const double cost = waves * static_cast<double>(k + (n > 1 ? 8 : 6));
-            if (n == 1 || cost < best) {
-                best = cost;
-                per = k;
-            }
-        }
-        p.chunk = static_cast<int>(per * 128);
-        p.splits = static_cast<int>((static_cast<int64_t>(max_kv) + p.chunk - 1) / p.chunk);
-        p.slots = p.splits > 1 ? p.units * p.splits : 0;
-    } else {
-        // the CTAs that fit the GPU, no more than the keys give MIN_TILES tiles to
-        int fit = 0;
-        pick(dtype, c.d, p.rows, nullptr, 0, nullptr, &fit);
-        const double most_tiles = static_cast<double>(p.units) * ((static_cast<int64_t>(max_kv) + TILE_KEYS - 1) / TILE_KEYS);
-        const double need = (most_tiles + MIN_TILES - 1) / MIN_TILES;
-        p.ctas = num_sms * (fit > 0 ? fit : 1);
-        if (need < p.ctas) p.ctas = static_cast<int>(need) < 1 ? 1 : static_cast<int>(need);
-        p.slots = 2 * static_cast<int64_t>(p.ctas);
-    }
+    // the CTAs that fit the GPU, no more than the keys give MIN_TILES tiles to
+    int fit = 1;
+    if (!p.tensor) pick(dtype, c.d, p.rows, nullptr, 0, nullptr, &fit);
+    const int tile = p.tensor ? 128 : TILE_KEYS;
+    const double most_tiles = static_cast<double>(p.units) * ((static_cast<int64_t>(max_kv) + tile - 1) / tile);
+    const double need = (most_tiles + MIN_TILES - 1) / MIN_TILES;
+    p.ctas = num_sms * (fit > 0 ? fit : 1);
+    if (need < p.ctas) p.ctas = static_cast<int>(need) < 1 ? 1 : static_cast<int>(need);
+    p.slots = 2 * static_cast<int64_t>(p.ctas);
     p.counter_bytes = (static_cast<size_t>(p.units) * sizeof(int) + 255) / 256 * 256;
     p.partial_bytes = static_cast<size_t>(p.slots) * p.rows * (c.d + 4) * sizeof(float);
     return p;

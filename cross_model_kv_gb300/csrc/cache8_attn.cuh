@@ -9,6 +9,8 @@ namespace c8 {
 constexpr float BIAS = 7.f;    // weights are taken against 2^-7 of the reference
 constexpr float MARGIN = 8.f;  // a reference is raised past this much (base 2)
 constexpr float NO_REF = -3.0e38f;
+constexpr int MIN_TILES = 4;       // a CTA's least share of the line of tiles
+constexpr int PREFILL_ROWS = 256;  // rows of a unit in the tcgen05 kernel
 
 __device__ __forceinline__ float ex2(float x) {  // relative error about 2^-22
     float y;
@@ -58,6 +60,86 @@ __device__ __forceinline__ RowBlock row_block(const AttnParams& P, int s, int rb
     B.pos_lo = sv.pos + static_cast<int>(B.row0 / P.g);
     B.kv_end = static_cast<int>(max(static_cast<int64_t>(0), min(kv, pos_hi + 1)));
     return B;
+}
+
+// Tiles of TILE keys of a unit: one at least, so that rows that see nothing are written.
+template <int TILE>
+__device__ __forceinline__ int unit_tiles(const RowBlock& B) {
+    return B.nrows == 0 ? 0 : max(1, (B.kv_end + TILE - 1) / TILE);
+}
+
+// Inclusive scan / sum over the CTA's NTHREADS threads (scratch: one value a warp).
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* scratch) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, v, x);
+        if (lane >= x) v += o;
+    }
+    __syncthreads();  // scratch is free
+    if (lane == 31) scratch[warp] = v;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) v += scratch[w];
+    return v;
+}
+template <int NTHREADS>
+__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* scratch) {
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
+    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0;
+    for (int w = 0; w < NTHREADS / 32; ++w) v += scratch[w];
+    return v;
+}
+
+struct LineStart {
+    int found;
+    int64_t before, total;
+};
+
+// The units' tiles form one line: layer, then entry (sequence, row block), then
+// head.  This CTA takes tiles [at, stop) of it, the first of them tile `first` of unit
+// (l, e, h); share is every CTA's number.  false: nothing is left for this CTA.
+template <int ROWS, int TILE, int NTHREADS>
+__device__ __forceinline__ bool line_start(const AttnParams& P, int64_t* scratch, LineStart* found, int64_t& at, int64_t& stop,
+                                           int64_t& share, int& l, int& e, int& h, int& first) {
+    const int entries = P.q.n_seq * P.row_blocks;
+    auto tiles_of = [&](int i) { return unit_tiles<TILE>(row_block(P, i / P.row_blocks, i % P.row_blocks, ROWS)); };
+    const int64_t mine0 = static_cast<int>(threadIdx.x) < entries ? tiles_of(threadIdx.x) : 0;
+    int64_t per_layer = mine0;
+    for (int i = threadIdx.x + NTHREADS; i < entries; i += NTHREADS) per_layer += tiles_of(i);
+    per_layer = block_sum<NTHREADS>(per_layer, scratch) * P.c.H;
+    const int64_t all = per_layer * P.c.n_layers;
+    share = max(static_cast<int64_t>(MIN_TILES), (all + gridDim.x - 1) / gridDim.x);
+    at = blockIdx.x * share;
+    if (at >= all) return false;
+    stop = min(all, at + share);
+    l = static_cast<int>(at / per_layer);
+    const int64_t want = at - l * per_layer;
+    e = -1;
+    int64_t before = 0;  // tiles of the entries before e, times H
+    for (int e0 = 0; e < 0; e0 += NTHREADS) {
+        if (e0 >= entries) return false;  // not reached while the call's arrays stay as they are
+        const int i = e0 + threadIdx.x;
+        const int64_t mine = (e0 == 0 ? mine0 : i < entries ? tiles_of(i) : 0) * P.c.H;
+        const int64_t incl = before + block_scan(mine, scratch);
+        if (threadIdx.x == 0) found->found = -1;
+        __syncthreads();
+        if (want >= incl - mine && want < incl) {
+            found->found = i;
+            found->before = incl - mine;
+        }
+        if (threadIdx.x == NTHREADS - 1) found->total = incl;
+        __syncthreads();
+        e = found->found;
+        before = e < 0 ? found->total : found->before;
+        __syncthreads();
+    }
+    const int tiles = tiles_of(e);
+    h = static_cast<int>((want - before) / tiles);
+    first = static_cast<int>(want - before - static_cast<int64_t>(h) * tiles);
+    return true;
 }
 
 // The partial results of one unit, in the order of its keys: slot(i), i < n.
