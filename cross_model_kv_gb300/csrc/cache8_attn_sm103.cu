@@ -54,6 +54,7 @@ constexpr int REGS_SOFTMAX = 144, REGS_CONVERT = 72, REGS_MMA = 40;
 constexpr int INFO_RING = 8;  // scales are written at most seven tiles before the softmax is done with them
 constexpr int SMEM_BYTES = (2 + 2 * STAGES) * TILE + 1024 + 2048;
 constexpr uint32_t TM_S = 0, TM_O = 256;  // TMEM columns, 128 more for tile 1
+constexpr float FACTOR_LOG2 = 60.f;  // a group's factor is used within 2^-60 .. 2^60
 constexpr uint64_t DRAIN_NS = 200ull * 1000 * 1000;
 
 __device__ __forceinline__ uint32_t sw_off(int r, int c) {  // 16-byte chunk c (0..15) of row r
@@ -391,8 +392,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
                         }
                     }
                 }
-                // the weights; P takes the columns of the scores
-                float factor = 0.f;
+                // the weights; P takes the columns of the scores.  No branch lies between them: one
+                // a 16-key group cost 72 us of 556.
+                float far = 0.f;  // the largest |log2 factor| of a group
 #pragma unroll
                 for (int g2 = 0; g2 < 2; ++g2) {
                     uint32_t pw[16];
@@ -408,20 +410,21 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
                             w[j] = make_float2(ex2(w[j].x), ex2(w[j].y));
                             pw[8 * c + j] = pack_half2(w[j].x, w[j].y);
                         }
-                        if (gq == 0 || ev[gq] != ev[gq - 1]) factor = ex2(e);
-                        float2 p = add2(add2(add2(w[0], w[1]), add2(w[2], w[3])), add2(add2(w[4], w[5]), add2(w[6], w[7])));
-                        float p1 = (p.x + p.y) * factor;
-                        if (fabsf(e) > 60.f) {
-                            p1 = 0.f;
-#pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                p1 += ex2(fmaf(__uint_as_float(sv[16 * gq + j]), k[gq], BIAS - m));
-                        }
-                        sum += p1;
+                        const float2 p = add2(add2(add2(w[0], w[1]), add2(w[2], w[3])), add2(add2(w[4], w[5]), add2(w[6], w[7])));
+                        far = fmaxf(far, fabsf(e));
+                        sum += fabsf(e) < FACTOR_LOG2 ? (p.x + p.y) * ex2(e) : 0.f;
                     }
-                    __syncwarp();  // the warp-wide store, after branches that lanes may take apart
                     tmem_st16(cS + 16 * g2, pw);
                 }
+                if (far >= FACTOR_LOG2) {  // the sums of such groups from exponentials of their own
+#pragma unroll
+                    for (int gq = 0; gq < 4; ++gq)
+                        if (fabsf(mv - m - ev[gq]) >= FACTOR_LOG2) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) sum += ex2(fmaf(__uint_as_float(sv[16 * gq + j]), k[gq], BIAS - m));
+                        }
+                }
+                __syncwarp();
                 tmem_st_wait();
                 tc_fence_before();
                 mbar_arrive(&M.p_full[x][hf]);
