@@ -55,6 +55,7 @@ struct AttnParams {
     float* lse;  // or null
     int g;       // query heads of a KV head
     int row_blocks;
+    int min_tiles;      // a CTA's least share of the line of tiles
     float scale_log2;   // scale * log2(e)
     int* counters;      // [units], 0 before and after a call
     float* partial;     // [slots][rows][d] outputs in units of 2^mv
@@ -65,7 +66,8 @@ struct AttnParams {
 // How a call is cut: blocks of `rows` query rows, and their keys over CTAs.
 struct AttnPlan {
     bool tensor;  // the tcgen05 kernel
-    int rows, row_blocks;
+    bool few;     // the other one: few keys
+    int rows, row_blocks, min_tiles;
     int ctas;
     int64_t units;  // (layer, sequence, row block, head)
     int64_t slots;  // partial results: two a CTA

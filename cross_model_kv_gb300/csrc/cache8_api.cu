@@ -73,10 +73,10 @@ bool empty(const c8::Cache& c, const c8::Seqs& q) {
 
 c8::Err call_err(const kvb_ctx* c) { return c8::Err{c->err_dev, c->err_mirror, c->timeout_ns}; }
 
-// Blocks of a read or write: (K or V, layer, head, sequence, page that its tokens can touch).
+// Items of a read or write: (layer, head, sequence, page that its tokens can touch).
 bool too_many_blocks(const c8::Cache& c, const c8::Seqs& q) {
     const double items = (static_cast<double>(q.max_tokens) + c.page - 2) / c.page + 1;
-    return items * q.n_seq * c.H * c.n_layers * 2 > 2147483647.0;
+    return items * q.n_seq * c.H * c.n_layers > 2147483647.0;
 }
 
 // Counters (zeroed once; every call leaves them at zero) followed by the partial outputs.
@@ -169,6 +169,7 @@ kvb_status kvb_cache8_attention(kvb_ctx* c, const kvb_cache8* cache, const kvb_s
     a.partial = reinterpret_cast<float*>(static_cast<char*>(c->attn_ws) + c->attn_ws_counters);
     a.part_stat = reinterpret_cast<float4*>(a.partial + static_cast<size_t>(p.slots) * p.rows * c->d);
     a.row_blocks = p.row_blocks;
+    a.min_tiles = p.min_tiles;
     ProfScope ps(c, s, p.tensor ? "cache8_attention_tcgen05" : "cache8_attention");
     const cudaError_t e = p.tensor ? c8::launch_prefill(a, p, s) : c8::launch_decode(a, dtype, p, s);
     return e == cudaSuccess ? KVB_OK : cuda_fail(e, "cache8 attention launch");

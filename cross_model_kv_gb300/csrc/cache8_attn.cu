@@ -39,9 +39,9 @@ namespace c8 {
 
 namespace {
 
-constexpr int NWARPS = 4;
-constexpr int NT = NWARPS * 32;
-constexpr int TILE_KEYS = 16 * NWARPS;  // one step of the CTA
+constexpr int WARPS = 4;        // of a CTA; 16 keys each make its step, a tile of the line
+constexpr int WARPS_FEW = 8;    // where there are few keys: two CTAs an SM, their step 128 keys
+constexpr int FEW_TILES = 4;
 constexpr int LIST_PAGES = 256;         // pages listed in shared memory at a time
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -92,7 +92,7 @@ constexpr int resident_ctas(size_t element, int D, int NB) {
     return D < 64 ? 4 : D == 64 ? (NB == 1 ? 4 : NB == 2 ? 3 : 2) : NB == 1 ? (element == 4 ? 3 : 4) : 2;
 }
 
-template <typename T, int D, int NB>
+template <typename T, int D, int NB, int NWARPS>
 struct Shape8 {
     static constexpr int PARTS = sizeof(T) == 4 ? 2 : 1;  // fp16 parts of a query element and of a weight
     static constexpr int ROWS = 8 * NB;
@@ -104,9 +104,12 @@ struct Shape8 {
     }
 };
 
-template <typename T, int D, int NB>
-__global__ void __launch_bounds__(NT, resident_ctas(sizeof(T), D, NB)) decode_kernel(const __grid_constant__ AttnParams P) {
-    using S8 = Shape8<T, D, NB>;
+template <typename T, int D, int NB, int NWARPS>
+__global__ void __launch_bounds__(NWARPS * 32, NWARPS == WARPS ? resident_ctas(sizeof(T), D, NB) : 2)
+    decode_kernel(const __grid_constant__ AttnParams P) {
+    constexpr int NT = NWARPS * 32, TILE_KEYS = 16 * NWARPS;
+    constexpr int DEPTH = D <= 64 ? 2 : 1;  // 16-key steps of a warp in flight: 4 KB at d 128 and 64
+    using S8 = Shape8<T, D, NB, NWARPS>;
     constexpr int PARTS = S8::PARTS, ROWS = S8::ROWS, KS = S8::KS;
     constexpr int KB = D / 4, VB = D / 8;                    // bytes of a lane: of a key row, of a value row
     constexpr int KW = KB / 4, VW = VB >= 4 ? VB / 4 : 1;    // words
@@ -162,41 +165,86 @@ __global__ void __launch_bounds__(NT, resident_ctas(sizeof(T), D, NB)) decode_ke
         }
         return end;
     };
-    int listed = list_pages(k0);
-
-    // query fragments (every warp needs all of them: row block b is laid out by warp b % NWARPS)
+    // the rows' elements are asked for first, then the pages; the first codes come while the
+    // rows are laid out (row block b by warp b % NWARPS; every warp needs all of them)
     const T* query = static_cast<const T*>(P.query);
     const int64_t hq0 = (static_cast<int64_t>(l) * P.c.H + h) * P.g;
-    for (int b = warp; b < NB; b += NWARPS) {
-        const int row = 8 * b + r;
-        float q[KB];
-        float amax = 0.f;
-        if (row < nrows) {
-            const int64_t gr = row0 + row;
-            const int64_t i = gr / P.g;
-            const T* p = query + ((hq0 + (gr - i * P.g)) * P.q.T + B.tok0 + i) * D + c * KB;
+    constexpr int QB = (NB + NWARPS - 1) / NWARPS;
+    float q[QB][KB];
 #pragma unroll
-            for (int e = 0; e < KB; e += 2) {
-                const float2 x = load2(p + e);
-                q[e] = x.x;
-                q[e + 1] = x.y;
+    for (int i = 0; i < QB; ++i) {
+        const int row = 8 * (warp + i * NWARPS) + r;
+        if (row < nrows) {
+            const T* p = query + B.row_of(P, hq0, row) * D + c * KB;
+#pragma unroll
+            for (int x = 0; x < KB; x += 2) {
+                const float2 y = load2(p + x);
+                q[i][x] = y.x;
+                q[i][x + 1] = y.y;
             }
         } else {
 #pragma unroll
-            for (int e = 0; e < KB; ++e) q[e] = 0.f;
+            for (int x = 0; x < KB; ++x) q[i][x] = 0.f;
         }
+    }
+    int listed = list_pages(k0);
+    __syncthreads();
+    const int64_t slab = layer * P.c.n_pages * P.c.H + h;  // block of page 0
+    uint32_t kr[DEPTH][2][KW], vr[DEPTH][4][VW];
+    auto load_k = [&](int j, uint32_t (&kw)[2][KW]) {
+        const int pi = (j >> P.c.page_log2) - page0;
+        if (s_page[pi] < 0) {  // every key of the page is masked
 #pragma unroll
-        for (int e = 0; e < KB; ++e) amax = fmaxf(amax, fabsf(q[e]));
+            for (int x = 0; x < KW; ++x) kw[0][x] = kw[1][x] = 0;
+            return;
+        }
+        const int64_t blk = slab + static_cast<int64_t>(s_page[pi]) * P.c.H;
+        const uint8_t* p = P.c.code[0] + ((blk << P.c.page_log2) + (j & (P.c.page - 1))) * D;
+        load_codes<KB>(p + r * D + c * KB, kw[0]);
+        load_codes<KB>(p + (r + 8) * D + c * KB, kw[1]);
+    };
+    auto load_v = [&](int j, uint32_t (&vw)[4][VW]) {
+        const int pi = (j >> P.c.page_log2) - page0;
+        if (s_page[pi] < 0) {
+#pragma unroll
+            for (int x = 0; x < VW; ++x) vw[0][x] = vw[1][x] = vw[2][x] = vw[3][x] = 0;
+            return;
+        }
+        const int64_t blk = slab + static_cast<int64_t>(s_page[pi]) * P.c.H;
+        const uint8_t* p = P.c.code[1] + ((blk << P.c.page_log2) + (j & (P.c.page - 1))) * D + r * VB;
+        load_codes<VB>(p + (2 * c) * D, vw[0]);
+        load_codes<VB>(p + (2 * c + 1) * D, vw[1]);
+        load_codes<VB>(p + (2 * c + 8) * D, vw[2]);
+        load_codes<VB>(p + (2 * c + 9) * D, vw[3]);
+    };
+    auto first_codes = [&](int kc, int listed) {
+#pragma unroll
+        for (int i = 0; i < DEPTH; ++i) {
+            const int j = kc + (warp + i * NWARPS) * 16;
+            if (j < listed) {
+                load_k(j, kr[i]);
+                load_v(j, vr[i]);
+            }
+        }
+    };
+    first_codes(k0, listed);
+#pragma unroll
+    for (int i = 0; i < QB; ++i) {
+        const int b = warp + i * NWARPS;
+        if (b >= NB) break;
+        float amax = 0.f;
+#pragma unroll
+        for (int x = 0; x < KB; ++x) amax = fmaxf(amax, fabsf(q[i][x]));
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
         const int eq = max((__float_as_int(amax) >> 23) - 127, -100) - 13;  // amax 2^-eq in [2^13, 2^14)
         const float inv = pow2(-eq);
-        if (c == 0) sqs[row] = pow2(eq) * P.scale_log2;
+        if (c == 0) sqs[8 * b + r] = pow2(eq) * P.scale_log2;
 #pragma unroll
         for (int t = 0; t < KS; ++t)
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
-                const float a = q[4 * t + 2 * w] * inv, z = q[4 * t + 2 * w + 1] * inv;
+                const float a = q[i][4 * t + 2 * w] * inv, z = q[i][4 * t + 2 * w + 1] * inv;
                 const uint32_t hi = pack_half2(a, z);
                 sq[((b * KS + t) * 2 + w) * 32 + lane] = hi;
                 if constexpr (PARTS == 2) {
@@ -214,7 +262,7 @@ __global__ void __launch_bounds__(NT, resident_ctas(sizeof(T), D, NB)) decode_ke
         for (int j = 0; j < 2; ++j) {
             const int row = 8 * b + 2 * c + j;
             qs[b][j] = sqs[row];
-            qpos[b][j] = row < nrows ? B.pos + static_cast<int>((row0 + row) / P.g) : INT32_MIN;
+            qpos[b][j] = row < nrows ? B.pos + static_cast<int>(quotient(row0 + row, P.g)) : INT32_MIN;
         }
     uint32_t qf[NB * PARTS == 1 ? KS : 1][2];  // in registers where one fragment set serves
     if constexpr (NB * PARTS == 1) {
@@ -238,43 +286,8 @@ __global__ void __launch_bounds__(NT, resident_ctas(sizeof(T), D, NB)) decode_ke
         }
     }
 
-    const int64_t slab = layer * P.c.n_pages * P.c.H + h;  // block of page 0
-    uint32_t kw[2][KW], vw[4][VW];
-    auto load_k = [&](int j) {
-        const int pi = (j >> P.c.page_log2) - page0;
-        if (s_page[pi] < 0) {  // every key of the page is masked
-#pragma unroll
-            for (int x = 0; x < KW; ++x) kw[0][x] = kw[1][x] = 0;
-            return;
-        }
-        const int64_t blk = slab + static_cast<int64_t>(s_page[pi]) * P.c.H;
-        const uint8_t* p = P.c.code[0] + ((blk << P.c.page_log2) + (j & (P.c.page - 1))) * D;
-        load_codes<KB>(p + r * D + c * KB, kw[0]);
-        load_codes<KB>(p + (r + 8) * D + c * KB, kw[1]);
-    };
-    auto load_v = [&](int j) {
-        const int pi = (j >> P.c.page_log2) - page0;
-        if (s_page[pi] < 0) {
-#pragma unroll
-            for (int x = 0; x < VW; ++x) vw[0][x] = vw[1][x] = vw[2][x] = vw[3][x] = 0;
-            return;
-        }
-        const int64_t blk = slab + static_cast<int64_t>(s_page[pi]) * P.c.H;
-        const uint8_t* p = P.c.code[1] + ((blk << P.c.page_log2) + (j & (P.c.page - 1))) * D + r * VB;
-        load_codes<VB>(p + (2 * c) * D, vw[0]);
-        load_codes<VB>(p + (2 * c + 1) * D, vw[1]);
-        load_codes<VB>(p + (2 * c + 8) * D, vw[2]);
-        load_codes<VB>(p + (2 * c + 9) * D, vw[3]);
-    };
-    int kc = k0;  // keys [kc, listed) are listed
-    for (;;) {
-    int j = kc + 16 * warp;
-    if (j < listed) {
-        load_k(j);
-        load_v(j);
-    }
-    for (; j < listed; j += TILE_KEYS) {
-        const int jn = j + TILE_KEYS;
+    // 16 keys from j on, whose codes are in kw and vw; those of jn are asked for instead
+    auto step = [&](int j, int jn, int listed, uint32_t (&kw)[2][KW], uint32_t (&vw)[4][VW]) {
         const int pi = (j >> P.c.page_log2) - page0;
         const bool bad = s_page[pi] < 0;
         const float ks = s_ks[pi], ev = s_ev[pi];
@@ -299,7 +312,7 @@ __global__ void __launch_bounds__(NT, resident_ctas(sizeof(T), D, NB)) decode_ke
                 }
             }
         }
-        if (jn < listed) load_k(jn);
+        if (jn < listed) load_k(jn, kw);
         // scores in base 2, masked; keys r, r + 8 and query rows 2c, 2c + 1 of each row block
         const bool whole = !bad && j + 16 <= k1 && j + 15 <= B.pos_lo;
         bool raise = false;
@@ -377,13 +390,20 @@ __global__ void __launch_bounds__(NT, resident_ctas(sizeof(T), D, NB)) decode_ke
                     for (int p = 0; p < PARTS; ++p) mma16816(o[b][2 * x + y], a0, a1, a2, a3, pt[b][p][0], pt[b][p][1]);
             }
         }
-        if (jn < listed) load_v(jn);
-    }
-    if (listed >= k1) break;
-    __syncthreads();  // every warp is done with the list
-    kc = listed;
-    listed = list_pages(kc);
-    __syncthreads();
+        if (jn < listed) load_v(jn, vw);
+    };
+    for (int kc = k0;;) {  // keys [kc, listed) are listed, and the first codes asked for
+        int j = kc + 16 * warp;
+        for (; j < listed; j += DEPTH * TILE_KEYS)
+#pragma unroll
+            for (int i = 0; i < DEPTH; ++i)
+                if (j + i * TILE_KEYS < listed) step(j + i * TILE_KEYS, j + (i + DEPTH) * TILE_KEYS, listed, kr[i], vr[i]);
+        if (listed >= k1) break;
+        __syncthreads();  // every warp is done with the list
+        kc = listed;
+        listed = list_pages(kc);
+        __syncthreads();
+        first_codes(kc, listed);
     }
 
     // join the warps: outputs in units of 2^mv, sums in units of 2^m (both with the bias)
@@ -405,15 +425,15 @@ __global__ void __launch_bounds__(NT, resident_ctas(sizeof(T), D, NB)) decode_ke
     T* out = static_cast<T*>(P.out);
     auto row_of = [&](int row) { return B.row_of(P, hq0, row); };
     // the CTAs that share this unit, and this one's slot
-    const int64_t u0 = at - first, c0 = u0 / share;
-    const int pieces = static_cast<int>((u0 + tiles - 1) / share - c0) + 1;
+    const int64_t u0 = at - first, c0 = quotient(u0, share);
+    const int pieces = static_cast<int>(quotient(u0 + tiles - 1, share) - c0) + 1;
     const int64_t part0 = (2 * static_cast<int64_t>(blockIdx.x) + (first == 0)) * ROWS;
     for (int i = threadIdx.x; i < nrows * (D / 4); i += NT) {
         const int row = i / (D / 4), d4 = i % (D / 4);
         Joined z;
-#pragma unroll
+#pragma unroll 4
         for (int w = 0; w < NWARPS; ++w) z.reference(stat[w * ROWS + row]);
-#pragma unroll
+#pragma unroll 4
         for (int w = 0; w < NWARPS; ++w)
             z.add(stat[w * ROWS + row], reinterpret_cast<const float4*>(so + (w * ROWS + row) * D)[d4]);
         if (pieces == 1) {
@@ -445,49 +465,50 @@ __global__ void __launch_bounds__(NT, resident_ctas(sizeof(T), D, NB)) decode_ke
     }
 }
 
-// One instance: CTAs of it that fit an SM (s null), or its launch.
-template <typename T, int D, int NB>
+// One instance: CTAs of it that fit an SM (P null), or its launch.
+template <typename T, int D, int NB, int NWARPS>
 cudaError_t instance(const AttnParams* P, int ctas, cudaStream_t s, int* fit) {
-    constexpr size_t smem = Shape8<T, D, NB>::smem();
-    static int resident = [] {
-        int n = 0;
-        if (cudaFuncSetAttribute(decode_kernel<T, D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) !=
-                cudaSuccess ||
-            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_kernel<T, D, NB>, NT, smem) != cudaSuccess)
-            return 0;
-        return n;
-    }();
-    if (fit) *fit = resident;
-    if (!P) return cudaSuccess;
-    cudaError_t e = cudaFuncSetAttribute(decode_kernel<T, D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
+    constexpr size_t smem = Shape8<T, D, NB, NWARPS>::smem();
+    const auto kernel = decode_kernel<T, D, NB, NWARPS>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    decode_kernel<T, D, NB><<<ctas, NT, smem, s>>>(*P);
+    if (!P) {
+        static const int resident = [&] {
+            int n = 0;
+            return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, NWARPS * 32, smem) == cudaSuccess ? n : 0;
+        }();
+        *fit = resident;
+        return cudaSuccess;
+    }
+    kernel<<<ctas, NWARPS * 32, smem, s>>>(*P);
     return cudaGetLastError();
 }
 
 template <typename T, int D>
-cudaError_t instance_rows(int rows, const AttnParams* P, int ctas, cudaStream_t s, int* fit) {
+cudaError_t instance_rows(int rows, bool few, const AttnParams* P, int ctas, cudaStream_t s, int* fit) {
     switch (rows) {
-        case 8: return instance<T, D, 1>(P, ctas, s, fit);
-        case 16: return instance<T, D, 2>(P, ctas, s, fit);
-        default: return instance<T, D, 4>(P, ctas, s, fit);
+        case 8:
+            if constexpr (D >= 64)
+                if (few) return instance<T, D, 1, WARPS_FEW>(P, ctas, s, fit);
+            return instance<T, D, 1, WARPS>(P, ctas, s, fit);
+        case 16: return instance<T, D, 2, WARPS>(P, ctas, s, fit);
+        default: return instance<T, D, 4, WARPS>(P, ctas, s, fit);
     }
 }
 
 template <typename T>
-cudaError_t instance_dim(int d, int rows, const AttnParams* P, int ctas, cudaStream_t s, int* fit) {
+cudaError_t instance_dim(int d, int rows, bool few, const AttnParams* P, int ctas, cudaStream_t s, int* fit) {
     switch (d) {
-        case 16: return instance_rows<T, 16>(rows, P, ctas, s, fit);
-        case 32: return instance_rows<T, 32>(rows, P, ctas, s, fit);
-        case 64: return instance_rows<T, 64>(rows, P, ctas, s, fit);
-        default: return instance_rows<T, 128>(rows, P, ctas, s, fit);
+        case 16: return instance_rows<T, 16>(rows, few, P, ctas, s, fit);
+        case 32: return instance_rows<T, 32>(rows, few, P, ctas, s, fit);
+        case 64: return instance_rows<T, 64>(rows, few, P, ctas, s, fit);
+        default: return instance_rows<T, 128>(rows, few, P, ctas, s, fit);
     }
 }
 
-cudaError_t pick(kvb_dtype dtype, int d, int rows, const AttnParams* P, int ctas, cudaStream_t s, int* fit) {
-    return dtype == KVB_BF16 ? instance_dim<__nv_bfloat16>(d, rows, P, ctas, s, fit)
-                             : instance_dim<float>(d, rows, P, ctas, s, fit);
+cudaError_t pick(kvb_dtype dtype, int d, int rows, bool few, const AttnParams* P, int ctas, cudaStream_t s, int* fit) {
+    return dtype == KVB_BF16 ? instance_dim<__nv_bfloat16>(d, rows, few, P, ctas, s, fit)
+                             : instance_dim<float>(d, rows, few, P, ctas, s, fit);
 }
 
 }  // namespace
@@ -496,16 +517,20 @@ AttnPlan plan_attention(const Cache& c, const Seqs& q, kvb_dtype dtype, int g, i
     AttnPlan p{};
     const int64_t most = static_cast<int64_t>(q.max_tokens) * g;  // rows of one sequence and head
     const double max_kv = q.max_kv > 0 ? q.max_kv : 1;
-    p.tensor = dtype == KVB_BF16 && c.d == 128 && most > 64;
+    p.tensor = dtype == KVB_BF16 && c.d == 128 && most > 32;
     p.rows = p.tensor ? PREFILL_ROWS : most <= 8 ? 8 : most <= 16 ? 16 : 32;
     p.row_blocks = static_cast<int>((most + p.rows - 1) / p.rows);
     p.units = static_cast<int64_t>(c.n_layers) * q.n_seq * c.H * p.row_blocks;
-    // the CTAs that fit the GPU, no more than the keys give MIN_TILES tiles to
+    auto tiles = [&](int keys) { return static_cast<double>(p.units) * ((static_cast<int64_t>(max_kv) + keys - 1) / keys); };
+    // up to eight rows over few keys (less than FEW_TILES of 64 for each of four CTAs an SM):
+    // 8 warps a CTA take 128 keys in one step and the unit has few pieces to join (one token
+    // over 4096 keys: 11.5 us; with 4 warps and 4 tiles each 14.9, with 16 warps 13.0)
+    p.few = !p.tensor && p.rows == 8 && c.d >= 64 && tiles(16 * WARPS) < static_cast<double>(FEW_TILES) * 4 * num_sms;
     int fit = 1;
-    if (!p.tensor) pick(dtype, c.d, p.rows, nullptr, 0, nullptr, &fit);
-    const int tile = p.tensor ? 128 : TILE_KEYS;
-    const double most_tiles = static_cast<double>(p.units) * ((static_cast<int64_t>(max_kv) + tile - 1) / tile);
-    const double need = (most_tiles + MIN_TILES - 1) / MIN_TILES;
+    if (!p.tensor) pick(dtype, c.d, p.rows, p.few, nullptr, 0, nullptr, &fit);
+    // the CTAs that fit the GPU, no more than the keys give the least share to
+    p.min_tiles = p.few ? 1 : MIN_TILES;
+    const double need = (tiles(p.tensor ? 128 : 16 * (p.few ? WARPS_FEW : WARPS)) + p.min_tiles - 1) / p.min_tiles;
     p.ctas = num_sms * (fit > 0 ? fit : 1);
     if (need < p.ctas) p.ctas = static_cast<int>(need) < 1 ? 1 : static_cast<int>(need);
     p.slots = 2 * static_cast<int64_t>(p.ctas);
@@ -515,7 +540,7 @@ AttnPlan plan_attention(const Cache& c, const Seqs& q, kvb_dtype dtype, int g, i
 }
 
 cudaError_t launch_decode(const AttnParams& P, kvb_dtype dtype, const AttnPlan& p, cudaStream_t s) {
-    return pick(dtype, P.c.d, p.rows, &P, p.ctas, s, nullptr);
+    return pick(dtype, P.c.d, p.rows, p.few, &P, p.ctas, s, nullptr);
 }
 
 }  // namespace c8

@@ -9,7 +9,7 @@ namespace c8 {
 constexpr float BIAS = 7.f;    // weights are taken against 2^-7 of the reference
 constexpr float MARGIN = 8.f;  // a reference is raised past this much (base 2)
 constexpr float NO_REF = -3.0e38f;
-constexpr int MIN_TILES = 4;       // a CTA's least share of the line of tiles
+constexpr int MIN_TILES = 4;       // a CTA's least share of the line of tiles, but for few keys
 constexpr int PREFILL_ROWS = 256;  // rows of a unit in the tcgen05 kernel
 
 __device__ __forceinline__ float ex2(float x) {  // relative error about 2^-22
@@ -28,6 +28,13 @@ __device__ __forceinline__ void store_out(__nv_bfloat16* p, float4 v) {
 }
 __device__ __forceinline__ void store_out(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
 
+// a / b of non-negative numbers, in 32 bits where they fit (a 64-bit division is a
+// long routine, and the set-up of a CTA has several).
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+
 // A block of query rows of one sequence and head: row = token * g + head of the
 // group, so the rows of a block are close in position.
 struct RowBlock {
@@ -37,7 +44,7 @@ struct RowBlock {
     int kv_end;            // keys that its last row may see
     // index of a row in [n_layers][Hq][T]
     __device__ __forceinline__ int64_t row_of(const AttnParams& P, int64_t hq0, int row) const {
-        const int64_t gr = row0 + row, i = gr / P.g;
+        const int64_t gr = row0 + row, i = quotient(gr, P.g);
         return (hq0 + (gr - i * P.g)) * P.q.T + tok0 + i;
     }
 };
@@ -56,8 +63,8 @@ __device__ __forceinline__ RowBlock row_block(const AttnParams& P, int s, int rb
         err_set(P.err, DEV_ERR_BAD_SEQ);
         kv = P.q.max_kv;
     }
-    const int64_t pos_hi = sv.pos + (B.row0 + B.nrows - 1) / P.g;  // position of the block's last row
-    B.pos_lo = sv.pos + static_cast<int>(B.row0 / P.g);
+    const int64_t pos_hi = sv.pos + quotient(B.row0 + B.nrows - 1, P.g);  // position of the block's last row
+    B.pos_lo = sv.pos + static_cast<int>(quotient(B.row0, P.g));
     B.kv_end = static_cast<int>(max(static_cast<int64_t>(0), min(kv, pos_hi + 1)));
     return B;
 }
@@ -106,38 +113,57 @@ __device__ __forceinline__ bool line_start(const AttnParams& P, int64_t* scratch
                                            int64_t& share, int& l, int& e, int& h, int& first) {
     const int entries = P.q.n_seq * P.row_blocks;
     auto tiles_of = [&](int i) { return unit_tiles<TILE>(row_block(P, i / P.row_blocks, i % P.row_blocks, ROWS)); };
-    const int64_t mine0 = static_cast<int>(threadIdx.x) < entries ? tiles_of(threadIdx.x) : 0;
-    int64_t per_layer = mine0;
-    for (int i = threadIdx.x + NTHREADS; i < entries; i += NTHREADS) per_layer += tiles_of(i);
-    per_layer = block_sum<NTHREADS>(per_layer, scratch) * P.c.H;
-    const int64_t all = per_layer * P.c.n_layers;
-    share = max(static_cast<int64_t>(MIN_TILES), (all + gridDim.x - 1) / gridDim.x);
-    at = blockIdx.x * share;
-    if (at >= all) return false;
-    stop = min(all, at + share);
-    l = static_cast<int>(at / per_layer);
-    const int64_t want = at - l * per_layer;
-    e = -1;
-    int64_t before = 0;  // tiles of the entries before e, times H
-    for (int e0 = 0; e < 0; e0 += NTHREADS) {
-        if (e0 >= entries) return false;  // not reached while the call's arrays stay as they are
-        const int i = e0 + threadIdx.x;
-        const int64_t mine = (e0 == 0 ? mine0 : i < entries ? tiles_of(i) : 0) * P.c.H;
-        const int64_t incl = before + block_scan(mine, scratch);
-        if (threadIdx.x == 0) found->found = -1;
-        __syncthreads();
-        if (want >= incl - mine && want < incl) {
-            found->found = i;
-            found->before = incl - mine;
+    int64_t before = 0, want;  // tiles of the entries before e, times H; and up to this CTA's first
+    auto place = [&](int64_t per_layer) {
+        const int64_t all = per_layer * P.c.n_layers;
+        share = max(static_cast<int64_t>(P.min_tiles), quotient(all + gridDim.x - 1, gridDim.x));
+        at = blockIdx.x * share;
+        if (at >= all) return false;
+        stop = min(all, at + share);
+        l = static_cast<int>(quotient(at, per_layer));
+        want = at - l * per_layer;
+        return true;
+    };
+    if (entries <= 32) {  // every warp for itself: no barrier
+        const int lane = threadIdx.x & 31;
+        const int64_t mine = lane < entries ? static_cast<int64_t>(tiles_of(lane)) * P.c.H : 0;
+        int64_t incl = mine;
+#pragma unroll
+        for (int x = 1; x < 32; x <<= 1) {
+            const int64_t o = __shfl_up_sync(0xffffffffu, incl, x);
+            if (lane >= x) incl += o;
         }
-        if (threadIdx.x == NTHREADS - 1) found->total = incl;
-        __syncthreads();
-        e = found->found;
-        before = e < 0 ? found->total : found->before;
-        __syncthreads();
+        if (!place(__shfl_sync(0xffffffffu, incl, 31))) return false;
+        const uint32_t hit = __ballot_sync(0xffffffffu, want >= incl - mine && want < incl);
+        if (hit == 0) return false;  // not reached while the call's arrays stay as they are
+        e = __ffs(hit) - 1;
+        before = __shfl_sync(0xffffffffu, incl - mine, e);
+    } else {
+        const int64_t mine0 = static_cast<int>(threadIdx.x) < entries ? tiles_of(threadIdx.x) : 0;
+        int64_t per_layer = mine0;
+        for (int i = threadIdx.x + NTHREADS; i < entries; i += NTHREADS) per_layer += tiles_of(i);
+        if (!place(block_sum<NTHREADS>(per_layer, scratch) * P.c.H)) return false;
+        e = -1;
+        for (int e0 = 0; e < 0; e0 += NTHREADS) {
+            if (e0 >= entries) return false;  // likewise
+            const int i = e0 + threadIdx.x;
+            const int64_t mine = (e0 == 0 ? mine0 : i < entries ? tiles_of(i) : 0) * P.c.H;
+            const int64_t incl = before + block_scan(mine, scratch);
+            if (threadIdx.x == 0) found->found = -1;
+            __syncthreads();
+            if (want >= incl - mine && want < incl) {
+                found->found = i;
+                found->before = incl - mine;
+            }
+            if (threadIdx.x == NTHREADS - 1) found->total = incl;
+            __syncthreads();
+            e = found->found;
+            before = e < 0 ? found->total : found->before;
+            __syncthreads();
+        }
     }
     const int tiles = tiles_of(e);
-    h = static_cast<int>((want - before) / tiles);
+    h = static_cast<int>(quotient(want - before, tiles));
     first = static_cast<int>(want - before - static_cast<int64_t>(h) * tiles);
     return true;
 }
