@@ -71,6 +71,7 @@ struct AttnPlan {
     int ctas;
     int64_t units;  // (layer, sequence, row block, head)
     int64_t slots;  // partial results: two a CTA
+    double tiles;   // of all units, at most
     size_t counter_bytes, partial_bytes;
 };
 AttnPlan plan_attention(const Cache& c, const Seqs& q, kvb_dtype dtype, int g, int num_sms);

@@ -162,8 +162,10 @@ kvb_status kvb_cache8_attention(kvb_ctx* c, const kvb_cache8* cache, const kvb_s
     a.scale_log2 = static_cast<float>((scale > 0.0 ? scale : 1.0 / std::sqrt(static_cast<double>(c->d))) * 1.4426950408889634);
     a.err = call_err(c);
     const c8::AttnPlan p = c8::plan_attention(a.c, a.q, dtype, a.g, c->num_sms);
-    if (p.units > 0x7fffffffLL)
-        return fail(KVB_ERR_UNSUPPORTED, "kvb_cache8_attention: too many query rows, sequences or layers in one call");
+    // the kernels count rows of a sequence, units and tiles of 64 or 128 keys in 32 bits
+    constexpr double most = 1 << 30;
+    if (static_cast<double>(p.units) > most || p.tiles > most || static_cast<double>(a.q.max_tokens) * a.g > most)
+        return fail(KVB_ERR_UNSUPPORTED, "kvb_cache8_attention: more query rows, sequences, layers or keys than one call takes (2^30 tiles of 64 keys)");
     if ((st = ensure_attn_ws(c, p, s)) != KVB_OK) return st;
     a.counters = static_cast<int*>(c->attn_ws);
     a.partial = reinterpret_cast<float*>(static_cast<char*>(c->attn_ws) + c->attn_ws_counters);

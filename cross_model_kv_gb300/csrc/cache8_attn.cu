@@ -40,7 +40,7 @@ namespace c8 {
 namespace {
 
 constexpr int WARPS = 4;        // of a CTA; 16 keys each make its step, a tile of the line
-constexpr int WARPS_FEW = 8;    // where there are few keys: two CTAs an SM, their step 128 keys
+constexpr int WARPS_FEW = 8;    // where there are few keys: one CTA an SM, its step 128 keys
 constexpr int FEW_TILES = 4;
 constexpr int LIST_PAGES = 256;         // pages listed in shared memory at a time
 
@@ -105,7 +105,7 @@ struct Shape8 {
 };
 
 template <typename T, int D, int NB, int NWARPS>
-__global__ void __launch_bounds__(NWARPS * 32, NWARPS == WARPS ? resident_ctas(sizeof(T), D, NB) : 2)
+__global__ void __launch_bounds__(NWARPS * 32, NWARPS == WARPS ? resident_ctas(sizeof(T), D, NB) : 1)
     decode_kernel(const __grid_constant__ AttnParams P) {
     constexpr int NT = NWARPS * 32, TILE_KEYS = 16 * NWARPS;
     constexpr int DEPTH = D <= 64 ? 2 : 1;  // 16-key steps of a warp in flight: 4 KB at d 128 and 64
@@ -123,12 +123,12 @@ __global__ void __launch_bounds__(NWARPS * 32, NWARPS == WARPS ? resident_ctas(s
     float* s_ev = s_ks + LIST_PAGES + 1;                              // exponent of the value scale
     __shared__ int s_last;
     __shared__ LineStart s_start;
-    __shared__ int64_t s_scan[NWARPS];
+    __shared__ int s_scan[NWARPS];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = lane >> 2, c = lane & 3;
 
-    int64_t at, stop, share;
+    int at, stop, share;
     int l, e, h, first;
     if (!line_start<ROWS, TILE_KEYS, NT>(P, s_scan, &s_start, at, stop, share, l, e, h, first)) return;
     const int entries = P.q.n_seq * P.row_blocks;
@@ -139,10 +139,10 @@ __global__ void __launch_bounds__(NWARPS * 32, NWARPS == WARPS ? resident_ctas(s
     // one unit, or a piece of one, after another
     for (;;) {
     const int s = e / P.row_blocks;
-    const int last = static_cast<int>(min(static_cast<int64_t>(tiles), first + (stop - at)));  // tiles [first, last)
+    const int last = min(tiles, first + (stop - at));  // tiles [first, last)
     const int k0 = first * TILE_KEYS, k1 = min(B.kv_end, last * TILE_KEYS);
     const int nrows = B.nrows;
-    const int64_t row0 = B.row0;
+    const int row0 = B.row0;
     const int64_t unit = (static_cast<int64_t>(l) * entries + e) * P.c.H + h;
     const int64_t layer = static_cast<int64_t>(P.c.l_begin) + l;
 
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(NWARPS * 32, NWARPS == WARPS ? resident_ctas(s
         for (int j = 0; j < 2; ++j) {
             const int row = 8 * b + 2 * c + j;
             qs[b][j] = sqs[row];
-            qpos[b][j] = row < nrows ? B.pos + static_cast<int>(quotient(row0 + row, P.g)) : INT32_MIN;
+            qpos[b][j] = row < nrows ? B.pos + (row0 + row) / P.g : INT32_MIN;
         }
     uint32_t qf[NB * PARTS == 1 ? KS : 1][2];  // in registers where one fragment set serves
     if constexpr (NB * PARTS == 1) {
@@ -425,8 +425,8 @@ __global__ void __launch_bounds__(NWARPS * 32, NWARPS == WARPS ? resident_ctas(s
     T* out = static_cast<T*>(P.out);
     auto row_of = [&](int row) { return B.row_of(P, hq0, row); };
     // the CTAs that share this unit, and this one's slot
-    const int64_t u0 = at - first, c0 = quotient(u0, share);
-    const int pieces = static_cast<int>(quotient(u0 + tiles - 1, share) - c0) + 1;
+    const int u0 = at - first, c0 = u0 / share;
+    const int pieces = (u0 + tiles - 1) / share - c0 + 1;
     const int64_t part0 = (2 * static_cast<int64_t>(blockIdx.x) + (first == 0)) * ROWS;
     for (int i = threadIdx.x; i < nrows * (D / 4); i += NT) {
         const int row = i / (D / 4), d4 = i % (D / 4);
@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(NWARPS * 32, NWARPS == WARPS ? resident_ctas(s
         }
     }
     if (pieces > 1)
-        join_splits<T, D, ROWS, NT>(P, B, Pieces{pieces, 2 * c0 + 1, 2 * c0 + 2, 2}, unit, hq0, &s_last, so, NWARPS * ROWS * D);
+        join_splits<T, D, ROWS, NT>(P, B, Pieces{pieces, c0}, unit, hq0, &s_last, so, NWARPS * ROWS * D);
 
     at += last - first;
     if (at >= stop) return;
@@ -533,6 +533,7 @@ AttnPlan plan_attention(const Cache& c, const Seqs& q, kvb_dtype dtype, int g, i
     const double need = (tiles(p.tensor ? 128 : 16 * (p.few ? WARPS_FEW : WARPS)) + p.min_tiles - 1) / p.min_tiles;
     p.ctas = num_sms * (fit > 0 ? fit : 1);
     if (need < p.ctas) p.ctas = static_cast<int>(need) < 1 ? 1 : static_cast<int>(need);
+    p.tiles = tiles(p.tensor ? 128 : 64);
     p.slots = 2 * static_cast<int64_t>(p.ctas);
     p.counter_bytes = (static_cast<size_t>(p.units) * sizeof(int) + 255) / 256 * 256;
     p.partial_bytes = static_cast<size_t>(p.slots) * p.rows * (c.d + 4) * sizeof(float);

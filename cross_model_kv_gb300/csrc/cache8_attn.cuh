@@ -28,23 +28,16 @@ __device__ __forceinline__ void store_out(__nv_bfloat16* p, float4 v) {
 }
 __device__ __forceinline__ void store_out(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
 
-// a / b of non-negative numbers, in 32 bits where they fit (a 64-bit division is a
-// long routine, and the set-up of a CTA has several).
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
-    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-    return a / b;
-}
-
 // A block of query rows of one sequence and head: row = token * g + head of the
 // group, so the rows of a block are close in position.
 struct RowBlock {
-    int64_t row0;
+    int row0;
     int nrows, tok0, pos;  // nrows 0: the sequence has no such rows
     int pos_lo;            // position of the block's first row
     int kv_end;            // keys that its last row may see
     // index of a row in [n_layers][Hq][T]
     __device__ __forceinline__ int64_t row_of(const AttnParams& P, int64_t hq0, int row) const {
-        const int64_t gr = row0 + row, i = quotient(gr, P.g);
+        const int gr = row0 + row, i = gr / P.g;
         return (hq0 + (gr - i * P.g)) * P.q.T + tok0 + i;
     }
 };
@@ -52,10 +45,10 @@ struct RowBlock {
 __device__ __forceinline__ RowBlock row_block(const AttnParams& P, int s, int rb, int rows) {
     RowBlock B{};
     const SeqView sv = seq_view(P.q, s, P.err);
-    const int64_t total = static_cast<int64_t>(sv.n) * P.g;
-    B.row0 = static_cast<int64_t>(rb) * rows;
+    const int total = sv.n * P.g;  // and rows of a call, and tiles of its line, stay below 2^30
+    B.row0 = rb * rows;
     if (B.row0 >= total) return B;
-    B.nrows = static_cast<int>(min(static_cast<int64_t>(rows), total - B.row0));
+    B.nrows = min(rows, total - B.row0);
     B.tok0 = sv.tok0;
     B.pos = sv.pos;
     int64_t kv = P.q.kv_len ? static_cast<int64_t>(__ldg(P.q.kv_len + s)) : static_cast<int64_t>(sv.pos) + sv.n;
@@ -63,8 +56,8 @@ __device__ __forceinline__ RowBlock row_block(const AttnParams& P, int s, int rb
         err_set(P.err, DEV_ERR_BAD_SEQ);
         kv = P.q.max_kv;
     }
-    const int64_t pos_hi = sv.pos + quotient(B.row0 + B.nrows - 1, P.g);  // position of the block's last row
-    B.pos_lo = sv.pos + static_cast<int>(quotient(B.row0, P.g));
+    const int64_t pos_hi = sv.pos + (B.row0 + B.nrows - 1) / P.g;  // position of the block's last row
+    B.pos_lo = sv.pos + B.row0 / P.g;
     B.kv_end = static_cast<int>(max(static_cast<int64_t>(0), min(kv, pos_hi + 1)));
     return B;
 }
@@ -76,11 +69,11 @@ __device__ __forceinline__ int unit_tiles(const RowBlock& B) {
 }
 
 // Inclusive scan / sum over the CTA's NTHREADS threads (scratch: one value a warp).
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* scratch) {
+__device__ __forceinline__ int block_scan(int v, int* scratch) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int x = 1; x < 32; x <<= 1) {
-        const int64_t o = __shfl_up_sync(0xffffffffu, v, x);
+        const int o = __shfl_up_sync(0xffffffffu, v, x);
         if (lane >= x) v += o;
     }
     __syncthreads();  // scratch is free
@@ -90,7 +83,7 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* scratch) {
     return v;
 }
 template <int NTHREADS>
-__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* scratch) {
+__device__ __forceinline__ int block_sum(int v, int* scratch) {
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
     if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
@@ -101,36 +94,35 @@ __device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* scratch) {
 }
 
 struct LineStart {
-    int found;
-    int64_t before, total;
+    int found, before, total;
 };
 
 // The units' tiles form one line: layer, then entry (sequence, row block), then
 // head.  This CTA takes tiles [at, stop) of it, the first of them tile `first` of unit
 // (l, e, h); share is every CTA's number.  false: nothing is left for this CTA.
 template <int ROWS, int TILE, int NTHREADS>
-__device__ __forceinline__ bool line_start(const AttnParams& P, int64_t* scratch, LineStart* found, int64_t& at, int64_t& stop,
-                                           int64_t& share, int& l, int& e, int& h, int& first) {
+__device__ __forceinline__ bool line_start(const AttnParams& P, int* scratch, LineStart* found, int& at, int& stop, int& share,
+                                           int& l, int& e, int& h, int& first) {
     const int entries = P.q.n_seq * P.row_blocks;
     auto tiles_of = [&](int i) { return unit_tiles<TILE>(row_block(P, i / P.row_blocks, i % P.row_blocks, ROWS)); };
-    int64_t before = 0, want;  // tiles of the entries before e, times H; and up to this CTA's first
-    auto place = [&](int64_t per_layer) {
-        const int64_t all = per_layer * P.c.n_layers;
-        share = max(static_cast<int64_t>(P.min_tiles), quotient(all + gridDim.x - 1, gridDim.x));
-        at = blockIdx.x * share;
+    int before = 0, want;  // tiles of the entries before e, times H; and up to this CTA's first
+    auto place = [&](int per_layer) {
+        const int all = per_layer * P.c.n_layers;
+        share = max(P.min_tiles, (all + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
+        at = static_cast<int>(blockIdx.x) * share;
         if (at >= all) return false;
         stop = min(all, at + share);
-        l = static_cast<int>(quotient(at, per_layer));
+        l = at / per_layer;
         want = at - l * per_layer;
         return true;
     };
     if (entries <= 32) {  // every warp for itself: no barrier
         const int lane = threadIdx.x & 31;
-        const int64_t mine = lane < entries ? static_cast<int64_t>(tiles_of(lane)) * P.c.H : 0;
-        int64_t incl = mine;
+        const int mine = lane < entries ? tiles_of(lane) * P.c.H : 0;
+        int incl = mine;
 #pragma unroll
         for (int x = 1; x < 32; x <<= 1) {
-            const int64_t o = __shfl_up_sync(0xffffffffu, incl, x);
+            const int o = __shfl_up_sync(0xffffffffu, incl, x);
             if (lane >= x) incl += o;
         }
         if (!place(__shfl_sync(0xffffffffu, incl, 31))) return false;
@@ -139,16 +131,16 @@ __device__ __forceinline__ bool line_start(const AttnParams& P, int64_t* scratch
         e = __ffs(hit) - 1;
         before = __shfl_sync(0xffffffffu, incl - mine, e);
     } else {
-        const int64_t mine0 = static_cast<int>(threadIdx.x) < entries ? tiles_of(threadIdx.x) : 0;
-        int64_t per_layer = mine0;
+        const int mine0 = static_cast<int>(threadIdx.x) < entries ? tiles_of(threadIdx.x) : 0;
+        int per_layer = mine0;
         for (int i = threadIdx.x + NTHREADS; i < entries; i += NTHREADS) per_layer += tiles_of(i);
         if (!place(block_sum<NTHREADS>(per_layer, scratch) * P.c.H)) return false;
         e = -1;
         for (int e0 = 0; e < 0; e0 += NTHREADS) {
             if (e0 >= entries) return false;  // likewise
             const int i = e0 + threadIdx.x;
-            const int64_t mine = (e0 == 0 ? mine0 : i < entries ? tiles_of(i) : 0) * P.c.H;
-            const int64_t incl = before + block_scan(mine, scratch);
+            const int mine = (e0 == 0 ? mine0 : i < entries ? tiles_of(i) : 0) * P.c.H;
+            const int incl = before + block_scan(mine, scratch);
             if (threadIdx.x == 0) found->found = -1;
             __syncthreads();
             if (want >= incl - mine && want < incl) {
@@ -163,17 +155,17 @@ __device__ __forceinline__ bool line_start(const AttnParams& P, int64_t* scratch
         }
     }
     const int tiles = tiles_of(e);
-    h = static_cast<int>(quotient(want - before, tiles));
-    first = static_cast<int>(want - before - static_cast<int64_t>(h) * tiles);
+    h = (want - before) / tiles;
+    first = want - before - h * tiles;
     return true;
 }
 
-// The partial results of one unit, in the order of its keys: slot(i), i < n.
+// The partial results of one unit, in the order of its keys: CTAs c0 .. c0 + n - 1
+// share it; a CTA's slot is 2c for the piece that it begins with and 2c + 1 for one that
+// it ends with.
 struct Pieces {
-    int n;
-    int64_t first, next;
-    int stride;
-    __device__ __forceinline__ int64_t slot(int i) const { return i == 0 ? first : next + static_cast<int64_t>(i - 1) * stride; }
+    int n, c0;
+    __device__ __forceinline__ int64_t slot(int i) const { return i == 0 ? 2 * c0 + 1 : 2 * (c0 + i); }
 };
 
 // Parts of one row's result, each with its references: first every part's

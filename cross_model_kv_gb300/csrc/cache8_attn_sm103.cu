@@ -161,7 +161,7 @@ struct Segment {
 
 // The CTA's place in the line of tiles.
 struct Walk {
-    int64_t at, stop, share;
+    int at, stop, share;
     int e, h, l, first;
 };
 
@@ -173,7 +173,7 @@ struct Smem {
     int abort, last;
     int more[2];        // a segment follows (by parity of its number)
     Segment seg[2];
-    int64_t scan[NUM_THREADS / 32];
+    int scan[NUM_THREADS / 32];
     LineStart start;
     Walk walk;
     alignas(16) TileInfo info[INFO_RING];
@@ -228,8 +228,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
             M.more[i] = 0;
             return;
         }
-        const int last = static_cast<int>(min(static_cast<int64_t>(tiles), W.first + (W.stop - W.at)));
-        const int64_t u0 = W.at - W.first, c0 = quotient(u0, W.share);
+        const int last = min(tiles, W.first + (W.stop - W.at));
+        const int u0 = W.at - W.first, c0 = u0 / W.share;
         g.B = B;
         g.s = W.e / P.row_blocks;
         g.l = W.l;
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
         g.k0 = W.first * TK;
         g.k1 = min(B.kv_end, last * TK);
         g.unit = (static_cast<int64_t>(W.l) * entries + W.e) * P.c.H + W.h;
-        g.pieces = Pieces{static_cast<int>(quotient(u0 + tiles - 1, W.share) - c0) + 1, 2 * c0 + 1, 2 * c0 + 2, 2};
+        g.pieces = Pieces{(u0 + tiles - 1) / W.share - c0 + 1, c0};
         g.whole = g.pieces.n == 1;
         g.slot = 2 * static_cast<int64_t>(blockIdx.x) + (W.first == 0);
         M.more[i] = 1;
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
                 mbar_arrive(&M.q_full[x]);
             }
             // keys below `see` are visible to this row
-            const int see = valid ? min(k1, G.B.pos + static_cast<int>(quotient(G.B.row0 + brow, P.g)) + 1) : 0;
+            const int see = valid ? min(k1, G.B.pos + (G.B.row0 + brow) / P.g + 1) : 0;
             for (int u = 0; u < nsteps; ++u) {
                 const uint32_t gt = base + (u >> 1), ring = gt & (INFO_RING - 1);
                 const int hf = u & 1;
