@@ -87,6 +87,17 @@ __device__ __forceinline__ void err_set(const Err& e, int code) {
     }
 }
 
+// The checked build's index checks (KVB_IN_BOUNDS) on this error record.
+__device__ __forceinline__ bool check_bounds(const Err& e, int64_t first, int64_t count, int64_t size) {
+    if (first >= 0 && count >= 0 && first + count <= size) return true;
+    err_set(e, DEV_ERR_BOUNDS);
+    return false;
+}
+// Blocks (layer, page, head) that a call may touch.
+__device__ __forceinline__ int64_t blocks_of(const Cache& c) {
+    return (static_cast<int64_t>(c.l_begin) + c.n_layers) * c.n_pages * c.H;
+}
+
 // 2^e, -126 <= e <= 127.
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
 // e of a normal power of two.

@@ -158,8 +158,9 @@ __global__ void __launch_bounds__(NWARPS * 32, NWARPS == WARPS ? resident_ctas(s
                 err_set(P.err, DEV_ERR_BAD_SEQ);
                 pid = -1;
             }
-            s_page[i] = pid;
             const int64_t b = (layer * P.c.n_pages + pid) * P.c.H + h;
+            if (pid >= 0 && !KVB_IN_BOUNDS(P.err, b, 1, blocks_of(P.c))) pid = -1;
+            s_page[i] = pid;
             s_ks[i] = pid < 0 ? 1.f : __ldg(P.c.scale[0] + b);
             s_ev[i] = pid < 0 ? 0.f : static_cast<float>(exponent_of(__ldg(P.c.scale[1] + b)));
         }
@@ -174,7 +175,7 @@ __global__ void __launch_bounds__(NWARPS * 32, NWARPS == WARPS ? resident_ctas(s
 #pragma unroll
     for (int i = 0; i < QB; ++i) {
         const int row = 8 * (warp + i * NWARPS) + r;
-        if (row < nrows) {
+        if (row < nrows && KVB_IN_BOUNDS(P.err, B.row_of(P, hq0, row), 1, rows_of(P))) {
             const T* p = query + B.row_of(P, hq0, row) * D + c * KB;
 #pragma unroll
             for (int x = 0; x < KB; x += 2) {
@@ -430,6 +431,7 @@ __global__ void __launch_bounds__(NWARPS * 32, NWARPS == WARPS ? resident_ctas(s
     const int64_t part0 = (2 * static_cast<int64_t>(blockIdx.x) + (first == 0)) * ROWS;
     for (int i = threadIdx.x; i < nrows * (D / 4); i += NT) {
         const int row = i / (D / 4), d4 = i % (D / 4);
+        if (!KVB_IN_BOUNDS(P.err, row_of(row), 1, rows_of(P))) continue;
         Joined z;
 #pragma unroll 4
         for (int w = 0; w < NWARPS; ++w) z.reference(stat[w * ROWS + row]);

@@ -42,6 +42,11 @@ struct RowBlock {
     }
 };
 
+// Rows of q, out and lse.
+__device__ __forceinline__ int64_t rows_of(const AttnParams& P) {
+    return static_cast<int64_t>(P.c.n_layers) * P.c.H * P.g * P.q.T;
+}
+
 __device__ __forceinline__ RowBlock row_block(const AttnParams& P, int s, int rb, int rows) {
     RowBlock B{};
     const SeqView sv = seq_view(P.q, s, P.err);
@@ -261,6 +266,7 @@ __device__ __forceinline__ void join_splits(const AttnParams& P, const RowBlock&
             z.weigh(listed ? weight[row * active + i] : ex2(stat(row, i).y - z.mv), 
                     __ldcg(reinterpret_cast<const float4*>(P.partial + (pieces.slot(i) * ROWS + row) * D) + d4));
         const int64_t o = B.row_of(P, hq0, row);
+        if (!KVB_IN_BOUNDS(P.err, o, 1, rows_of(P))) continue;
         store_out(out + o * D + 4 * d4, z.output());
         if (d4 == 0 && P.lse) P.lse[o] = z.lse();
     }

@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
             const int k0 = G.k0, k1 = G.k1;
             const int nsteps = TR * x < G.B.nrows ? (k1 - k0 + SK - 1) / SK : 0;
             const int brow = TR * x + row;
-            const bool valid = brow < G.B.nrows;
+            const bool valid = brow < G.B.nrows && KVB_IN_BOUNDS(P.err, G.B.row_of(P, (static_cast<int64_t>(G.l) * P.c.H + G.h) * P.g, brow), 1, rows_of(P));
             // worked out where it is used: kept, it would cost the score loop's registers
             auto first_head = [&] { return (static_cast<int64_t>(G.l) * P.c.H + G.h) * P.g; };
             auto row_index = [&] { return valid ? G.B.row_of(P, first_head(), brow) : 0; };  // in [n_layers][Hq][T]
@@ -508,7 +508,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
                 for (int i = 0; i < 4; ++i) {
                     const int j = k0 + t * TK + 32 * i + r32;
                     // slots past the last visible key may hold anything: not read
-                    const bool have = j < k1 && pid[i] >= 0 && pid[i] < P.c.n_pages;
+                    const bool have = j < k1 && pid[i] >= 0 && pid[i] < P.c.n_pages &&
+                                      KVB_IN_BOUNDS(P.err, block0 + static_cast<int64_t>(pid[i]) * P.c.H, 1, blocks_of(P.c));
                     u[i] = load16_if(from[kv] + static_cast<uint64_t>(static_cast<uint32_t>(pid[i])) * page_bytes + (j & pm) * HD, have);
                 }
             };

@@ -119,7 +119,10 @@ __device__ __forceinline__ bool place_of(const RwParams& P, const Item& it, bool
     const bool bad = pid < 0 || pid >= P.c.n_pages || sv.pos < 0;
     if (bad && report) err_set(P.err, DEV_ERR_BAD_SEQ);
     o.block = bad ? -1 : ((static_cast<int64_t>(P.c.l_begin) + it.l) * P.c.n_pages + pid) * P.c.H + it.h;
-    return true;
+    // every access of the item lies in these rows, and in these slots of this block
+    return KVB_IN_BOUNDS(P.err, o.row, o.m, static_cast<int64_t>(P.c.n_layers) * P.c.H * P.q.T) &&
+           KVB_IN_BOUNDS(P.err, max(o.block, static_cast<int64_t>(0)), 1, blocks_of(P.c)) &&
+           KVB_IN_BOUNDS(P.err, o.lo, o.m, P.c.page);
 }
 
 // One page's K and V blocks per group of GS threads.  Their new values stay in

@@ -106,7 +106,7 @@ __device__ __forceinline__ bool check_bounds(const DevErr& e, int64_t first, int
     return false;
 }
 #if defined(KVB_CHECK_BOUNDS) && KVB_CHECK_BOUNDS
-#define KVB_IN_BOUNDS(err, first, count, size) ::kvb::check_bounds((err), (first), (count), (size))
+#define KVB_IN_BOUNDS(err, first, count, size) check_bounds((err), (first), (count), (size))
 #else  // the arguments are named (not evaluated) so that their variables count as used
 #define KVB_IN_BOUNDS(err, first, count, size) \
     ((void)sizeof(err), (void)sizeof(first), (void)sizeof(count), (void)sizeof(size), true)
