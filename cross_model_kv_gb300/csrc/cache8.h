@@ -58,6 +58,7 @@ struct AttnParams {
     int min_tiles;      // a CTA's least share of the line of tiles
     float scale_log2;   // scale * log2(e)
     int* counters;      // [units], 0 before and after a call
+    int2* shared_by;    // [units], tcgen05 kernel: CTAs that share the unit, the first of them
     float* partial;     // [slots][rows][d] outputs in units of 2^mv
     float4* part_stat;  // [slots][rows] (m, mv, sum, -)
     Err err;
@@ -72,7 +73,7 @@ struct AttnPlan {
     int64_t units;  // (layer, sequence, row block, head)
     int64_t slots;  // partial results: two a CTA
     double tiles;   // of all units, at most
-    size_t counter_bytes, partial_bytes;
+    size_t counter_bytes, partial_bytes, unit_bytes;
 };
 AttnPlan plan_attention(const Cache& c, const Seqs& q, kvb_dtype dtype, int g, int num_sms);
 cudaError_t launch_decode(const AttnParams& P, kvb_dtype dtype, const AttnPlan& p, cudaStream_t s);

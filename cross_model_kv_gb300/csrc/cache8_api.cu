@@ -79,10 +79,10 @@ bool too_many_blocks(const c8::Cache& c, const c8::Seqs& q) {
     return items * q.n_seq * c.H * c.n_layers > 2147483647.0;
 }
 
-// Counters (zeroed once; every call leaves them at zero) followed by the partial outputs.
+// Counters (zeroed once; every call leaves them at zero), then the partial outputs and what is noted of units.
 kvb_status ensure_attn_ws(kvb_ctx* c, const c8::AttnPlan& p, cudaStream_t s) {
-    const size_t need = p.counter_bytes + p.partial_bytes;
-    if (need <= c->attn_ws_bytes && p.counter_bytes <= c->attn_ws_counters) return KVB_OK;
+    const size_t rest = p.partial_bytes + p.unit_bytes;
+    if (p.counter_bytes <= c->attn_ws_counters && c->attn_ws_counters + rest <= c->attn_ws_bytes) return KVB_OK;
     cudaError_t e;
     if (c->attn_ws) {
         if ((e = cudaDeviceSynchronize()) != cudaSuccess) return cuda_fail(e, "sync before growing the attention workspace");
@@ -92,7 +92,7 @@ kvb_status ensure_attn_ws(kvb_ctx* c, const c8::AttnPlan& p, cudaStream_t s) {
     }
     // room for counters of larger calls to come, so that a batch that grows by a sequence does not reallocate
     const size_t counters = p.counter_bytes < 65536 ? 65536 : 2 * p.counter_bytes;
-    const size_t bytes = counters + p.partial_bytes + p.partial_bytes / 4;
+    const size_t bytes = counters + rest + rest / 4;
     if ((e = cudaMalloc(&c->attn_ws, bytes)) != cudaSuccess) return cuda_fail(e, "cudaMalloc attention workspace");
     if ((e = cudaMemset(c->attn_ws, 0, counters)) != cudaSuccess || (e = cudaStreamSynchronize(0)) != cudaSuccess)
         return cuda_fail(e, "zeroing the attention workspace");
@@ -167,7 +167,8 @@ kvb_status kvb_cache8_attention(kvb_ctx* c, const kvb_cache8* cache, const kvb_s
     if (static_cast<double>(p.units) > most || p.tiles > most || static_cast<double>(a.q.max_tokens) * a.g > most)
         return fail(KVB_ERR_UNSUPPORTED, "kvb_cache8_attention: more query rows, sequences, layers or keys than one call takes (2^30 tiles of 64 keys)");
     if ((st = ensure_attn_ws(c, p, s)) != KVB_OK) return st;
-    a.counters = static_cast<int*>(c->attn_ws);
+    a.counters = static_cast<int*>(c->attn_ws);  // the tcgen05 kernel has no use for them
+    a.shared_by = reinterpret_cast<int2*>(static_cast<char*>(c->attn_ws) + c->attn_ws_counters + p.partial_bytes);
     a.partial = reinterpret_cast<float*>(static_cast<char*>(c->attn_ws) + c->attn_ws_counters);
     a.part_stat = reinterpret_cast<float4*>(a.partial + static_cast<size_t>(p.slots) * p.rows * c->d);
     a.row_blocks = p.row_blocks;

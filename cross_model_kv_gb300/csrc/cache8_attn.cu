@@ -537,7 +537,8 @@ AttnPlan plan_attention(const Cache& c, const Seqs& q, kvb_dtype dtype, int g, i
     if (need < p.ctas) p.ctas = static_cast<int>(need) < 1 ? 1 : static_cast<int>(need);
     p.tiles = tiles(p.tensor ? 128 : 64);
     p.slots = 2 * static_cast<int64_t>(p.ctas);
-    p.counter_bytes = (static_cast<size_t>(p.units) * sizeof(int) + 255) / 256 * 256;
+    p.counter_bytes = p.tensor ? 0 : (static_cast<size_t>(p.units) * sizeof(int) + 255) / 256 * 256;
+    p.unit_bytes = p.tensor ? static_cast<size_t>(p.units) * sizeof(int2) : 0;
     p.partial_bytes = static_cast<size_t>(p.slots) * p.rows * (c.d + 4) * sizeof(float);
     return p;
 }

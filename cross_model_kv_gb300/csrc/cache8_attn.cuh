@@ -204,26 +204,21 @@ struct Joined {
 };
 
 // After a piece of a unit is written: the last CTA of the unit to arrive joins
-// the pieces, in order.  Called by the CTA's first NTHREADS threads
-// (SOME: there are others, so they meet at named barrier 9); buf: shared memory of
+// the pieces, in order.  Called by all NTHREADS threads; buf: shared memory of
 // `cap` floats, free once they have met.  A warp takes a row's references and sum, the
 // weights of all chunks go to shared memory, then each thread adds its columns with
 // its loads in flight together: 64 pieces one after another took 15 us.
-template <typename T, int D, int ROWS, int NTHREADS, bool SOME = false>
+template <typename T, int D, int ROWS, int NTHREADS>
 __device__ __forceinline__ void join_splits(const AttnParams& P, const RowBlock& B, const Pieces& pieces, int64_t unit, int64_t hq0, int* s_last,
                                             float* buf, int cap) {
-    auto meet = [] {
-        if constexpr (SOME) named_bar_sync(9, NTHREADS);
-        else __syncthreads();
-    };
     __threadfence();
-    meet();
+    __syncthreads();
     if (threadIdx.x == 0) {
         const int n = atomicAdd(P.counters + unit, 1);
         *s_last = n == pieces.n - 1;
         if (n == pieces.n - 1) P.counters[unit] = 0;
     }
-    meet();
+    __syncthreads();
     if (!*s_last) return;
     __threadfence();
     const int active = pieces.n, lane = threadIdx.x & 31;
@@ -252,7 +247,7 @@ __device__ __forceinline__ void join_splits(const AttnParams& P, const RowBlock&
         for (int x = 1; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
         if (lane == 0) ref[row] = make_float4(m, mv, sum, 0.f);
     }
-    meet();
+    __syncthreads();
     T* out = static_cast<T*>(P.out);
     for (int e = threadIdx.x; e < B.nrows * (D / 4); e += NTHREADS) {
         const int row = e / (D / 4), d4 = e % (D / 4);

@@ -170,7 +170,7 @@ struct Smem {
     uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // [tile][buffer]
     uint64_t q_full[2], drain[4], info_full[INFO_RING];
     uint32_t tmem;
-    int abort, last;
+    int abort;
     int more[2];        // a segment follows (by parity of its number)
     Segment seg[2];
     int scan[NUM_THREADS / 32];
@@ -239,6 +239,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
         g.unit = (static_cast<int64_t>(W.l) * entries + W.e) * P.c.H + W.h;
         g.pieces = Pieces{(u0 + tiles - 1) / W.share - c0 + 1, c0};
         g.whole = g.pieces.n == 1;
+        P.shared_by[g.unit] = make_int2(g.pieces.n, g.pieces.c0);  // every CTA of the unit the same
         g.slot = 2 * static_cast<int64_t>(blockIdx.x) + (W.first == 0);
         M.more[i] = 1;
         W.at += last - W.first;
@@ -288,8 +289,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
             const int brow = TR * x + row;
             const bool valid = brow < G.B.nrows && KVB_IN_BOUNDS(P.err, G.B.row_of(P, (static_cast<int64_t>(G.l) * P.c.H + G.h) * P.g, brow), 1, rows_of(P));
             // worked out where it is used: kept, it would cost the score loop's registers
-            auto first_head = [&] { return (static_cast<int64_t>(G.l) * P.c.H + G.h) * P.g; };
-            auto row_index = [&] { return valid ? G.B.row_of(P, first_head(), brow) : 0; };  // in [n_layers][Hq][T]
+            auto row_index = [&] { return valid ? G.B.row_of(P, (static_cast<int64_t>(G.l) * P.c.H + G.h) * P.g, brow) : 0; };  // in [n_layers][Hq][T]
             float m = NO_REF, mv = NO_REF, sum = 0.f;
             // the row as fp16 under a power of two: largest element in [2^13, 2^14)
             float qs;
@@ -471,10 +471,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
                 if (!G.whole) P.part_stat[part] = make_float4(m, mv, sum, 0.f);
                 else if (P.lse) P.lse[out_row] = sum == 0.f ? -INFINITY : (m - BIAS + log2f(sum)) * 0.693147180559945f;
             }
-            // the queries are idle: every product of the segment has completed
-            if (!G.whole)
-                join_splits<__nv_bfloat16, HD, ROWS, SOFT, true>(P, G.B, G.pieces, G.unit, first_head(), &M.last, reinterpret_cast<float*>(sQ),
-                                                                 2 * TILE / 4);
             tc_fence_before();
             __syncthreads();  // the segment is done, the next one worked out
         }
@@ -660,12 +656,48 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
     if (threadIdx.x == 0 && *abort_flag) *reinterpret_cast<volatile int*>(P.err.mirror) = DEV_ERR_TIMEOUT;
 }
 
+// Joins the pieces of the units that several CTAs shared, in the order of their keys,
+// a warp a row: 256 rows of a unit are too many for its last CTA, which was 20 to
+// 30 us behind the others (1024 tokens over 16K: 570 us with that, see the table of cases).
+constexpr int JOIN_ROWS = 32;  // of a CTA
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnParams P) {
+    constexpr int PER = ROWS / JOIN_ROWS;
+    const int unit = blockIdx.x / PER, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int entries = P.q.n_seq * P.row_blocks;
+    const int h = unit % P.c.H, e = unit / P.c.H % entries, l = unit / P.c.H / entries;
+    const RowBlock B = row_block(P, e / P.row_blocks, e % P.row_blocks, ROWS);
+    const int row0 = (blockIdx.x % PER) * JOIN_ROWS;
+    if (row0 >= B.nrows) return;
+    const int2 by = P.shared_by[unit];
+    if (by.x <= 1) return;
+    const Pieces pieces{by.x, by.y};
+    for (int row = row0 + warp; row < min(row0 + JOIN_ROWS, B.nrows); row += 8) {
+        auto stat = [&](int i) { return P.part_stat[pieces.slot(i) * ROWS + row]; };
+        Joined z;
+        for (int i = lane; i < pieces.n; i += 32) z.reference(stat(i));
+#pragma unroll
+        for (int x = 1; x < 32; x <<= 1) {
+            z.m = fmaxf(z.m, __shfl_xor_sync(0xffffffffu, z.m, x));
+            z.mv = fmaxf(z.mv, __shfl_xor_sync(0xffffffffu, z.mv, x));
+        }
+#pragma unroll 4
+        for (int i = 0; i < pieces.n; ++i)
+            z.add(stat(i), reinterpret_cast<const float4*>(P.partial + (pieces.slot(i) * ROWS + row) * HD)[lane]);
+        const int64_t o = B.row_of(P, (static_cast<int64_t>(l) * P.c.H + h) * P.g, row);
+        if (!KVB_IN_BOUNDS(P.err, o, 1, rows_of(P))) continue;
+        store_out(static_cast<__nv_bfloat16*>(P.out) + o * HD + 4 * lane, z.output());
+        if (lane == 0 && P.lse) P.lse[o] = z.lse();
+    }
+}
+
 }  // namespace
 
 cudaError_t launch_prefill(const AttnParams& P, const AttnPlan& p, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
     if (e != cudaSuccess) return e;
     prefill_kernel<<<p.ctas, NUM_THREADS, SMEM_BYTES, s>>>(P);
+    if ((e = cudaGetLastError()) != cudaSuccess || p.ctas == 1) return e;
+    join_kernel<<<static_cast<unsigned>(p.units * (ROWS / JOIN_ROWS)), 256, 0, s>>>(P);
     return cudaGetLastError();
 }
 
