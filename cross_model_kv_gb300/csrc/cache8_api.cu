@@ -164,7 +164,7 @@ kvb_status kvb_cache8_attention(kvb_ctx* c, const kvb_cache8* cache, const kvb_s
     const c8::AttnPlan p = c8::plan_attention(a.c, a.q, dtype, a.g, c->num_sms);
     // the kernels count rows of a sequence, units and tiles of 64 or 128 keys in 32 bits
     constexpr double most = 1 << 30;
-    if (static_cast<double>(p.units) > most || p.tiles > most || static_cast<double>(a.q.max_tokens) * a.g > most)
+    if (static_cast<double>(p.units) * (p.tensor ? 8 : 1) > most || p.tiles > most || static_cast<double>(a.q.max_tokens) * a.g > most)
         return fail(KVB_ERR_UNSUPPORTED, "kvb_cache8_attention: more query rows, sequences, layers or keys than one call takes (2^30 tiles of 64 keys)");
     if ((st = ensure_attn_ws(c, p, s)) != KVB_OK) return st;
     a.counters = static_cast<int*>(c->attn_ws);  // the tcgen05 kernel has no use for them

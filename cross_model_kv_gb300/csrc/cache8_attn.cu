@@ -89,7 +89,7 @@ __device__ __forceinline__ float2 load2(const float* p) { return __ldg(reinterpr
 // 64 bytes of codes in flight leave; the rest of a thread's state may spill, it is
 // not used inside the key loop.
 constexpr int resident_ctas(size_t element, int D, int NB) {
-    return D < 64 ? 4 : D == 64 ? (NB == 1 ? 4 : NB == 2 ? 3 : 2) : NB == 1 ? (element == 4 ? 3 : 4) : 2;
+    return D < 64 ? 4 : (NB == 1 ? 4 : 3) - (D == 128 && element == 4 ? 1 : 0);
 }
 
 template <typename T, int D, int NB, int NWARPS>
@@ -493,8 +493,7 @@ cudaError_t instance_rows(int rows, bool few, const AttnParams* P, int ctas, cud
             if constexpr (D >= 64)
                 if (few) return instance<T, D, 1, WARPS_FEW>(P, ctas, s, fit);
             return instance<T, D, 1, WARPS>(P, ctas, s, fit);
-        case 16: return instance<T, D, 2, WARPS>(P, ctas, s, fit);
-        default: return instance<T, D, 4, WARPS>(P, ctas, s, fit);
+        default: return instance<T, D, 2, WARPS>(P, ctas, s, fit);
     }
 }
 
@@ -519,8 +518,13 @@ AttnPlan plan_attention(const Cache& c, const Seqs& q, kvb_dtype dtype, int g, i
     AttnPlan p{};
     const int64_t most = static_cast<int64_t>(q.max_tokens) * g;  // rows of one sequence and head
     const double max_kv = q.max_kv > 0 ? q.max_kv : 1;
+    // More than 32 rows of bf16 and head_dim 128 go to the tensor-core kernel: 8 sequences of
+    // 4096 keys, 8 heads, rows 24 / 32 / 40 / 64 / 128: 45 / 46 / 57 / 68 / 117 us here, 54 / 55 /
+    // 54 / 55 / 53 there.  Else blocks of 8 or 16 rows; of 32 (fewer warps, spilled registers) they
+    // took 55 / 61 us at 24 / 32 rows and gained 8 % only for fp32 rows in the hundreds; four warps
+    // with 16 rows each over the same keys took 82 us at 40 rows.
     p.tensor = dtype == KVB_BF16 && c.d == 128 && most > 32;
-    p.rows = p.tensor ? PREFILL_ROWS : most <= 8 ? 8 : most <= 16 ? 16 : 32;
+    p.rows = p.tensor ? PREFILL_ROWS : most <= 8 ? 8 : 16;
     p.row_blocks = static_cast<int>((most + p.rows - 1) / p.rows);
     p.units = static_cast<int64_t>(c.n_layers) * q.n_seq * c.H * p.row_blocks;
     auto tiles = [&](int keys) { return static_cast<double>(p.units) * ((static_cast<int64_t>(max_kv) + keys - 1) / keys); };
