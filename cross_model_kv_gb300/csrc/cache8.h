@@ -110,6 +110,11 @@ __device__ __forceinline__ int exponent_for(float amax) {
     return min(max(e, E_MIN), E_MAX);
 }
 
+// Ask for `bytes` (a multiple of 16, 16-byte aligned) to be brought to L2.
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
 // Two e4m3 codes (low byte: a), to nearest even, saturating.
 __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
     uint16_t r;
