@@ -9,9 +9,9 @@
 //   warps 0..3, 4..7  softmax of tile 0, 1, a row a thread, 64 keys a step: scores
 //                 from TMEM to registers, P as fp16 over them, the sum in fp32; O is
 //                 rescaled in TMEM on the rare raise;
-//   warps 8..15   read the codes (prefetched into registers a tile ahead), convert
-//                 them to fp16 (exact) and lay them out as operands, keys and values
-//                 alike: 128-byte swizzle, key rows, K-major for S and MN-major for O;
+//   warps 8..15   read the codes, four warps of K and four of V (prefetched into
+//                 registers a tile ahead), convert them to fp16 (exact) and lay them
+//                 out as operands, keys and values alike: 128-byte swizzle, key rows, K-major for S and MN-major for O;
 //                 also the scales of the tile's 16-key groups and the CTA's next piece;
 //   warps 16, 17  one thread each issues S_x = Q_x K^T for tile x;
 //   warps 18, 19  and O_x += P_x V (P from TMEM): four threads, so that no product
@@ -199,9 +199,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < STAGES; ++i) {
-            mbar_init(&M.k_full[i], CONV);
+            mbar_init(&M.k_full[i], CONV / 2);
             mbar_init(&M.k_empty[i], 2);
-            mbar_init(&M.v_full[i], CONV);
+            mbar_init(&M.v_full[i], CONV / 2);
             mbar_init(&M.v_empty[i], 2);
         }
         for (int x = 0; x < 2; ++x) {
@@ -478,7 +478,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
         // ------------------------------------------------------- codes -> fp16 operands
         regs_down<REGS_CONVERT>();
         const int tid = threadIdx.x - SOFT;
-        const int r32 = tid >> 3, c16 = tid & 7;  // row within 32 keys, 16-code column
+        const int kv = tid >> 7;                               // half of the threads for K, half for V
+        const int r16 = (tid & 127) >> 3, c16 = tid & 7;       // row within 16 keys, 16-code column
+        uint8_t* const operand = kv ? sV : sK;
+        uint64_t* const full = kv ? M.v_full : M.k_full;
+        uint64_t* const empty = kv ? M.v_empty : M.k_empty;
         const int pm = P.c.page - 1;
         const uint32_t page_bytes = static_cast<uint32_t>(P.c.H << P.c.page_log2) * HD;
         bool go = true;
@@ -489,37 +493,31 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
             const int64_t block0 = (static_cast<int64_t>(P.c.l_begin) + G.l) * P.c.n_pages * P.c.H + G.h;  // of page 0
             // this thread's first code in page 0; page_bytes from one page's block to the next's
             const int64_t first = (block0 << P.c.page_log2) * HD + c16 * 16;
-            const uint8_t* from[2] = {P.c.code[0] + first, P.c.code[1] + first};
-            uint4 kr[4], vr[4];
-            int pid[4], pid_next[4];  // pages of the tile being loaded and of the one after it
-            auto pages = [&](int t, int (&p)[4]) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    asm volatile("ld.global.u32 %0, [%1];"
-                                 : "=r"(p[i])
-                                 : "l"(table + (min(k0 + t * TK + 32 * i + r32, last) >> P.c.page_log2)));
+            const uint8_t* from = P.c.code[kv] + first;
+            uint4 raw[8];  // of the tile that is converted next
+            int pid[8];    // pages of the tile after it
+            auto page = [&](int t, int i) {
+                int p;
+                asm volatile("ld.global.u32 %0, [%1];"
+                             : "=r"(p)
+                             : "l"(table + (min(k0 + t * TK + 16 * i, last) >> P.c.page_log2)));
+                return p;
             };
-            auto load = [&](int kv, int t, uint4 (&u)[4]) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int j = k0 + t * TK + 32 * i + r32;
-                    // slots past the last visible key may hold anything: not read
-                    const bool have = j < k1 && pid[i] >= 0 && pid[i] < P.c.n_pages &&
-                                      KVB_IN_BOUNDS(P.err, block0 + static_cast<int64_t>(pid[i]) * P.c.H, 1, blocks_of(P.c));
-                    u[i] = load16_if(from[kv] + static_cast<uint64_t>(static_cast<uint32_t>(pid[i])) * page_bytes + (j & pm) * HD, have);
-                }
+            auto load = [&](int t, int i, int p) {
+                const int j = k0 + t * TK + 16 * i + r16;
+                // slots past the last visible key may hold anything: not read
+                const bool have = j < k1 && p >= 0 && p < P.c.n_pages &&
+                                  KVB_IN_BOUNDS(P.err, block0 + static_cast<int64_t>(p) * P.c.H, 1, blocks_of(P.c));
+                return load16_if(from + static_cast<uint64_t>(static_cast<uint32_t>(p)) * page_bytes + (j & pm) * HD, have);
             };
-            auto store = [&](uint8_t* tile, const uint4 (&u)[4]) {
+            auto store = [&](uint8_t* tile, int i, const uint4& u) {
                 // codes 16 c16 .. +15 are chunks 2 c16 and 2 c16 + 1; lanes of the upper 64 dims
                 // store theirs in the other order, so that eight lanes hit eight bank groups
                 const int flip = c16 >> 2;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint4 a = make_uint4(half2_of_lo(u[i].x), half2_of_hi(u[i].x), half2_of_lo(u[i].y), half2_of_hi(u[i].y));
-                    const uint4 b = make_uint4(half2_of_lo(u[i].z), half2_of_hi(u[i].z), half2_of_lo(u[i].w), half2_of_hi(u[i].w));
-                    *reinterpret_cast<uint4*>(tile + sw_off(32 * i + r32, 2 * c16 + flip)) = flip ? b : a;
-                    *reinterpret_cast<uint4*>(tile + sw_off(32 * i + r32, 2 * c16 + 1 - flip)) = flip ? a : b;
-                }
+                const uint4 a = make_uint4(half2_of_lo(u.x), half2_of_hi(u.x), half2_of_lo(u.y), half2_of_hi(u.y));
+                const uint4 b = make_uint4(half2_of_lo(u.z), half2_of_hi(u.z), half2_of_lo(u.w), half2_of_hi(u.w));
+                *reinterpret_cast<uint4*>(tile + sw_off(16 * i + r16, 2 * c16 + flip)) = flip ? b : a;
+                *reinterpret_cast<uint4*>(tile + sw_off(16 * i + r16, 2 * c16 + 1 - flip)) = flip ? a : b;
             };
             // scales of 16-key group `tid` of a tile, for eight threads: its page is asked for two
             // tiles ahead and its scales one, so that neither is waited for
@@ -544,14 +542,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
                 group_page(1);
             }
             if (ntiles > 0) {
-                pages(0, pid);
-                pages(1, pid_next);
-                load(0, 0, kr);
-                load(1, 0, vr);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) pid[i] = page(0, i);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    raw[i] = load(0, i, pid[i]);
+                    pid[i] = page(1, i);
+                }
             }
             uint32_t stage = base % STAGES, round = base / STAGES;
             for (int t = 0; go && t < ntiles; ++t) {
-                if (!(go = mbar_wait(&M.k_empty[stage], (round & 1) ^ 1, derr, abort_flag))) break;
+                if (!(go = mbar_wait(&empty[stage], (round & 1) ^ 1, derr, abort_flag))) break;
                 if (tid < 8) {
                     TileInfo& I = M.info[(base + t) & (INFO_RING - 1)];
                     I.ks[tid] = ks;
@@ -560,18 +561,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
                     scales();
                     group_page(t + 2);
                 }
-                store(sK + stage * TILE, kr);
-                fence_proxy_async_smem();
-                mbar_arrive(&M.k_full[stage]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) pid[i] = pid_next[i];
-                if (t + 1 < ntiles) load(0, t + 1, kr);
-                if (t + 2 < ntiles) pages(t + 2, pid_next);
-                if (!(go = mbar_wait(&M.v_empty[stage], (round & 1) ^ 1, derr, abort_flag))) break;
-                store(sV + stage * TILE, vr);
+                for (int i = 0; i < 8; ++i) {  // each chunk's registers ask for the next tile's at once
+                    store(operand + stage * TILE, i, raw[i]);
+                    raw[i] = load(t + 1, i, pid[i]);
+                    pid[i] = page(t + 2, i);
+                }
                 fence_proxy_async_smem();
-                mbar_arrive(&M.v_full[stage]);
-                if (t + 1 < ntiles) load(1, t + 1, vr);
+                mbar_arrive(&full[stage]);
                 if (++stage == STAGES) {
                     stage = 0;
                     ++round;
