@@ -80,6 +80,15 @@ __device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
         : "memory");
 }
 
+// One lane of a converged warp, always the same.  The issuing warps run converged and elect the
+// lane at the products only: under `lane == 0` eight of them and their commit took 840 to 1160
+// cycles to issue, so 400 to 600 (1024 tokens over 16K: 526 -> 503 us).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p)::"memory");
+    return p != 0;
+}
+
 template <int N>
 __device__ __forceinline__ void regs_up() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -581,7 +590,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
     } else {
         // ------------------------------------------------------- products
         regs_down<REGS_MMA>();
-        const int x = warp & 1;  // tile
+        const int who = __shfl_sync(0xffffffffu, warp - 16, 0), x = who & 1;  // tile
         const uint32_t cS = tmem_base + TM_S + 128u * x;
         bool go = true;
         uint32_t even = 0, odd = 0;  // uses of the tile's score buffers before this segment
@@ -590,42 +599,51 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
             const int ntiles = (G.k1 - G.k0 + TK - 1) / TK;
             const bool idle = TR * x >= G.B.nrows;
             const int nsteps = (G.k1 - G.k0 + SK - 1) / SK;
-            if (lane == 0 && warp < 18) {
+            if (who < 2) {
                 constexpr uint32_t idesc = idesc_f16_f32(TR, SK);
                 const uint64_t q = desc_k(sQ + x * TILE), k0 = desc_k(sK);
-                go = go && (ntiles == 0 || mbar_wait(&M.q_full[x], n & 1, derr, abort_flag));
+                go = go && (ntiles == 0 || wait_all(&M.q_full[x], n & 1));
                 for (int t = 0; go && t < ntiles; ++t) {
                     const uint32_t stage = (base + t) % STAGES;
-                    if (!(go = mbar_wait(&M.k_full[stage], ((base + t) / STAGES) & 1, derr, abort_flag))) break;
+                    if (!(go = wait_all(&M.k_full[stage], ((base + t) / STAGES) & 1))) break;
                     for (int hf = 0; go && !idle && hf < 2 && 2 * t + hf < nsteps; ++hf) {
                         // P of this buffer's use before lies where these scores go
                         const uint32_t use = (hf ? odd : even) + t;
-                        if (use > 0 && !(go = mbar_wait(&M.pv_done[x][hf], (use - 1) & 1, derr, abort_flag))) break;
+                        if (use > 0 && !(go = wait_all(&M.pv_done[x][hf], (use - 1) & 1))) break;
                         tc_fence_after();
                         const uint64_t k = k0 + (stage * TILE + hf * SK * 128) / 16;
+                        if (elect_one()) {
 #pragma unroll
-                        for (int kk = 0; kk < HD / 16; ++kk) umma_bf16(cS + SK * hf, q + step_k(kk), k + step_k(kk), idesc, kk != 0);
-                        umma_commit(&M.s_full[x][hf]);
+                            for (int kk = 0; kk < HD / 16; ++kk)
+                                umma_bf16(cS + SK * hf, q + step_k(kk), k + step_k(kk), idesc, kk != 0);
+                            umma_commit(&M.s_full[x][hf]);
+                        }
+                        __syncwarp();
                     }
-                    if (go) umma_commit(&M.k_empty[stage]);
+                    if (go && elect_one()) umma_commit(&M.k_empty[stage]);
+                    __syncwarp();
                 }
-            } else if (lane == 0) {
+            } else {
                 constexpr uint32_t idesc = idesc_f16_f32(TR, HD) | IDESC_B_MN;
                 const uint32_t cO = tmem_base + TM_O + 128u * x;
                 const uint64_t v0 = desc_v(sV);
                 for (int t = 0; go && t < ntiles; ++t) {
                     const uint32_t stage = (base + t) % STAGES;
-                    if (!(go = mbar_wait(&M.v_full[stage], ((base + t) / STAGES) & 1, derr, abort_flag))) break;
+                    if (!(go = wait_all(&M.v_full[stage], ((base + t) / STAGES) & 1))) break;
                     for (int hf = 0; go && !idle && hf < 2 && 2 * t + hf < nsteps; ++hf) {
-                        if (!(go = mbar_wait(&M.p_full[x][hf], ((hf ? odd : even) + t) & 1, derr, abort_flag))) break;
+                        if (!(go = wait_all(&M.p_full[x][hf], ((hf ? odd : even) + t) & 1))) break;
                         tc_fence_after();
                         const uint64_t v = v0 + (stage * TILE) / 16 + step_v(4 * hf);
+                        if (elect_one()) {
 #pragma unroll
-                        for (int kk = 0; kk < SK / 16; ++kk)
-                            umma_f16_ts(cO, cS + SK * hf + 8u * kk, v + step_v(kk), idesc, (t | hf | kk) != 0);
-                        umma_commit(&M.pv_done[x][hf]);
+                            for (int kk = 0; kk < SK / 16; ++kk)
+                                umma_f16_ts(cO, cS + SK * hf + 8u * kk, v + step_v(kk), idesc, (t | hf | kk) != 0);
+                            umma_commit(&M.pv_done[x][hf]);
+                        }
+                        __syncwarp();
                     }
-                    if (go) umma_commit(&M.v_empty[stage]);
+                    if (go && elect_one()) umma_commit(&M.v_empty[stage]);
+                    __syncwarp();
                 }
             }
             __syncwarp();
@@ -636,9 +654,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
             }
             __syncthreads();
         }
-        if (lane == 0) {
-            umma_commit(&M.drain[warp - 16]);  // every MMA issued here completes before TMEM is released
-            mbar_wait_drain(&M.drain[warp - 16], 0, DRAIN_NS);
+        if (elect_one()) {
+            umma_commit(&M.drain[who]);  // every MMA issued here completes before TMEM is released
+            mbar_wait_drain(&M.drain[who], 0, DRAIN_NS);
         }
         __syncwarp();
     }
