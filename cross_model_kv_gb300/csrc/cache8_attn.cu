@@ -32,6 +32,7 @@
 // 512 / 2048 keys as CTAs of their own took 588 / 402 us for 32 sequences of 32768
 // keys: about 4.6 us a CTA.)  The last CTA to arrive at a unit that several share
 // joins its pieces in order, so results do not depend on timing.
+// 32 sequences of 32768 keys, one token each, 64 query and 8 KV heads: 334 us, 6.4 TB/s.
 #include "cache8_attn.cuh"
 
 namespace kvb {
@@ -531,12 +532,18 @@ AttnPlan plan_attention(const Cache& c, const Seqs& q, kvb_dtype dtype, int g, i
     AttnPlan p{};
     const int64_t most = static_cast<int64_t>(q.max_tokens) * g;  // rows of one sequence and head
     const double max_kv = q.max_kv > 0 ? q.max_kv : 1;
-    // More than 32 rows of bf16 and head_dim 128 go to the tensor-core kernel: 8 sequences of
-    // 4096 keys, 8 heads, rows 24 / 32 / 40 / 64 / 128: 45 / 46 / 57 / 68 / 117 us here, 54 / 55 /
-    // 54 / 55 / 53 there.  Else blocks of 8 or 16 rows; of 32 (fewer warps, spilled registers) they
-    // took 55 / 61 us at 24 / 32 rows and gained 8 % only for fp32 rows in the hundreds; four warps
+    // bf16 rows go to the tensor-core kernel where more than two blocks of 16 would read the keys
+    // again, three at head_dim 64.  8 heads, rows 24 / 32 / 40 / 64 / 128, us:
+    //   d 128  8 x 4096 keys    here  48 /  49 /  61 /  75 / 128   there  50 /  50 /  52 /  52 /  49
+    //          16 x 16384            237 / 239 / 342 / 450 / 882         248 / 249 / 249 / 250 / 202
+    //          1 x 4096               22 /  22 /  24 /  33 /  34          25 /  27 /  27 /  28 /  28
+    //   d 64   8 x 4096               32 /  32 /  41 /  48 /  81          43 /  44 /  45 /  45 /  41
+    //          16 x 16384            176 / 176 / 254 / 336 / 658         214 / 214 / 215 / 214 / 175
+    //          1 x 4096               16 /  16 /  17 /  23 /  24          23 /  25 /  26 /  25 /  25
+    // Else blocks of 8 or 16 rows; of 32 (fewer warps, spilled registers) they took 55 / 61 us at
+    // 24 / 32 rows, d 128, 8 x 4096, and gained 8 % only for fp32 rows in the hundreds; four warps
     // with 16 rows each over the same keys took 82 us at 40 rows.
-    p.tensor = dtype == KVB_BF16 && c.d == 128 && most > 32;
+    p.tensor = dtype == KVB_BF16 && c.d >= 64 && most > (c.d == 128 ? 32 : 48);
     p.rows = p.tensor ? PREFILL_ROWS : most <= 8 ? 8 : 16;
     p.row_blocks = static_cast<int>((most + p.rows - 1) / p.rows);
     p.units = static_cast<int64_t>(c.n_layers) * q.n_seq * c.H * p.row_blocks;

@@ -1,5 +1,5 @@
 // Attention over the paged 8-bit cache on the 5th-generation tensor cores: many
-// query rows (prompts over a cached prefix, several drafted tokens), bf16, head_dim 128.
+// query rows (prompts over a cached prefix, several drafted tokens), bf16, head_dim 64 and 128.
 //
 // The mathematics and the references are those of cache8_attn.cu; here the
 // products are large enough to be bound by the SM itself.  One CTA an SM takes 256
@@ -11,10 +11,11 @@
 //                 rescaled in TMEM on the rare raise;
 //   warps 8..15   read the codes, four warps of K and four of V (prefetched into
 //                 registers a tile ahead), convert them to fp16 (exact) and lay them
-//                 out as operands, keys and values alike: 128-byte swizzle, key rows, K-major for S and MN-major for O;
+//                 out as operands, keys and values alike: 128-byte swizzle, key rows,
+//                 K-major for S and MN-major for O;
 //                 also the scales of the tile's 16-key groups and the CTA's next piece;
-//   warps 16, 17  one thread each issues S_x = Q_x K^T for tile x;
-//   warps 18, 19  and O_x += P_x V (P from TMEM): four threads, so that no product
+//   warps 16, 17  one lane each issues S_x = Q_x K^T for tile x;
+//   warps 18, 19  and O_x += P_x V (P from TMEM): four warps, so that no product
 //                 waits behind a wait of another kind.
 // TMEM: score buffer b of tile x at 128 x + 64 b, O_x at 256 + 128 x.  P takes its
 // scores' columns, so a buffer's next scores are issued when O_x += P V has
@@ -27,6 +28,9 @@
 // The weights carry the value scale, w = 2^(s + e_v - mv); a 16-key group's sum goes
 // into the denominator with the factor 2^(mv - m - e_v), or is taken from
 // exponentials of its own where that factor could leave fp32's range.
+// 1024 tokens over 16K, 64 query and 8 KV heads: 503 us, 1.13 PF/s, about 4200 cycles for
+// each 128 keys of 256 rows.  No unit is full; the two tiles' chains S -> softmax -> P V
+// hide most of each other's waits, not all.
 // Every wait is bounded; after one gives up, its role runs through the rest without
 // touching TMEM, meeting the others at every barrier.
 #include <cfloat>
@@ -42,9 +46,8 @@ constexpr int TR = 128;              // rows of a tile, TMEM lanes
 constexpr int ROWS = PREFILL_ROWS;   // 256: two tiles
 constexpr int TK = 128;              // keys of an operand tile
 constexpr int SK = 64;               // keys of a step (two score buffers a tile in TMEM)
-constexpr int HD = 128;
 constexpr int ATOM = 128 * 128;  // bytes of 128 rows x 64 fp16
-constexpr int TILE = 2 * ATOM;
+constexpr int tile_bytes(int HD) { return HD / 64 * ATOM; }  // 128 rows
 constexpr int STAGES = 2;  // operand tiles of K, and of V
 constexpr int SOFT = 256, CONV = 256;
 constexpr int NUM_THREADS = SOFT + CONV + 128;
@@ -52,7 +55,7 @@ constexpr int NUM_THREADS = SOFT + CONV + 128;
 // the launch's 640 * 96 = 61440.
 constexpr int REGS_SOFTMAX = 144, REGS_CONVERT = 72, REGS_MMA = 40;
 constexpr int INFO_RING = 8;  // scales are written at most seven tiles before the softmax is done with them
-constexpr int SMEM_BYTES = (2 + 2 * STAGES) * TILE + 1024 + 2048;
+constexpr int smem_bytes(int HD) { return (2 + 2 * STAGES) * tile_bytes(HD) + 1024 + 2048; }
 constexpr uint32_t TM_S = 0, TM_O = 256;  // TMEM columns, 128 more for tile 1
 constexpr float FACTOR_LOG2 = 60.f;  // a group's factor is used within 2^-60 .. 2^60
 constexpr uint64_t DRAIN_NS = 200ull * 1000 * 1000;
@@ -188,7 +191,9 @@ struct Smem {
     alignas(16) TileInfo info[INFO_RING];
 };
 
+template <int HD>
 __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_constant__ AttnParams P) {
+    constexpr int TILE = tile_bytes(HD);
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t* sQ = smem;
@@ -304,12 +309,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
             float qs;
             {
                 const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(P.query) + row_index() * HD);
-                uint4 u[16];
+                uint4 u[HD / 8];
 #pragma unroll
-                for (int c = 0; c < 16; ++c) u[c] = valid ? __ldg(q + c) : make_uint4(0, 0, 0, 0);
+                for (int c = 0; c < HD / 8; ++c) u[c] = valid ? __ldg(q + c) : make_uint4(0, 0, 0, 0);
                 float amax = 0.f;
 #pragma unroll
-                for (int c = 0; c < 16; ++c) {
+                for (int c = 0; c < HD / 8; ++c) {
                     const uint32_t w[4] = {u[c].x, u[c].y, u[c].z, u[c].w};
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
@@ -319,7 +324,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
                 const float inv = pow2(-eq);
                 qs = pow2(eq) * P.scale_log2;
 #pragma unroll
-                for (int c = 0; c < 16; ++c) {
+                for (int c = 0; c < HD / 8; ++c) {
                     const uint32_t w[4] = {u[c].x, u[c].y, u[c].z, u[c].w};
                     uint32_t o[4];
 #pragma unroll
@@ -488,7 +493,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
         regs_down<REGS_CONVERT>();
         const int tid = threadIdx.x - SOFT;
         const int kv = tid >> 7;                               // half of the threads for K, half for V
-        const int r16 = (tid & 127) >> 3, c16 = tid & 7;       // row within 16 keys, 16-code column
+        constexpr int COLS = HD / 16, RP = 128 / COLS, N = TK / RP;  // 16-code columns of a row, rows of a pass, passes
+        const int rr = (tid & 127) / COLS, c16 = tid % COLS;   // row of the pass, column
         uint8_t* const operand = kv ? sV : sK;
         uint64_t* const full = kv ? M.v_full : M.k_full;
         uint64_t* const empty = kv ? M.v_empty : M.k_empty;
@@ -503,17 +509,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
             // this thread's first code in page 0; page_bytes from one page's block to the next's
             const int64_t first = (block0 << P.c.page_log2) * HD + c16 * 16;
             const uint8_t* from = P.c.code[kv] + first;
-            uint4 raw[8];  // of the tile that is converted next
-            int pid[8];    // pages of the tile after it
+            uint4 raw[N];  // of the tile that is converted next
+            int pid[N];    // pages of the tile after it
             auto page = [&](int t, int i) {
                 int p;
                 asm volatile("ld.global.u32 %0, [%1];"
                              : "=r"(p)
-                             : "l"(table + (min(k0 + t * TK + 16 * i, last) >> P.c.page_log2)));
+                             : "l"(table + (min(k0 + t * TK + RP * i + (RP > 16 ? rr : 0), last) >> P.c.page_log2)));
                 return p;
             };
             auto load = [&](int t, int i, int p) {
-                const int j = k0 + t * TK + 16 * i + r16;
+                const int j = k0 + t * TK + RP * i + rr;
                 // slots past the last visible key may hold anything: not read
                 const bool have = j < k1 && p >= 0 && p < P.c.n_pages &&
                                   KVB_IN_BOUNDS(P.err, block0 + static_cast<int64_t>(p) * P.c.H, 1, blocks_of(P.c));
@@ -521,12 +527,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
             };
             auto store = [&](uint8_t* tile, int i, const uint4& u) {
                 // codes 16 c16 .. +15 are chunks 2 c16 and 2 c16 + 1; lanes of the upper 64 dims
-                // store theirs in the other order, so that eight lanes hit eight bank groups
+                // store theirs in the other order, so that eight lanes hit eight bank groups (of a row
+                // of 64 dims: the eight lanes are two rows, which the swizzle sets apart)
                 const int flip = c16 >> 2;
                 const uint4 a = make_uint4(half2_of_lo(u.x), half2_of_hi(u.x), half2_of_lo(u.y), half2_of_hi(u.y));
                 const uint4 b = make_uint4(half2_of_lo(u.z), half2_of_hi(u.z), half2_of_lo(u.w), half2_of_hi(u.w));
-                *reinterpret_cast<uint4*>(tile + sw_off(16 * i + r16, 2 * c16 + flip)) = flip ? b : a;
-                *reinterpret_cast<uint4*>(tile + sw_off(16 * i + r16, 2 * c16 + 1 - flip)) = flip ? a : b;
+                *reinterpret_cast<uint4*>(tile + sw_off(RP * i + rr, 2 * c16 + flip)) = flip ? b : a;
+                *reinterpret_cast<uint4*>(tile + sw_off(RP * i + rr, 2 * c16 + 1 - flip)) = flip ? a : b;
             };
             // scales of 16-key group `tid` of a tile, for eight threads: its page is asked for two
             // tiles ahead and its scales one, so that neither is waited for
@@ -552,9 +559,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
             }
             if (ntiles > 0) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) pid[i] = page(0, i);
+                for (int i = 0; i < N; ++i) pid[i] = page(0, i);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
+                for (int i = 0; i < N; ++i) {
                     raw[i] = load(0, i, pid[i]);
                     pid[i] = page(1, i);
                 }
@@ -571,7 +578,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
                     group_page(t + 2);
                 }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {  // each chunk's registers ask for the next tile's at once
+                for (int i = 0; i < N; ++i) {  // each chunk's registers ask for the next tile's at once
                     store(operand + stage * TILE, i, raw[i]);
                     raw[i] = load(t + 1, i, pid[i]);
                     pid[i] = page(t + 2, i);
@@ -673,8 +680,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
 
 // Joins the pieces of the units that several CTAs shared, in the order of their keys,
 // a warp a row: 256 rows of a unit are too many for its last CTA, which was 20 to
-// 30 us behind the others (1024 tokens over 16K: 570 us with that, see the table of cases).
+// 30 us behind the others (1024 tokens over 16K: 570 us with that, 527 without).
 constexpr int JOIN_ROWS = 32;  // of a CTA
+template <int HD>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnParams P) {
     constexpr int PER = ROWS / JOIN_ROWS;
     const int unit = blockIdx.x / PER, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -697,23 +705,28 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnP
         }
 #pragma unroll 4
         for (int i = 0; i < pieces.n; ++i)
-            z.add(stat(i), reinterpret_cast<const float4*>(P.partial + (pieces.slot(i) * ROWS + row) * HD)[lane]);
+            z.add(stat(i), reinterpret_cast<const float4*>(P.partial + (pieces.slot(i) * ROWS + row) * HD)[lane % (HD / 4)]);
         const int64_t o = B.row_of(P, (static_cast<int64_t>(l) * P.c.H + h) * P.g, row);
         if (!KVB_IN_BOUNDS(P.err, o, 1, rows_of(P))) continue;
-        store_out(static_cast<__nv_bfloat16*>(P.out) + o * HD + 4 * lane, z.output());
+        if (lane < HD / 4) store_out(static_cast<__nv_bfloat16*>(P.out) + o * HD + 4 * lane, z.output());
         if (lane == 0 && P.lse) P.lse[o] = z.lse();
     }
+}
+
+template <int HD>
+cudaError_t launch(const AttnParams& P, const AttnPlan& p, cudaStream_t s) {
+    cudaError_t e = cudaFuncSetAttribute(prefill_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(HD));
+    if (e != cudaSuccess) return e;
+    prefill_kernel<HD><<<p.ctas, NUM_THREADS, smem_bytes(HD), s>>>(P);
+    if ((e = cudaGetLastError()) != cudaSuccess || p.ctas == 1) return e;
+    join_kernel<HD><<<static_cast<unsigned>(p.units * (ROWS / JOIN_ROWS)), 256, 0, s>>>(P);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_prefill(const AttnParams& P, const AttnPlan& p, cudaStream_t s) {
-    cudaError_t e = cudaFuncSetAttribute(prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
-    if (e != cudaSuccess) return e;
-    prefill_kernel<<<p.ctas, NUM_THREADS, SMEM_BYTES, s>>>(P);
-    if ((e = cudaGetLastError()) != cudaSuccess || p.ctas == 1) return e;
-    join_kernel<<<static_cast<unsigned>(p.units * (ROWS / JOIN_ROWS)), 256, 0, s>>>(P);
-    return cudaGetLastError();
+    return P.c.d == 64 ? launch<64>(P, p, s) : launch<128>(P, p, s);
 }
 
 }  // namespace c8

@@ -402,8 +402,11 @@ kvb_status kvb_cache8_read(kvb_ctx* ctx, const kvb_cache8* cache, const kvb_seqs
  *   scale   > 0, or 0 for 1/sqrt(d)
  * seq_pos may be negative here.  To attend over the call's own tokens too, write
  * them first.  Scores, softmax and sums are fp32; queries enter the products
- * exactly (bf16) or as an fp16 pair (fp32: 22 bits), probabilities as fp16
- * (bf16) or an fp16 pair (fp32).  Workspace (partial outputs where keys are
+ * as fp16 under a power of two for each row (bf16: exact down to 2^-28 of the
+ * row's largest element) or as an fp16 pair (fp32: 22 bits), probabilities as
+ * fp16 (bf16) or an fp16 pair (fp32).  The result does not depend on timing.
+ * Calls whose layers x sequences x heads x keys make 2^30 tiles of 64 keys or
+ * more are refused.  Workspace (partial outputs where keys are
  * split) belongs to the context and grows on demand, which synchronises: make
  * a call of the largest size before capturing a stream.
  */

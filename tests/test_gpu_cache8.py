@@ -663,3 +663,17 @@ def test_prompt_over_bad_pages_reports_and_sees_the_others(kvb):
     kvb.kvb_ctx_check(P.ctx)
     assert torch.allclose(out[:, :, 30:].float(), o2.float(), rtol=2.0 ** -7, atol=2.0 ** -9)
     assert torch.allclose(lse[:, :, 30:], z2, rtol=0, atol=2.0 ** -16)
+
+
+@pytest.mark.parametrize("page,H,g,n,lens", [(64, 1, 8, [100, 33, 0], [1500, 40, 10]), (16, 2, 4, [257, 64, 1], [900, 64, 300]),
+                                             (128, 1, 16, [70, 20, 16], [700, 129, 16]), (32, 2, 1, [513, 128, 65], [513, 640, 65])])
+def test_prompt_of_head_dim_64(kvb, page, H, g, n, lens):
+    P = Pool(kvb, 2, H, 64, page, 3, max(lens), seed=page + g + 1)
+    P.fill(lens)
+    q = torch.from_numpy(1.5 * P.rng.standard_normal((2, H * g, sum(n), 64))).to(BF).cuda()
+    pos = np.asarray(lens) - n
+    out, lse = attend(P, q, offsets(n), pos)
+    kvb.kvb_ctx_check(P.ctx)
+    check_attention(P, q, offsets(n), pos, out, lse)
+    o2, z2 = attend(P, q, offsets(n), pos)
+    assert torch.equal(out, o2) and torch.equal(lse, z2)
