@@ -21,14 +21,13 @@
 // scores' columns, so a buffer's next scores are issued when O_x += P V has
 // completed; meanwhile the softmax works on the other buffer (one buffer of 128
 // keys left it waiting 2500 of 5800 cycles for each 128 keys).
-// What 128 keys of 256 rows cost an SM, cycles: products 2048; special functions
-// (32768 exponentials at 16 a cycle, and the fp16 conversions) 2048 to 3072;
-// shared memory 3072 (192 KB of S operands, 64 of V, 64 + 64 of the conversion, at
-// 128 bytes a cycle).
+// What 128 keys of 256 rows cost an SM, cycles: products 2048; shared memory 3072
+// (192 KB of S operands, 64 of V, 64 + 64 of the conversion, at 128 bytes a cycle);
+// exponentials about 1000, maxima, masks and conversions on the ALU about 2000.
 // The weights carry the value scale, w = 2^(s + e_v - mv); a 16-key group's sum goes
 // into the denominator with the factor 2^(mv - m - e_v), or is taken from
 // exponentials of its own where that factor could leave fp32's range.
-// 1024 tokens over 16K, 64 query and 8 KV heads: 503 us, 1.13 PF/s, about 4200 cycles for
+// 1024 tokens over 16K, 64 query and 8 KV heads: 495 us, 1.15 PF/s, about 4200 cycles for
 // each 128 keys of 256 rows.  No unit is full; the two tiles' chains S -> softmax -> P V
 // hide most of each other's waits, not all.
 // Every wait is bounded; after one gives up, its role runs through the rest without
@@ -124,6 +123,13 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
     return d;
 }
+// The largest of three numbers, in one instruction; NaN loses, as in fmaxf (the row maxima by
+// fmaxf: 503 us, not 495, at 1024 tokens over 16K).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     float2 d;
     asm("{\n\t.reg .b64 x, y, w;\n\t"
@@ -155,6 +161,17 @@ __device__ __forceinline__ float load4_if(const float* p, bool pred) {
         : "=&f"(v)
         : "l"(p), "r"(static_cast<uint32_t>(pred)));
     return v;
+}
+
+// One look at a phase, without waiting.
+__device__ __forceinline__ bool mbar_complete(uint64_t* bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
 }
 
 struct TileInfo {
@@ -368,12 +385,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
                 float ms = -INFINITY, mvs = -INFINITY;
 #pragma unroll
                 for (int gq = 0; gq < 4; ++gq) {
-                    float top[4];
+                    float top[5];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        top[j] = fmaxf(fmaxf(__uint_as_float(sv[16 * gq + 4 * j]), __uint_as_float(sv[16 * gq + 4 * j + 1])),
-                                       fmaxf(__uint_as_float(sv[16 * gq + 4 * j + 2]), __uint_as_float(sv[16 * gq + 4 * j + 3])));
-                    const float best = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * k[gq];
+                    for (int j = 0; j < 5; ++j)
+                        top[j] = max3(__uint_as_float(sv[16 * gq + 3 * j]), __uint_as_float(sv[16 * gq + 3 * j + 1]),
+                                      __uint_as_float(sv[16 * gq + 3 * j + 2]));
+                    const float best = fmaxf(max3(top[0], top[1], top[2]), max3(top[3], top[4], __uint_as_float(sv[16 * gq + 15]))) * k[gq];
                     ms = fmaxf(ms, best);
                     mvs = fmaxf(mvs, best + ev[gq]);
                 }
@@ -609,6 +626,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
             if (who < 2) {
                 constexpr uint32_t idesc = idesc_f16_f32(TR, SK);
                 const uint64_t q = desc_k(sQ + x * TILE), k0 = desc_k(sK);
+                // With no time to wait, queries that are not there yet are a timeout at once: these waits
+                // are short enough for mbar_wait never to look at the clock.  (Asked at every wait: 510
+                // us, not 495, for 1024 tokens over 16K.)
+                if (go && ntiles > 0 && derr.timeout_ns == 0 && !__all_sync(0xffffffffu, mbar_complete(&M.q_full[x], n & 1))) {
+                    dev_err_set(derr, DEV_ERR_TIMEOUT);
+                    *abort_flag = 1;
+                    go = false;
+                }
                 go = go && (ntiles == 0 || wait_all(&M.q_full[x], n & 1));
                 for (int t = 0; go && t < ntiles; ++t) {
                     const uint32_t stage = (base + t) % STAGES;
