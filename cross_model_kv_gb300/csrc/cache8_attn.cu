@@ -58,10 +58,14 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     return y;
 }
 
-// W consecutive 32-bit words (B bytes), read once: not kept in L1.
-template <int B>
+// W consecutive 32-bit words (B bytes), read once: not kept in L1.  WHOLE: 32 bytes are 32-byte
+// aligned and come in one load, else (16-byte aligned) in two.
+template <int B, bool WHOLE = true>
 __device__ __forceinline__ void load_codes(const uint8_t* p, uint32_t* w) {
-    if constexpr (B == 32) {
+    if constexpr (B == 32 && !WHOLE) {
+        load_codes<16>(p, w);
+        load_codes<16>(p + 16, w + 4);
+    } else if constexpr (B == 32) {
         asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                      : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
                      : "l"(p));
@@ -105,7 +109,8 @@ struct Shape8 {
     }
 };
 
-template <typename T, int D, int NB, int NWARPS>
+// WHOLE: key rows can be read 32 bytes at a time (see whole_rows).
+template <typename T, int D, int NB, int NWARPS, bool WHOLE>
 __global__ void __launch_bounds__(NWARPS * 32, NWARPS == WARPS ? resident_ctas(sizeof(T), D, NB) : 1)
     decode_kernel(const __grid_constant__ AttnParams P) {
     constexpr int NT = NWARPS * 32, TILE_KEYS = 16 * NWARPS;
@@ -202,8 +207,8 @@ __global__ void __launch_bounds__(NWARPS * 32, NWARPS == WARPS ? resident_ctas(s
         }
         const int64_t blk = slab + static_cast<int64_t>(s_page[pi]) * P.c.H;
         const uint8_t* p = P.c.code[0] + ((blk << P.c.page_log2) + (j & (P.c.page - 1))) * D;
-        load_codes<KB>(p + r * D + c * KB, kw[0]);
-        load_codes<KB>(p + (r + 8) * D + c * KB, kw[1]);
+        load_codes<KB, WHOLE>(p + r * D + c * KB, kw[0]);
+        load_codes<KB, WHOLE>(p + (r + 8) * D + c * KB, kw[1]);
     };
     auto load_v = [&](int j, uint32_t (&vw)[4][VW]) {
         const int pi = (j >> P.c.page_log2) - page0;
@@ -481,11 +486,17 @@ __global__ void __launch_bounds__(NWARPS * 32, NWARPS == WARPS ? resident_ctas(s
     }
 }
 
+// A lane takes 32 bytes of a key row at head_dim 128.  Rows and pages are multiples of 128
+// bytes, so all of them lie as the buffer does, which is 16-byte aligned: where it is not
+// 32-byte aligned, instances of their own read halves.  32 sequences of 32768 keys: 335 us, in
+// halves 353; both in one kernel under a predicate cost every call 1.3 %.
+bool whole_rows(const Cache& c) { return (reinterpret_cast<uintptr_t>(c.code[0]) & 31u) == 0; }
+
 // One instance: CTAs of it that fit an SM (P null), or its launch.
-template <typename T, int D, int NB, int NWARPS>
+template <typename T, int D, int NB, int NWARPS, bool WHOLE>
 cudaError_t instance(const AttnParams* P, int ctas, cudaStream_t s, int* fit) {
     constexpr size_t smem = Shape8<T, D, NB, NWARPS>::smem();
-    const auto kernel = decode_kernel<T, D, NB, NWARPS>;
+    const auto kernel = decode_kernel<T, D, NB, NWARPS, WHOLE>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     if (!P) {
@@ -500,30 +511,32 @@ cudaError_t instance(const AttnParams* P, int ctas, cudaStream_t s, int* fit) {
     return cudaGetLastError();
 }
 
-template <typename T, int D>
+template <typename T, int D, bool WHOLE = true>
 cudaError_t instance_rows(int rows, bool few, const AttnParams* P, int ctas, cudaStream_t s, int* fit) {
     switch (rows) {
         case 8:
             if constexpr (D >= 64)
-                if (few) return instance<T, D, 1, WARPS_FEW>(P, ctas, s, fit);
-            return instance<T, D, 1, WARPS>(P, ctas, s, fit);
-        default: return instance<T, D, 2, WARPS>(P, ctas, s, fit);
+                if (few) return instance<T, D, 1, WARPS_FEW, WHOLE>(P, ctas, s, fit);
+            return instance<T, D, 1, WARPS, WHOLE>(P, ctas, s, fit);
+        default: return instance<T, D, 2, WARPS, WHOLE>(P, ctas, s, fit);
     }
 }
 
 template <typename T>
-cudaError_t instance_dim(int d, int rows, bool few, const AttnParams* P, int ctas, cudaStream_t s, int* fit) {
-    switch (d) {
+cudaError_t instance_dim(const Cache& c, int rows, bool few, const AttnParams* P, int ctas, cudaStream_t s, int* fit) {
+    switch (c.d) {
         case 16: return instance_rows<T, 16>(rows, few, P, ctas, s, fit);
         case 32: return instance_rows<T, 32>(rows, few, P, ctas, s, fit);
         case 64: return instance_rows<T, 64>(rows, few, P, ctas, s, fit);
-        default: return instance_rows<T, 128>(rows, few, P, ctas, s, fit);
+        default:
+            return whole_rows(c) ? instance_rows<T, 128>(rows, few, P, ctas, s, fit)
+                                 : instance_rows<T, 128, false>(rows, few, P, ctas, s, fit);
     }
 }
 
-cudaError_t pick(kvb_dtype dtype, int d, int rows, bool few, const AttnParams* P, int ctas, cudaStream_t s, int* fit) {
-    return dtype == KVB_BF16 ? instance_dim<__nv_bfloat16>(d, rows, few, P, ctas, s, fit)
-                             : instance_dim<float>(d, rows, few, P, ctas, s, fit);
+cudaError_t pick(kvb_dtype dtype, const Cache& c, int rows, bool few, const AttnParams* P, int ctas, cudaStream_t s, int* fit) {
+    return dtype == KVB_BF16 ? instance_dim<__nv_bfloat16>(c, rows, few, P, ctas, s, fit)
+                             : instance_dim<float>(c, rows, few, P, ctas, s, fit);
 }
 
 }  // namespace
@@ -553,7 +566,7 @@ AttnPlan plan_attention(const Cache& c, const Seqs& q, kvb_dtype dtype, int g, i
     // over 4096 keys: 11.5 us; with 4 warps and 4 tiles each 14.9, with 16 warps 13.0)
     p.few = !p.tensor && p.rows == 8 && c.d >= 64 && tiles(16 * WARPS) < static_cast<double>(FEW_TILES) * 4 * num_sms;
     int fit = 1;
-    if (!p.tensor) pick(dtype, c.d, p.rows, p.few, nullptr, 0, nullptr, &fit);
+    if (!p.tensor) pick(dtype, c, p.rows, p.few, nullptr, 0, nullptr, &fit);
     // the CTAs that fit the GPU, no more than the keys give the least share to
     p.min_tiles = p.few ? 1 : MIN_TILES;
     const double need = (tiles(p.tensor ? 128 : 16 * (p.few ? WARPS_FEW : WARPS)) + p.min_tiles - 1) / p.min_tiles;
@@ -568,7 +581,7 @@ AttnPlan plan_attention(const Cache& c, const Seqs& q, kvb_dtype dtype, int g, i
 }
 
 cudaError_t launch_decode(const AttnParams& P, kvb_dtype dtype, const AttnPlan& p, cudaStream_t s) {
-    return pick(dtype, P.c.d, p.rows, p.few, &P, p.ctas, s, nullptr);
+    return pick(dtype, P.c, p.rows, p.few, &P, p.ctas, s, nullptr);
 }
 
 }  // namespace c8

@@ -329,6 +329,7 @@ kvb_status kvb_attention_cosine(kvb_ctx* ctx, kvb_dtype dtype, const void* q, in
  * under a larger scale changes only if it becomes subnormal, and c * 2^e is
  * exact in bf16.
  *   k, v             device [L_tgt][n_pages][H][page_tokens][d] bytes, 16-byte aligned
+ *                    (at d = 128 attention of few rows reads a k aligned to 32 bytes faster)
  *   k_scale, v_scale device float32 [L_tgt][n_pages][H]
  * page_tokens is 16, 32, 64 or 128 and d (the context's) 16, 32, 64 or 128.
  * The caller owns the four buffers; they need no initial value, since only
