@@ -16,6 +16,10 @@ namespace c8 {
 constexpr int E_MIN = -117;  // 2^-9 (the least code) * 2^-117 is the least normal float
 constexpr int E_MAX = 119;   // 448 * 2^119 is finite
 
+// Positions of a sequence are counted in 32 bits.  The attention kernels name keys that lie past
+// the last one (and do not read them): up to 382 with tiles asked for two ahead.
+constexpr int64_t MAX_KEYS = 0x7ffffc00;
+
 // The error word of the context and its host mirror (pinned, written by the
 // kernel that finds the error, so that a call needs no copy back).
 struct Err {

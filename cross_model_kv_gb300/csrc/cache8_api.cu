@@ -61,7 +61,7 @@ kvb_status check_call(kvb_ctx* c, const kvb_cache8* cache, const kvb_seqs* seqs,
     sv->max_tokens = seqs->max_tokens;
     const int64_t room = static_cast<int64_t>(seqs->max_pages) * pt;
     const int64_t kv = seqs->max_kv > 0 && seqs->max_kv < room ? seqs->max_kv : room;
-    if (kv > 0x7fffff00LL) return fail(KVB_ERR_UNSUPPORTED, w + ": more than 2^31 cache positions in a sequence");
+    if (kv > c8::MAX_KEYS) return fail(KVB_ERR_UNSUPPORTED, w + ": more than 2^31 - 1024 cache positions in a sequence");
     sv->max_kv = static_cast<int>(kv);
     sv->T = T;
     return KVB_OK;

@@ -156,7 +156,8 @@ __global__ void __launch_bounds__(NWARPS * 32, NWARPS == WARPS ? resident_ctas(s
     int page0 = 0;
     auto list_pages = [&](int k) {
         page0 = k >> P.c.page_log2;
-        const int end = min(k1, k + (LIST_PAGES << P.c.page_log2));
+        const int span = LIST_PAGES << P.c.page_log2;
+        const int end = k1 - k > span ? k + span : k1;  // k + span may pass 2^31
         const int npages = end > k ? ((end - 1) >> P.c.page_log2) - page0 + 1 : 0;
         for (int i = threadIdx.x; i < npages; i += NT) {
             int pid = __ldg(P.q.page_table + static_cast<int64_t>(s) * P.q.max_pages + page0 + i);

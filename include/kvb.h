@@ -352,7 +352,8 @@ typedef struct {
  *   max_tokens  the most tokens that one sequence owns
  *   kv_len      [n_seq], or NULL for seq_pos[s] + its tokens: cache positions
  *               that kvb_cache8_attention may read (the other calls ignore it)
- *   max_kv      the largest kv_len, or 0 for max_pages * page_tokens
+ *   max_kv      the largest kv_len, or 0 for max_pages * page_tokens; a call whose
+ *               sequences could have more than 2^31 - 1024 positions is refused
  * max_tokens and max_kv size the launches.  Sequences that run past max_tokens,
  * T, max_kv or their row of the page table, and pages outside [0, n_pages), are
  * found by the kernels: KVB_ERR_INVALID_ARG is recorded on the context, and

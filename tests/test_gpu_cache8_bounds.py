@@ -1,8 +1,10 @@
-"""The 8-bit cache at the edges of what its calls accept: how the buffers are aligned."""
+"""The 8-bit cache at the edges of what its calls accept: how the buffers are
+aligned, and positions up to the last that a call may name."""
 import numpy as np
 import pytest
 
-from test_gpu_cache8 import BF, F32, Pool, attend, i32, kvb, offsets  # noqa: F401  (kvb: the fixture)
+from cases import to_host64
+from test_gpu_cache8 import BF, F32, Pool, i32, kvb, offsets  # noqa: F401  (kvb: the fixture)
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -55,3 +57,56 @@ def test_codes_aligned_to_16_bytes(kvb, d, g, n, dtype):  # noqa: F811
     kvb.kvb_ctx_check(P.ctx)
     assert all(torch.equal(a, b) for a, b in zip(*back))
     assert torch.equal(near.k.view(torch.uint8), far.k) and torch.equal(near.v.view(torch.uint8), far.v)
+
+
+# ------------------------------------------------------------------ positions up to 2^31
+
+@pytest.mark.parametrize("d,g,dtype", [(16, 1, BF), (64, 2, F32), (128, 8, BF), (64, 50, BF)])
+def test_the_last_positions_that_a_call_may_name(kvb, d, g, dtype):  # noqa: F811
+    # 2^31 - 1024 positions, the most that is accepted, on three pages that repeat: a list of
+    # pages that is asked for from near the end would pass 2^31.  Every key counts as often as its page comes.
+    # Tolerance: each CTA adds the keys of its share one after another in fp32, 16 (bf16 prompt
+    # kernel, 152 CTAs) or 32 (152 CTAs at least, 4 warps) at a time: steps of 2^-23 each, in
+    # numerator and denominator; then the formats' 2^-11 for weights and 2^-8 for the output.
+    page, kv = 128, 0x7ffffc00
+    P = Pool(kvb, 1, 1, d, page, 1, 3 * page, spare=0)
+    P.fill([3 * page])
+    table = i32(P.table[0])[torch.arange(kv // page, device="cuda") % 3][None].contiguous()
+    q = torch.from_numpy(4.0 * P.rng.standard_normal((1, g, 1, d))).to(dtype).cuda()  # few keys decide
+    out, lse = torch.empty_like(q), torch.empty((1, g, 1), device="cuda")
+    seqs = kvb.Seqs(table, i32([0, 1]), i32([kv - 1]), max_tokens=1)
+    kvb.kvb_cache8_attention(P.ctx, P.cache, seqs, q, out, lse)
+    kvb.kvb_ctx_check(P.ctx)
+    k, v = (P.ref.sequence(x, P.table[0], 3 * page, 0, 0) for x in (0, 1))
+    times = np.repeat([kv // page - 2 * (kv // page // 3) - (kv // page % 3 > 1), 0, kv // page // 3], page)
+    times[page:2 * page] = kv // page - times[0] - times[-1]
+    s = to_host64(q)[0, :, 0] @ k.T / np.sqrt(d)
+    w = np.exp(s - s.max(axis=1, keepdims=True)) * times
+    z = s.max(axis=1) + np.log(w.sum(axis=1))
+    w /= w.sum(axis=1, keepdims=True)
+    steps = kv / 152 / 16
+    tol = (w @ np.abs(v)) * (2 * steps * 2.0 ** -23 + 2.0 ** -10) + np.abs(w @ v) * 2.0 ** -8
+    assert (np.abs(to_host64(out)[0, :, 0] - w @ v) <= tol).all()
+    assert (np.abs(to_host64(lse)[0, :, 0] - z) <= steps * 2.0 ** -23 + 2.0 ** -10).all()
+
+
+def test_more_positions_are_refused(kvb):  # noqa: F811
+    P = Pool(kvb, 1, 1, 64, 128, 1, 128)
+    P.fill([5])
+    q = torch.zeros((1, 1, 1, 64), device="cuda")
+    lib = kvb.load_library()
+
+    def status(call, max_pages, max_kv):  # the sequence itself stays at its five positions
+        s = P.seqs([0, 1], [4])
+        s.struct.max_pages, s.struct.max_kv = max_pages, max_kv
+        if call == "attention":
+            return lib.kvb_cache8_attention(P.ctx.handle, P.cache.ref, s.ref, 0, 1, 0, q.data_ptr(), 1, 1, 0.0, q.data_ptr(),
+                                            None, None)
+        return getattr(lib, "kvb_cache8_" + call)(P.ctx.handle, P.cache.ref, s.ref, 0, 1, 0, q.data_ptr(), q.data_ptr(), 1, None)
+
+    most = 0x7ffffc00 // 128
+    for call in ("write", "read", "attention"):
+        assert status(call, most, 0) == 0 and status(call, most + 1, 0x7ffffc00) == 0
+        for max_kv in (0, 0x7ffffc01, 0x7fffffff):
+            assert status(call, most + 1, max_kv) == 3
+    kvb.kvb_ctx_check(P.ctx)
