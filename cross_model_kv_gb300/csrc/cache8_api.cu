@@ -79,26 +79,40 @@ bool too_many_blocks(const c8::Cache& c, const c8::Seqs& q) {
     return items * q.n_seq * c.H * c.n_layers > 2147483647.0;
 }
 
-// Counters (zeroed once; every call leaves them at zero), then the partial outputs and what is noted of units.
-kvb_status ensure_attn_ws(kvb_ctx* c, const c8::AttnPlan& p, cudaStream_t s) {
-    const size_t rest = p.partial_bytes + p.unit_bytes;
-    if (p.counter_bytes <= c->attn_ws_counters && c->attn_ws_counters + rest <= c->attn_ws_bytes) return KVB_OK;
-    cudaError_t e;
-    if (c->attn_ws) {
-        if ((e = cudaDeviceSynchronize()) != cudaSuccess) return cuda_fail(e, "sync before growing the attention workspace");
-        cudaFree(c->attn_ws);
-        c->attn_ws = nullptr;
-        c->attn_ws_bytes = c->attn_ws_counters = 0;
+// One buffer of the attention workspace made large enough, with room for calls to come; the
+// old one is kept until the context goes (its sizes grow by a quarter at least, so all of
+// them together stay within five times the last).
+kvb_status grow(kvb_ctx* c, void** buf, size_t* have, size_t need, size_t bytes, bool zeroed, cudaStream_t s) {
+    if (need <= *have) return KVB_OK;
+    cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
+    cudaError_t e = cudaStreamIsCapturing(s, &capturing);
+    if (e != cudaSuccess) return cuda_fail(e, "growing the attention workspace");
+    if (capturing != cudaStreamCaptureStatusNone)
+        return fail(KVB_ERR_UNSUPPORTED,
+                    "kvb_cache8_attention: the workspace would have to grow on a stream that is being captured; make this call once before");
+    try {
+        c->attn_outgrown.reserve(c->attn_outgrown.size() + 1);
+    } catch (...) {
+        return fail(KVB_ERR_OOM, "host allocation failed");
     }
-    // room for counters of larger calls to come, so that a batch that grows by a sequence does not reallocate
-    const size_t counters = p.counter_bytes < 65536 ? 65536 : 2 * p.counter_bytes;
-    const size_t bytes = counters + rest + rest / 4;
-    if ((e = cudaMalloc(&c->attn_ws, bytes)) != cudaSuccess) return cuda_fail(e, "cudaMalloc attention workspace");
-    if ((e = cudaMemset(c->attn_ws, 0, counters)) != cudaSuccess || (e = cudaStreamSynchronize(0)) != cudaSuccess)
+    void* p = nullptr;
+    if ((e = cudaMalloc(&p, bytes)) != cudaSuccess) return cuda_fail(e, "cudaMalloc attention workspace");
+    if (zeroed && (e = cudaMemsetAsync(p, 0, bytes, s)) != cudaSuccess) {
+        cudaFree(p);
         return cuda_fail(e, "zeroing the attention workspace");
-    c->attn_ws_bytes = bytes;
-    c->attn_ws_counters = counters;
+    }
+    if (*buf) c->attn_outgrown.push_back(*buf);
+    *buf = p;
+    *have = bytes;
     return KVB_OK;
+}
+
+// Counters (zeroed once; every call leaves them at zero), and the partial outputs with what is noted of units.
+kvb_status ensure_attn_ws(kvb_ctx* c, const c8::AttnPlan& p, cudaStream_t s) {
+    const size_t parts = p.partial_bytes + p.unit_bytes;
+    const kvb_status st = grow(c, &c->attn_counters, &c->attn_counters_bytes, p.counter_bytes,
+                               p.counter_bytes < 65536 ? 65536 : 2 * p.counter_bytes, true, s);
+    return st != KVB_OK ? st : grow(c, &c->attn_parts, &c->attn_parts_bytes, parts, parts + parts / 4, false, s);
 }
 
 }  // namespace
@@ -167,9 +181,9 @@ kvb_status kvb_cache8_attention(kvb_ctx* c, const kvb_cache8* cache, const kvb_s
     if (static_cast<double>(p.units) * (p.tensor ? 8 : 1) > most || p.tiles > most || static_cast<double>(a.q.max_tokens) * a.g > most)
         return fail(KVB_ERR_UNSUPPORTED, "kvb_cache8_attention: more query rows, sequences, layers or keys than one call takes (2^30 tiles of 64 keys)");
     if ((st = ensure_attn_ws(c, p, s)) != KVB_OK) return st;
-    a.counters = static_cast<int*>(c->attn_ws);  // the tcgen05 kernel has no use for them
-    a.shared_by = reinterpret_cast<int2*>(static_cast<char*>(c->attn_ws) + c->attn_ws_counters + p.partial_bytes);
-    a.partial = reinterpret_cast<float*>(static_cast<char*>(c->attn_ws) + c->attn_ws_counters);
+    a.counters = static_cast<int*>(c->attn_counters);  // the tcgen05 kernel has no use for them
+    a.partial = static_cast<float*>(c->attn_parts);
+    a.shared_by = reinterpret_cast<int2*>(static_cast<char*>(c->attn_parts) + p.partial_bytes);
     a.part_stat = reinterpret_cast<float4*>(a.partial + static_cast<size_t>(p.slots) * p.rows * c->d);
     a.row_blocks = p.row_blocks;
     a.min_tiles = p.min_tiles;

@@ -192,7 +192,9 @@ kvb_status kvb_ctx_destroy(kvb_ctx* c) {
     cudaFree(c->scratch);
     cudaFree(c->err_dev);
     cudaFree(c->strip_ctr);
-    cudaFree(c->attn_ws);
+    cudaFree(c->attn_counters);
+    cudaFree(c->attn_parts);
+    for (void* p : c->attn_outgrown) cudaFree(p);
     if (c->err_mirror) cudaFreeHost(c->err_mirror);
     for (auto& r : c->prof) {
         cudaEventDestroy(r.start);

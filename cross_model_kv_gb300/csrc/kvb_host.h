@@ -21,9 +21,12 @@ struct kvb_ctx {
     int* err_dev = nullptr;    // error word written by kernels
     int* strip_ctr = nullptr;  // [4]: next / finished chunk of the strip fused into the map kernel, next map tile
     int* err_mirror = nullptr; // pinned host copy, refreshed after each call
-    void* attn_ws = nullptr;   // 8-bit cache attention: arrival counters (kept at 0 between calls), then partials
-    size_t attn_ws_bytes = 0;
-    size_t attn_ws_counters = 0;  // how many counters the workspace starts with
+    // 8-bit cache attention: arrival counters (kept at 0 between calls) and partial results.  Each
+    // only grows; what it outgrew lives on, since captured graphs hold its address.
+    void* attn_counters = nullptr;
+    void* attn_parts = nullptr;
+    size_t attn_counters_bytes = 0, attn_parts_bytes = 0;
+    std::vector<void*> attn_outgrown;
     // kernel timing (kvb_profile_enable / kvb_profile_read)
     struct ProfRec {
         const char* name;

@@ -408,9 +408,11 @@ kvb_status kvb_cache8_read(kvb_ctx* ctx, const kvb_cache8* cache, const kvb_seqs
  * row's largest element) or as an fp16 pair (fp32: 22 bits), probabilities as
  * fp16 (bf16) or an fp16 pair (fp32).  The result does not depend on timing.
  * Calls whose layers x sequences x heads x keys make 2^30 tiles of 64 keys or
- * more are refused.  Workspace (partial outputs where keys are
- * split) belongs to the context and grows on demand, which synchronises: make
- * a call of the largest size before capturing a stream.
+ * more are refused.  Workspace (partial outputs where keys are split) belongs to
+ * the context and grows on demand.  It cannot grow on a stream that is being
+ * captured (KVB_ERR_UNSUPPORTED): make each call once before capturing it.  What
+ * a later call outgrows is kept until the context is destroyed, so that captured
+ * graphs stay valid.
  */
 kvb_status kvb_cache8_attention(kvb_ctx* ctx, const kvb_cache8* cache, const kvb_seqs* seqs, int32_t l_begin,
                                 int32_t n_layers, kvb_dtype dtype, const void* q, int32_t n_q_heads, int64_t T,
