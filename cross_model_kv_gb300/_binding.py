@@ -179,6 +179,7 @@ class Ctx:
         self.L_s, self.L_t = src.n_layers, tgt.n_layers
         self.H, self.d, self.k = src.n_kv_heads, src.head_dim, top_k
         self.max_pos, self.device = max_pos, device
+        self.cache8_of = (self.L_t, self.H, self.d)  # sizes that an 8-bit cache must have
 
     def __del__(self):
         if getattr(self, "handle", None) and _lib is not None:
@@ -371,7 +372,7 @@ class Cache8:
     def __init__(self, ctx: Ctx, k, v, k_scale, v_scale):
         import torch
         L, n_pages, H, page, d = k.shape
-        if (L, H, d) != (ctx.L_t, ctx.H, ctx.d):
+        if (L, H, d) != ctx.cache8_of:
             raise ValueError(f"cache8 codes must be [{ctx.L_t}][n_pages][{ctx.H}][page_tokens][{ctx.d}], got "
                              f"{list(k.shape)}")
         for t in (k, v):
@@ -381,6 +382,7 @@ class Cache8:
             if tuple(t.shape) != (L, n_pages, H) or t.dtype != torch.float32:
                 raise ValueError(f"cache8 scales must be float32 [{L}][{n_pages}][{H}]")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.of = ctx.cache8_of  # the calls index with their context's sizes
         self.n_pages, self.page_tokens = int(n_pages), int(page)
         self.struct = kvb_cache8(self.page_tokens, self.n_pages, _dev(k), _dev(v), _dev(k_scale), _dev(v_scale))
         self.ref = ctypes.addressof(self.struct)
@@ -451,7 +453,14 @@ def _same_as(name, t, shape, dtype):
         raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
 
 
+def _misfit(ctx, cache):
+    return ValueError(f"the cache was made for another context: [L_tgt, KV heads, head_dim] {list(cache.of)}, the call's "
+                      f"{list(ctx.cache8_of)}")
+
+
 def _cache8_rw(call, ctx: Ctx, cache: Cache8, seqs: Seqs, k, v, l_begin, stream):
+    if cache.of != ctx.cache8_of:
+        raise _misfit(ctx, cache)
     shape = k.shape
     if len(shape) != 4 or shape[1] != ctx.H or shape[3] != ctx.d:
         raise ValueError(f"k must be [n_layers][{ctx.H}][T][{ctx.d}], got {list(shape)}")
@@ -479,6 +488,8 @@ def kvb_cache8_attention(ctx: Ctx, cache: Cache8, seqs: Seqs, q, out, lse=None, 
     Token i of a sequence is at position seq_pos + i and sees the cache positions up
     to its own (and below kv_len where that is given).  scale 0 is 1/sqrt(d).
     """
+    if cache.of != ctx.cache8_of:
+        raise _misfit(ctx, cache)
     shape, dtype = q.shape, q.dtype
     if len(shape) != 4 or shape[3] != ctx.d:
         raise ValueError(f"q must be [n_layers][Hq][T][{ctx.d}], got {list(shape)}")

@@ -1,9 +1,9 @@
 """The 8-bit cache at the edges of what its calls accept: how the buffers are
-aligned, and positions up to the last that a call may name."""
+aligned, positions up to the last that a call may name, caches of other sizes."""
 import numpy as np
 import pytest
 
-from cases import to_host64
+from cases import spec, to_host64
 from test_gpu_cache8 import BF, F32, Pool, i32, kvb, offsets  # noqa: F401  (kvb: the fixture)
 
 torch = pytest.importorskip("torch")
@@ -110,3 +110,30 @@ def test_more_positions_are_refused(kvb):  # noqa: F811
         for max_kv in (0, 0x7ffffc01, 0x7fffffff):
             assert status(call, most + 1, max_kv) == 3
     kvb.kvb_ctx_check(P.ctx)
+
+
+# ------------------------------------------------------------------ one cache, several contexts
+
+def test_a_cache_of_another_context_s_sizes_is_refused(kvb):  # noqa: F811
+    # the library sees bare pointers: only the binding can tell that a cache has other sizes than
+    # the context that a call is made with
+    def tensors(L, H, d):
+        k = torch.zeros((L, H, 1, d), dtype=BF, device="cuda")
+        return k, torch.zeros_like(k)
+
+    def calls(ctx, cache, L, H, d):
+        k, v = tensors(L, H, d)
+        s = kvb.Seqs(i32([[0]]), i32([0, 1]), i32([0]), max_tokens=1)
+        return (lambda: kvb.kvb_cache8_write(ctx, cache, s, k, v), lambda: kvb.kvb_cache8_read(ctx, cache, s, k, v),
+                lambda: kvb.kvb_cache8_attention(ctx, cache, s, k, v))
+
+    make = lambda L, H, d: kvb.kvb_ctx_create(spec(1, H, d, 1e6), spec(L, H, d, 1e6), 1, 64)
+    cache = kvb.kvb_cache8_create(make(2, 2, 64), 1, 16)
+    for L, H, d in ((3, 2, 64), (1, 2, 64), (2, 4, 64), (2, 1, 64), (2, 2, 128), (2, 2, 32)):
+        for f in calls(make(L, H, d), cache, L, H, d):
+            with pytest.raises(ValueError, match="another context"):
+                f()
+    twin = make(2, 2, 64)  # of the same sizes: as good as its own
+    for f in calls(twin, cache, 2, 2, 64):
+        f()
+    kvb.kvb_ctx_check(twin)
