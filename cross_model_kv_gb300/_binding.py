@@ -487,6 +487,8 @@ def kvb_cache8_attention(ctx: Ctx, cache: Cache8, seqs: Seqs, q, out, lse=None, 
 
     Token i of a sequence is at position seq_pos + i and sees the cache positions up
     to its own (and below kv_len where that is given).  scale 0 is 1/sqrt(d).
+    Calls with one ctx share its workspace and must not overlap on the GPU: use one ctx
+    per concurrent stream (they may share a cache).
     """
     if cache.of != ctx.cache8_of:
         raise _misfit(ctx, cache)

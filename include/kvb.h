@@ -413,6 +413,12 @@ kvb_status kvb_cache8_read(kvb_ctx* ctx, const kvb_cache8* cache, const kvb_seqs
  * captured (KVB_ERR_UNSUPPORTED): make each call once before capturing it.  What
  * a later call outgrows is kept until the context is destroyed, so that captured
  * graphs stay valid.
+ * Attention calls on one context share that workspace: issue them, and replay
+ * graphs that hold them, on one stream, or order them, never overlapping on the
+ * GPU.  Calls that overlap mix their partial results, and leave counters behind
+ * that spoil later calls too.  Use one context per concurrent stream; contexts of
+ * one geometry may share a cache.  (kvb_cache8_write and kvb_cache8_read have no
+ * workspace.)
  */
 kvb_status kvb_cache8_attention(kvb_ctx* ctx, const kvb_cache8* cache, const kvb_seqs* seqs, int32_t l_begin,
                                 int32_t n_layers, kvb_dtype dtype, const void* q, int32_t n_q_heads, int64_t T,

@@ -1,7 +1,9 @@
 """The attention workspace of a context: it grows without taking away what captured
-graphs hold, and calls of different kinds share it without growing it in turn."""
+graphs hold, calls of different kinds share it without growing it in turn, and calls that
+overlap have a context each."""
 import pytest
 
+from cases import spec
 from test_gpu_cache8 import BF, UNSUPPORTED, Pool, i32, kvb, offsets, status_of  # noqa: F401  (kvb: the fixture)
 
 torch = pytest.importorskip("torch")
@@ -92,3 +94,45 @@ def test_growing_on_a_captured_stream_is_refused_and_the_capture_goes_on(kvb):  
     for _ in range(2):
         assert torch.equal(run["many"]()[0], want)
     kvb.kvb_ctx_check(P.ctx)
+
+
+def test_a_context_for_each_stream_and_one_context_on_ordered_streams(kvb):  # noqa: F811
+    P = Pool(kvb, 1, 2, 128, 16, 1, 3000)
+    P.fill([3000])
+    run = kinds(P)
+    want = {}
+    for name in run:
+        want[name] = [t.clone() for t in run[name]()]
+    torch.cuda.synchronize()
+
+    last = {}
+
+    def check(names):
+        torch.cuda.synchronize()
+        for name in names:
+            assert all(torch.equal(a, b) for a, b in zip(last[name], want[name])), name
+
+    # two contexts of one geometry over one cache, their calls side by side
+    s = spec(1, 2, 128, 1e6)
+    other = kvb.kvb_ctx_create(s, s, 1, 64)
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    for a, b in (("many", "prompt"), ("few", "counters"), ("prompt", "many")):
+        for _ in range(20):
+            for ctx, name, stream in ((P.ctx, a, streams[0]), (other, b, streams[1])):
+                with torch.cuda.stream(stream):
+                    last[name] = run[name](ctx)
+        check((a, b))
+    # one context, its calls on two streams in turn, each after the one before
+    done = torch.cuda.Event()
+    done.record()
+    for i in range(20):
+        for j, name in enumerate(run):
+            stream = streams[(i + j) % 2]
+            stream.wait_event(done)
+            with torch.cuda.stream(stream):
+                last[name] = run[name]()
+                done = torch.cuda.Event()
+                done.record()
+    check(run)
+    kvb.kvb_ctx_check(P.ctx)
+    kvb.kvb_ctx_check(other)
