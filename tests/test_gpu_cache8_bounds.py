@@ -137,3 +137,26 @@ def test_a_cache_of_another_context_s_sizes_is_refused(kvb):  # noqa: F811
     for f in calls(twin, cache, 2, 2, 64):
         f()
     kvb.kvb_ctx_check(twin)
+
+
+# ------------------------------------------------------------------ no time to wait
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_limit_of_no_time_runs_out_every_time(kvb, d, monkeypatch):  # noqa: F811
+    # the prompt kernel over one key and over many, again and again: never a matter of which warp is first
+    P = Pool(kvb, 1, 1, d, 16, 1, 2000)
+    P.fill([2000])
+    q = torch.randn(1, 60, 1, d, device="cuda").to(BF)
+    out = torch.empty_like(q)
+    monkeypatch.setenv("KVB_WAIT_TIMEOUT_MS", "0")
+    ctx0 = kvb.kvb_ctx_create(spec(1, 1, d, 1e6), spec(1, 1, d, 1e6), 1, 64)
+    monkeypatch.delenv("KVB_WAIT_TIMEOUT_MS")
+    for pos in [0, 1999] * 25:
+        kvb.kvb_cache8_attention(ctx0, P.cache, P.seqs([0, 1], [pos]), q, out)
+        with pytest.raises(kvb.KvbError) as e:
+            kvb.kvb_ctx_check(ctx0)
+        assert e.value.status == 7
+    kvb.kvb_cache8_attention(P.ctx, P.cache, P.seqs([0, 1], [0]), q, out)
+    kvb.kvb_ctx_check(P.ctx)
+    v = torch.from_numpy(P.ref.sequence(1, P.table[0], 1, 0, 0)).to(BF).cuda()  # one key: its value
+    assert torch.equal(out[0, :, 0], v.expand(60, d))
