@@ -33,6 +33,8 @@
 // keys: about 4.6 us a CTA.)  The last CTA to arrive at a unit that several share
 // joins its pieces in order, so results do not depend on timing.
 // 32 sequences of 32768 keys, one token each, 64 query and 8 KV heads: 334 us, 6.4 TB/s.
+#include <cfloat>
+
 #include "cache8_attn.cuh"
 
 namespace kvb {
@@ -272,6 +274,11 @@ __global__ void __launch_bounds__(NWARPS * 32, NWARPS == WARPS ? resident_ctas(s
             qs[b][j] = sqs[row];
             qpos[b][j] = row < nrows ? B.pos + (row0 + row) / P.g : INT32_MIN;
         }
+    // keys up to whole_to need no look at their scores, unless a row's factor could pass fp32
+    bool wide = false;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) wide |= fmaxf(qs[b][0], qs[b][1]) > WIDE_QUERY;
+    const int whole_to = __any_sync(0xffffffffu, wide) ? INT32_MIN : B.pos_lo;
     uint32_t qf[NB * PARTS == 1 ? KS : 1][2];  // in registers where one fragment set serves
     if constexpr (NB * PARTS == 1) {
 #pragma unroll
@@ -335,7 +342,7 @@ __global__ void __launch_bounds__(NWARPS * 32, NWARPS == WARPS ? resident_ctas(s
         if (jn < listed) load_k(jn, kw);
         if (D == 128) ahead(jn + TILE_KEYS, listed);
         // scores in base 2, masked; keys r, r + 8 and query rows 2c, 2c + 1 of each row block
-        const bool whole = !bad && j + 16 <= k1 && j + 15 <= B.pos_lo;
+        const bool whole = !bad && j + 16 <= k1 && j + 15 <= whole_to;
         bool raise = false;
 #pragma unroll
         for (int b = 0; b < NB; ++b)
@@ -343,6 +350,7 @@ __global__ void __launch_bounds__(NWARPS * 32, NWARPS == WARPS ? resident_ctas(s
             for (int u = 0; u < 4; ++u) {
                 float x = sc[b][u] * (ks * qs[b][u & 1]);
                 if (!whole) {
+                    x = sc[b][u] * fminf(ks * qs[b][u & 1], FLT_MAX);  // a score of 0 stays 0
                     const int key = j + r + 8 * (u >> 1);
                     if (bad || key >= k1 || key > qpos[b][u & 1]) x = -INFINITY;
                 }

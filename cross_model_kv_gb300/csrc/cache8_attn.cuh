@@ -9,6 +9,7 @@ namespace c8 {
 constexpr float BIAS = 7.f;    // weights are taken against 2^-7 of the reference
 constexpr float MARGIN = 8.f;  // a reference is raised past this much (base 2)
 constexpr float NO_REF = -3.0e38f;
+constexpr float WIDE_QUERY = 256.f;  // a row's factor above this may pass fp32 with a key scale (2^119 at most)
 constexpr int MIN_TILES = 4;       // a CTA's least share of the line of tiles, but for few keys
 constexpr int PREFILL_ROWS = 256;  // rows of a unit in the tcgen05 kernel
 

@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
                 }
                 const int eq = max((__float_as_int(amax) >> 23) - 127, -100) - 13;
                 const float inv = pow2(-eq);
-                qs = pow2(eq) * P.scale_log2;
+                qs = fminf(pow2(eq) * P.scale_log2, FLT_MAX);
 #pragma unroll
                 for (int c = 0; c < HD / 8; ++c) {
                     const uint32_t w[4] = {u[c].x, u[c].y, u[c].z, u[c].w};
@@ -343,6 +343,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
             }
             // keys below `see` are visible to this row
             const int see = valid ? min(k1, G.B.pos + (G.B.row0 + brow) / P.g + 1) : 0;
+            const bool wide = __any_sync(0xffffffffu, qs > WIDE_QUERY) != 0;
             for (int u = 0; u < nsteps; ++u) {
                 const uint32_t gt = base + (u >> 1), ring = gt & (INFO_RING - 1);
                 const int hf = u & 1;
@@ -356,7 +357,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
                 tmem_ld32(cS, sv);
                 tmem_ld32(cS + 32, sv + 32);
                 const TileInfo& I = M.info[ring];
-                const float4 ks4 = *reinterpret_cast<const float4*>(I.ks + 4 * hf), ev4 = *reinterpret_cast<const float4*>(I.ev + 4 * hf);
+                float4 ks4 = *reinterpret_cast<const float4*>(I.ks + 4 * hf);
+                const float4 ev4 = *reinterpret_cast<const float4*>(I.ev + 4 * hf);
+                if (wide) {  // a factor past the range of fp32 would make NaN of a score of 0
+                    const float most = 1e38f / fmaxf(qs, 1.f);
+                    ks4 = make_float4(fminf(ks4.x, most), fminf(ks4.y, most), fminf(ks4.z, most), fminf(ks4.w, most));
+                }
                 const float ev[4] = {ev4.x, ev4.y, ev4.z, ev4.w};
                 const float k[4] = {fmaxf(ks4.x * qs, FLT_MIN), fmaxf(ks4.y * qs, FLT_MIN), fmaxf(ks4.z * qs, FLT_MIN),
                                     fmaxf(ks4.w * qs, FLT_MIN)};

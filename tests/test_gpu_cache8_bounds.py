@@ -160,3 +160,28 @@ def test_a_limit_of_no_time_runs_out_every_time(kvb, d, monkeypatch):  # noqa: F
     kvb.kvb_ctx_check(P.ctx)
     v = torch.from_numpy(P.ref.sequence(1, P.table[0], 1, 0, 0)).to(BF).cuda()  # one key: its value
     assert torch.equal(out[0, :, 0], v.expand(60, d))
+
+
+# ------------------------------------------------------------------ products past the range of fp32
+
+@pytest.mark.parametrize("d,n,dtype", [(64, 1, BF), (128, 1, F32), (128, 9, BF), (64, 60, BF), (128, 60, BF)])
+def test_scores_of_zero_between_values_past_the_range_of_fp32(kvb, d, n, dtype):  # noqa: F811
+    # queries of 2^100 in the first dims, keys of 2^70 in the others: every product is 0, although
+    # the query's and the keys' scales together pass fp32.  The output is the mean of the values.
+    P = Pool(kvb, 1, 1, d, 16, 1, 200)
+    P.lens = np.asarray([200])
+    k = 2.0 ** 70 * P.rng.standard_normal((1, 1, 200, d))
+    k[..., :8] = 0
+    P.write([0, 200], [0], BF, x=[k, P.rng.standard_normal((1, 1, 200, d))])
+    q = np.zeros((1, 1, n, d))
+    q[..., :8] = 2.0 ** 100 * P.rng.standard_normal((1, 1, n, 8))
+    q = torch.from_numpy(q).to(dtype).cuda()
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:3], device="cuda")
+    kvb.kvb_cache8_attention(P.ctx, P.cache, P.seqs([0, n], [200 - n]), q, out, lse)
+    kvb.kvb_ctx_check(P.ctx)
+    v = P.ref.sequence(1, P.table[0], 200, 0, 0)
+    for i in range(n):
+        see = v[:200 - n + i + 1]
+        tol = 2.0 ** -8 * np.abs(see.mean(axis=0)) + 2.0 ** -10 * np.abs(see).mean(axis=0)
+        assert (np.abs(to_host64(out)[0, 0, i] - see.mean(axis=0)) <= tol).all()
+        assert abs(float(lse[0, 0, i]) - np.log(len(see))) <= 2.0 ** -16
