@@ -65,6 +65,7 @@ struct AttnParams {
     int2* shared_by;    // [units], tcgen05 kernel: CTAs that share the unit, the first of them
     float* partial;     // [slots][rows][d] outputs in units of 2^mv
     float4* part_stat;  // [slots][rows] (m, mv, sum, -)
+    int64_t units, slots;
     Err err;
 };
 
@@ -97,6 +98,10 @@ __device__ __forceinline__ bool check_bounds(const Err& e, int64_t first, int64_
     if (first >= 0 && count >= 0 && first + count <= size) return true;
     err_set(e, DEV_ERR_BOUNDS);
     return false;
+}
+// Entry p of sequence s's row of the page table.
+__device__ __forceinline__ bool table_in_bounds(const Seqs& q, const Err& e, int s, int64_t p) {
+    return KVB_IN_BOUNDS(e, s, 1, q.n_seq) && KVB_IN_BOUNDS(e, p, 1, q.max_pages);
 }
 // Blocks (layer, page, head) that a call may touch.
 __device__ __forceinline__ int64_t blocks_of(const Cache& c) {
@@ -146,6 +151,7 @@ struct SeqView {
     int tok0, n, pos;
 };
 __device__ __forceinline__ SeqView seq_view(const Seqs& q, int s, const Err& err) {
+    if (!KVB_IN_BOUNDS(err, s, 1, q.n_seq)) return SeqView{};
     const int a = __ldg(q.off + s), b = __ldg(q.off + s + 1);
     SeqView v{a, a < 0 || b < a ? 0 : b - a, __ldg(q.pos + s)};
     if (a < 0 || b < a || b > q.T || v.n > q.max_tokens || v.pos > 0x7fffffff - v.n) {

@@ -185,6 +185,8 @@ kvb_status kvb_cache8_attention(kvb_ctx* c, const kvb_cache8* cache, const kvb_s
     a.partial = static_cast<float*>(c->attn_parts);
     a.shared_by = reinterpret_cast<int2*>(static_cast<char*>(c->attn_parts) + p.partial_bytes);
     a.part_stat = reinterpret_cast<float4*>(a.partial + static_cast<size_t>(p.slots) * p.rows * c->d);
+    a.units = p.units;
+    a.slots = p.slots;
     a.row_blocks = p.row_blocks;
     a.min_tiles = p.min_tiles;
     ProfScope ps(c, s, p.tensor ? "cache8_attention_tcgen05" : "cache8_attention");

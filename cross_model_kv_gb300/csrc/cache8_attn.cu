@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(NWARPS * 32, NWARPS == WARPS ? resident_ctas(s
         const int end = k1 - k > span ? k + span : k1;  // k + span may pass 2^31
         const int npages = end > k ? ((end - 1) >> P.c.page_log2) - page0 + 1 : 0;
         for (int i = threadIdx.x; i < npages; i += NT) {
-            int pid = __ldg(P.q.page_table + static_cast<int64_t>(s) * P.q.max_pages + page0 + i);
+            int pid = table_in_bounds(P.q, P.err, s, page0 + i) ? __ldg(P.q.page_table + static_cast<int64_t>(s) * P.q.max_pages + page0 + i) : -1;
             if (pid < 0 || pid >= P.c.n_pages) {
                 err_set(P.err, DEV_ERR_BAD_SEQ);
                 pid = -1;
@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(NWARPS * 32, NWARPS == WARPS ? resident_ctas(s
         if (pieces == 1) {
             store_out(out + row_of(row) * D + 4 * d4, z.output());
             if (d4 == 0 && P.lse) P.lse[row_of(row)] = z.lse();
-        } else {
+        } else if (KVB_IN_BOUNDS(P.err, part0 + row, 1, P.slots * ROWS)) {
             reinterpret_cast<float4*>(P.partial + (part0 + row) * D)[d4] = z.acc;
             if (d4 == 0) P.part_stat[part0 + row] = make_float4(z.m, z.mv, z.sum, 0.f);
         }

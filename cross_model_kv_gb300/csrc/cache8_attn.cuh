@@ -174,6 +174,11 @@ struct Pieces {
     __device__ __forceinline__ int64_t slot(int i) const { return i == 0 ? 2 * c0 + 1 : 2 * (c0 + i); }
 };
 
+// All of them (the checked build).
+__device__ __forceinline__ bool pieces_in_bounds(const AttnParams& P, const Pieces& pieces) {
+    return KVB_IN_BOUNDS(P.err, pieces.slot(0), 1, P.slots) && KVB_IN_BOUNDS(P.err, pieces.slot(pieces.n - 1), 1, P.slots);
+}
+
 // Parts of one row's result, each with its references: first every part's
 // reference(), then every part's add().  st = (m, mv, sum, -).  A part that saw
 // nothing has NO_REF references and adds zeros; a NaN reaches the result.
@@ -215,9 +220,12 @@ __device__ __forceinline__ void join_splits(const AttnParams& P, const RowBlock&
     __threadfence();
     __syncthreads();
     if (threadIdx.x == 0) {
-        const int n = atomicAdd(P.counters + unit, 1);
-        *s_last = n == pieces.n - 1;
-        if (n == pieces.n - 1) P.counters[unit] = 0;
+        *s_last = false;
+        if (KVB_IN_BOUNDS(P.err, unit, 1, P.units) && pieces_in_bounds(P, pieces)) {
+            const int n = atomicAdd(P.counters + unit, 1);
+            *s_last = n == pieces.n - 1;
+            if (n == pieces.n - 1) P.counters[unit] = 0;
+        }
     }
     __syncthreads();
     if (!*s_last) return;

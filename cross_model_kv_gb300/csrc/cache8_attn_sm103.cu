@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
         g.unit = (static_cast<int64_t>(W.l) * entries + W.e) * P.c.H + W.h;
         g.pieces = Pieces{(u0 + tiles - 1) / W.share - c0 + 1, c0};
         g.whole = g.pieces.n == 1;
-        P.shared_by[g.unit] = make_int2(g.pieces.n, g.pieces.c0);  // every CTA of the unit the same
+        if (KVB_IN_BOUNDS(P.err, g.unit, 1, P.units)) P.shared_by[g.unit] = make_int2(g.pieces.n, g.pieces.c0);  // every CTA of the unit the same
         g.slot = 2 * static_cast<int64_t>(blockIdx.x) + (W.first == 0);
         M.more[i] = 1;
         W.at += last - W.first;
@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
                     uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(P.out) + out_row * HD + c0);
                     dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
                     dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-                } else if (valid) {
+                } else if (valid && KVB_IN_BOUNDS(P.err, part, 1, P.slots * ROWS)) {
                     uint4* dst = reinterpret_cast<uint4*>(P.partial + part * HD + c0);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) dst[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
@@ -494,8 +494,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
                 __syncwarp();
             }
             if (valid) {
-                if (!G.whole) P.part_stat[part] = make_float4(m, mv, sum, 0.f);
-                else if (P.lse) P.lse[out_row] = sum == 0.f ? -INFINITY : (m - BIAS + log2f(sum)) * 0.693147180559945f;
+                if (!G.whole) {
+                    if (KVB_IN_BOUNDS(P.err, part, 1, P.slots * ROWS)) P.part_stat[part] = make_float4(m, mv, sum, 0.f);
+                } else if (P.lse) P.lse[out_row] = sum == 0.f ? -INFINITY : (m - BIAS + log2f(sum)) * 0.693147180559945f;
             }
             tc_fence_before();
             __syncthreads();  // the segment is done, the next one worked out
@@ -524,10 +525,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
             uint4 raw[N];  // of the tile that is converted next
             int pid[N];    // pages of the tile after it
             auto page = [&](int t, int i) {
-                int p;
-                asm volatile("ld.global.u32 %0, [%1];"
-                             : "=r"(p)
-                             : "l"(table + (min(k0 + t * TK + RP * i + (RP > 16 ? rr : 0), last) >> P.c.page_log2)));
+                int p = -1;
+                const int at = min(k0 + t * TK + RP * i + (RP > 16 ? rr : 0), last) >> P.c.page_log2;
+                if (table_in_bounds(P.q, P.err, G.s, at)) asm volatile("ld.global.u32 %0, [%1];" : "=r"(p) : "l"(table + at));
                 return p;
             };
             auto load = [&](int t, int i, int p) {
@@ -555,12 +555,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
             auto group_page = [&](int t) {
                 const int j = k0 + t * TK + 16 * tid;
                 in_range = j < k1;
-                gp = in_range ? __ldg(table + (j >> P.c.page_log2)) : -1;
+                gp = in_range && table_in_bounds(P.q, P.err, G.s, j >> P.c.page_log2) ? __ldg(table + (j >> P.c.page_log2)) : -1;
             };
             auto scales = [&] {
-                const bool have = gp >= 0 && gp < P.c.n_pages;
-                if (in_range && !have) err_set(P.err, DEV_ERR_BAD_SEQ);
                 const int64_t blk = block0 + static_cast<int64_t>(gp) * P.c.H;
+                const bool have = gp >= 0 && gp < P.c.n_pages && KVB_IN_BOUNDS(P.err, blk, 1, blocks_of(P.c));
+                if (in_range && !have) err_set(P.err, DEV_ERR_BAD_SEQ);
                 ks = load4_if(P.c.scale[0] + blk, have);  // not looked at before the next tile
                 vs = load4_if(P.c.scale[1] + blk, have);
             };
@@ -711,9 +711,11 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnP
     const RowBlock B = row_block(P, e / P.row_blocks, e % P.row_blocks, ROWS);
     const int row0 = (blockIdx.x % PER) * JOIN_ROWS;
     if (row0 >= B.nrows) return;
+    if (!KVB_IN_BOUNDS(P.err, unit, 1, P.units)) return;
     const int2 by = P.shared_by[unit];
     if (by.x <= 1) return;
     const Pieces pieces{by.x, by.y};
+    if (!pieces_in_bounds(P, pieces)) return;
     for (int row = row0 + warp; row < min(row0 + JOIN_ROWS, B.nrows); row += 8) {
         auto stat = [&](int i) { return P.part_stat[pieces.slot(i) * ROWS + row]; };
         Joined z;

@@ -115,7 +115,7 @@ __device__ __forceinline__ bool place_of(const RwParams& P, const Item& it, bool
     o.m = static_cast<int>(min(static_cast<int64_t>(pos) + sv.n - p0, static_cast<int64_t>(P.c.page))) - o.lo;
     if (o.m <= 0) return false;
     o.row = (static_cast<int64_t>(it.l) * P.c.H + it.h) * P.q.T + sv.tok0 + (p0 + o.lo - pos);
-    const int pid = logical < P.q.max_pages ? __ldg(P.q.page_table + static_cast<int64_t>(it.s) * P.q.max_pages + logical) : -1;
+    const int pid = logical < P.q.max_pages && table_in_bounds(P.q, P.err, it.s, logical) ? __ldg(P.q.page_table + static_cast<int64_t>(it.s) * P.q.max_pages + logical) : -1;
     const bool bad = pid < 0 || pid >= P.c.n_pages || sv.pos < 0;
     if (bad && report) err_set(P.err, DEV_ERR_BAD_SEQ);
     o.block = bad ? -1 : ((static_cast<int64_t>(P.c.l_begin) + it.l) * P.c.n_pages + pid) * P.c.H + it.h;
