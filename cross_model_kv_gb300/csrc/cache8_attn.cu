@@ -348,9 +348,10 @@ __global__ void __launch_bounds__(NWARPS * 32, NWARPS == WARPS ? resident_ctas(s
         for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                float x = sc[b][u] * (ks * qs[b][u & 1]);
+                float f = ks * qs[b][u & 1];
+                if (!whole) f = fminf(f, FLT_MAX);  // a score of 0 stays 0
+                float x = sc[b][u] * f;
                 if (!whole) {
-                    x = sc[b][u] * fminf(ks * qs[b][u & 1], FLT_MAX);  // a score of 0 stays 0
                     const int key = j + r + 8 * (u >> 1);
                     if (bad || key >= k1 || key > qpos[b][u & 1]) x = -INFINITY;
                 }

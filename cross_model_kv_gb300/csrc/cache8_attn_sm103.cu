@@ -343,7 +343,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
             }
             // keys below `see` are visible to this row
             const int see = valid ? min(k1, G.B.pos + (G.B.row0 + brow) / P.g + 1) : 0;
-            const bool wide = __any_sync(0xffffffffu, qs > WIDE_QUERY) != 0;
+            // a step's visible keys that need no look at their scores: none where a factor could pass fp32
+            const int full = qs > WIDE_QUERY ? INT32_MAX : SK;
             for (int u = 0; u < nsteps; ++u) {
                 const uint32_t gt = base + (u >> 1), ring = gt & (INFO_RING - 1);
                 const int hf = u & 1;
@@ -357,21 +358,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_kernel(const __grid_co
                 tmem_ld32(cS, sv);
                 tmem_ld32(cS + 32, sv + 32);
                 const TileInfo& I = M.info[ring];
-                float4 ks4 = *reinterpret_cast<const float4*>(I.ks + 4 * hf);
+                const float4 ks4 = *reinterpret_cast<const float4*>(I.ks + 4 * hf);
                 const float4 ev4 = *reinterpret_cast<const float4*>(I.ev + 4 * hf);
-                if (wide) {  // a factor past the range of fp32 would make NaN of a score of 0
-                    const float most = 1e38f / fmaxf(qs, 1.f);
-                    ks4 = make_float4(fminf(ks4.x, most), fminf(ks4.y, most), fminf(ks4.z, most), fminf(ks4.w, most));
-                }
                 const float ev[4] = {ev4.x, ev4.y, ev4.z, ev4.w};
-                const float k[4] = {fmaxf(ks4.x * qs, FLT_MIN), fmaxf(ks4.y * qs, FLT_MIN), fmaxf(ks4.z * qs, FLT_MIN),
-                                    fmaxf(ks4.w * qs, FLT_MIN)};
+                float k[4] = {ks4.x * qs, ks4.y * qs, ks4.z * qs, ks4.w * qs};
                 // visible keys of this row are a prefix of the step's
                 const int nvis = min(see - (k0 + u * SK), SK);
-                const bool whole = nvis == SK && ks4.x != 0.f && ks4.y != 0.f && ks4.z != 0.f && ks4.w != 0.f;
+                const bool whole = nvis == full && ks4.x != 0.f && ks4.y != 0.f && ks4.z != 0.f && ks4.w != 0.f;
                 tmem_ld_wait();
                 if (!__all_sync(0xffffffffu, whole)) {
                     const float seen[4] = {ks4.x, ks4.y, ks4.z, ks4.w};
+#pragma unroll
+                    for (int gq = 0; gq < 4; ++gq) k[gq] = fminf(fmaxf(k[gq], FLT_MIN), FLT_MAX);  // of 0 and -inf: no NaN
 #pragma unroll
                     for (int j = 0; j < SK; ++j)
                         if (j >= nvis || seen[j >> 4] == 0.f) sv[j] = 0xff800000u;  // -inf
