@@ -32,7 +32,8 @@
 // 512 / 2048 keys as CTAs of their own took 588 / 402 us for 32 sequences of 32768
 // keys: about 4.6 us a CTA.)  The last CTA to arrive at a unit that several share
 // joins its pieces in order, so results do not depend on timing.
-// 32 sequences of 32768 keys, one token each, 64 query and 8 KV heads: 334 us, 6.4 TB/s.
+// 32 sequences of 32768 keys, one token each, 64 query and 8 KV heads: 338 us a call, 336
+// replayed from a graph, 6.4 TB/s (0.94 of the copy rate).
 #include <cfloat>
 
 #include "cache8_attn.cuh"
@@ -93,8 +94,9 @@ __device__ __forceinline__ float2 load2(const __nv_bfloat16* p) {
 }
 __device__ __forceinline__ float2 load2(const float* p) { return __ldg(reinterpret_cast<const float2*>(p)); }
 // CTAs to keep on an SM: what the accumulators (D/4 registers a row block) and the
-// 64 bytes of codes in flight leave; the rest of a thread's state may spill, it is
-// not used inside the key loop.
+// 64 bytes of codes in flight leave.  What spills for that: bf16, D 128, 8 rows: set-up only
+// (counted: 0.1 reloads for each 16 keys of a warp); 16 rows: about 10 of the 447 instructions
+// for each 16 keys are reloads, which a third CTA on the SM outweighs.
 constexpr int resident_ctas(size_t element, int D, int NB) {
     return D < 64 ? 4 : (NB == 1 ? 4 : 3) - (D == 128 && element == 4 ? 1 : 0);
 }
@@ -302,7 +304,7 @@ __global__ void __launch_bounds__(NWARPS * 32, NWARPS == WARPS ? resident_ctas(s
     }
 
     // the codes of 16 keys a step further ahead on their way to L2, by one lane for K and one for
-    // V: more in flight than the registers hold.  32 sequences of 32768 keys: 348 us without, 334 with
+    // V: more in flight than the registers hold.  32 sequences of 32768 keys (graph): 348 us without, 334 with
     // one step, 347 and 498 with four and eight; head_dim 64, two steps in registers, gains nothing
     auto ahead = [&](int j, int listed) {
         if (j < listed && lane < 2) {

@@ -14,7 +14,7 @@
 //                 out as operands, keys and values alike: 128-byte swizzle, key rows,
 //                 K-major for S and MN-major for O;
 //                 also the scales of the tile's 16-key groups and the CTA's next piece;
-//   warps 16, 17  one lane each issues S_x = Q_x K^T for tile x;
+//   warps 16, 17  one lane of each issues S_x = Q_x K^T for tile x;
 //   warps 18, 19  and O_x += P_x V (P from TMEM): four warps, so that no product
 //                 waits behind a wait of another kind.
 // TMEM: score buffer b of tile x at 128 x + 64 b, O_x at 256 + 128 x.  P takes its
@@ -27,8 +27,8 @@
 // The weights carry the value scale, w = 2^(s + e_v - mv); a 16-key group's sum goes
 // into the denominator with the factor 2^(mv - m - e_v), or is taken from
 // exponentials of its own where that factor could leave fp32's range.
-// 1024 tokens over 16K, 64 query and 8 KV heads: 495 us, 1.15 PF/s, about 4200 cycles for
-// each 128 keys of 256 rows.  No unit is full; the two tiles' chains S -> softmax -> P V
+// 1024 tokens over 16K, 64 query and 8 KV heads: 503 us a call, 497 replayed from a graph (the
+// steps' figures here are graph replays), 1.13 PF/s, about 4200 cycles for each 128 keys of 256 rows.  No unit is full; the two tiles' chains S -> softmax -> P V
 // hide most of each other's waits, not all.
 // Every wait is bounded; after one gives up, its role runs through the rest without
 // touching TMEM, meeting the others at every barrier.
