@@ -389,12 +389,15 @@ class Cache8:
 
 
 def kvb_cache8_create(ctx: Ctx, n_pages: int, page_tokens: int = 64) -> Cache8:
-    """Allocate a cache of n_pages pages for every target layer on the context's device."""
+    """Allocate a cache of n_pages pages for every target layer on the context's device.
+
+    Scales are 0, so that a sequence may begin inside a page; codes are not set.
+    """
     import torch
     dev = torch.device("cuda", ctx.device)
     shape = (ctx.L_t, int(n_pages), ctx.H, int(page_tokens), ctx.d)
     code = lambda: torch.empty(shape, dtype=torch.float8_e4m3fn, device=dev)
-    scale = lambda: torch.empty(shape[:3], dtype=torch.float32, device=dev)
+    scale = lambda: torch.zeros(shape[:3], dtype=torch.float32, device=dev)
     return Cache8(ctx, code(), code(), scale(), scale())
 
 

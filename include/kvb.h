@@ -333,7 +333,9 @@ kvb_status kvb_attention_cosine(kvb_ctx* ctx, kvb_dtype dtype, const void* q, in
  *   k_scale, v_scale device float32 [L_tgt][n_pages][H]
  * page_tokens is 16, 32, 64 or 128 and d (the context's) 16, 32, 64 or 128.
  * The caller owns the four buffers; they need no initial value, since only
- * slots that kvb_cache8_write has written are read.
+ * slots that kvb_cache8_write has written are read, with one exception: a block
+ * that is first written past its first slot takes its scale for an older one, so
+ * it has to be 0 (which counts as 2^-117) or a power of two.
  */
 typedef struct {
     int32_t page_tokens;

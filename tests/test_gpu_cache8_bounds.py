@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 
 from cases import spec, to_host64
+from oracle import cache8 as C8
 from test_gpu_cache8 import BF, F32, Pool, i32, kvb, offsets  # noqa: F401  (kvb: the fixture)
 
 torch = pytest.importorskip("torch")
@@ -185,3 +186,31 @@ def test_scores_of_zero_between_values_past_the_range_of_fp32(kvb, d, n, dtype):
         tol = 2.0 ** -8 * np.abs(see.mean(axis=0)) + 2.0 ** -10 * np.abs(see).mean(axis=0)
         assert (np.abs(to_host64(out)[0, 0, i] - see.mean(axis=0)) <= tol).all()
         assert abs(float(lse[0, 0, i]) - np.log(len(see))) <= 2.0 ** -16
+
+
+# ------------------------------------------------------------------ a page begun in its middle
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("d,page,pos,n", [(64, 32, 13, 5), (128, 64, 63, 1), (128, 16, 7, 40), (16, 128, 100, 20)])
+def test_a_sequence_that_begins_inside_a_page(kvb, d, page, pos, n, dtype):  # noqa: F811
+    # a new cache holds no older scale: its first tokens decide, wherever in the page they lie, although
+    # the memory that it gets was another's
+    ctx = kvb.kvb_ctx_create(spec(1, 2, d, 1e6), spec(1, 2, d, 1e6), 1, 64)
+    old = kvb.kvb_cache8_create(ctx, 4, page)
+    for t in (old.k_scale, old.v_scale):
+        t.fill_(float("nan"))
+    del old, t
+    cache = kvb.kvb_cache8_create(ctx, 4, page)
+    ref = C8.Cache8(1, 4, 2, page, d)
+    for t in ref.scales:
+        t[:] = 2.0 ** -117
+    table = [[2, 0, 3, 1]]
+    s = kvb.Seqs(i32(table), i32([0, n]), i32([pos]), max_tokens=n)
+    x = [torch.randn(1, 2, n, d, device="cuda").to(dtype) for _ in range(2)]
+    kvb.kvb_cache8_write(ctx, cache, s, *x)
+    y = [torch.empty_like(t) for t in x]
+    kvb.kvb_cache8_read(ctx, cache, s, *y)
+    kvb.kvb_ctx_check(ctx)
+    for kv in range(2):
+        ref.write(kv, to_host64(x[kv]), table, [0, n], [pos])
+        assert np.array_equal(to_host64(y[kv]), ref.read(kv, table, [0, n], [pos]))
