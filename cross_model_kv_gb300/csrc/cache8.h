@@ -82,7 +82,7 @@ struct AttnPlan {
 };
 AttnPlan plan_attention(const Cache& c, const Seqs& q, kvb_dtype dtype, int g, int num_sms);
 cudaError_t launch_decode(const AttnParams& P, kvb_dtype dtype, const AttnPlan& p, cudaStream_t s);
-cudaError_t launch_prefill(const AttnParams& P, const AttnPlan& p, cudaStream_t s);  // bf16, d 128
+cudaError_t launch_prefill(const AttnParams& P, const AttnPlan& p, cudaStream_t s);  // bf16, d 64 and 128
 
 #ifdef __CUDACC__
 
