@@ -1,6 +1,8 @@
 """The attention workspace of a context: it grows without taking away what captured
 graphs hold, calls of different kinds share it without growing it in turn, and calls that
 overlap have a context each."""
+import gc
+
 import pytest
 
 from cases import spec
@@ -38,6 +40,7 @@ def test_a_captured_call_outlives_larger_ones(kvb, first):  # noqa: F811
     out, lse = run[first]()  # sizes the workspace
     kvb.kvb_ctx_check(P.ctx)
     want = out.clone(), lse.clone()
+    gc.collect()  # a context that is destroyed during a capture ends it
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         run[first]()
@@ -81,6 +84,7 @@ def test_growing_on_a_captured_stream_is_refused_and_the_capture_goes_on(kvb):  
     run = kinds(P)
     few = [t.clone() for t in run["few"]()]
     torch.cuda.synchronize()
+    gc.collect()  # a context that is destroyed during a capture ends it
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         out, lse = run["few"]()
