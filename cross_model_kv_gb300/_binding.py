@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 
 import numpy as np
 
@@ -183,8 +184,23 @@ class Ctx:
 
     def __del__(self):
         if getattr(self, "handle", None) and _lib is not None:
-            _lib.kvb_ctx_destroy(self.handle)
+            _unused.append((_lib.kvb_ctx_destroy, self.handle))
             self.handle = None
+            _destroy_unused()
+
+
+# What Ctx and Stats objects that are gone leave.  Destroying it waits for the device, which would end a
+# stream capture, and the garbage collector may come by during one: then it waits for the next occasion.
+_unused = []
+
+
+def _destroy_unused():
+    torch = sys.modules.get("torch")
+    if torch is not None and torch.cuda.is_initialized() and torch.cuda.is_current_stream_capturing():
+        return
+    while _unused:
+        destroy, handle = _unused.pop(0)  # statistics before their context
+        destroy(handle)
 
 
 # ------------------------------------------------------------------ calls
@@ -196,6 +212,7 @@ def kvb_version() -> int:
 def kvb_ctx_create(src, tgt, top_k: int, max_pos: int, device: int = 0) -> Ctx:
     lib = load_library()
     s, t = _spec(src), _spec(tgt)
+    _destroy_unused()
     h = ctypes.c_void_p()
     _check(lib.kvb_ctx_create(ctypes.byref(s), ctypes.byref(t), int(top_k), int(max_pos), int(device),
                               ctypes.byref(h)))
@@ -269,8 +286,9 @@ class Stats:
 
     def __del__(self):
         if getattr(self, "handle", None) and _lib is not None:
-            _lib.kvb_stats_destroy(self.handle)
+            _unused.append((_lib.kvb_stats_destroy, self.handle))
             self.handle = None
+            _destroy_unused()
 
 
 def kvb_stats_create(ctx: Ctx, dtype: int, max_batch_tokens: int) -> Stats:

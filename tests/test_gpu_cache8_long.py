@@ -4,8 +4,6 @@ pages than one list holds; and what only one of the two kernels was tested with 
 Sequences share the pages of a small pool (any number may read a page), so that long ones cost
 little.  Tolerances are those of test_gpu_cache8.py unless a test derives its own.
 """
-import gc
-
 import numpy as np
 import pytest
 
@@ -109,7 +107,6 @@ def test_prompts_captured_on_a_side_stream_while_the_cache_grows(kvb):  # noqa: 
     seqs = kvb.Seqs(P.dtab, off, pos, max_tokens=n, max_kv=900)
     kvb.kvb_cache8_attention(P.ctx, P.cache, seqs, q, out, lse)  # sizes the workspace
     torch.cuda.synchronize()
-    gc.collect()  # a context that is destroyed during a capture ends it
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph, stream=side):
         kvb.kvb_cache8_write(P.ctx, P.cache, seqs, k, v)

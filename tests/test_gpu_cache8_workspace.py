@@ -40,7 +40,6 @@ def test_a_captured_call_outlives_larger_ones(kvb, first):  # noqa: F811
     out, lse = run[first]()  # sizes the workspace
     kvb.kvb_ctx_check(P.ctx)
     want = out.clone(), lse.clone()
-    gc.collect()  # a context that is destroyed during a capture ends it
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         run[first]()
@@ -84,7 +83,6 @@ def test_growing_on_a_captured_stream_is_refused_and_the_capture_goes_on(kvb):  
     run = kinds(P)
     few = [t.clone() for t in run["few"]()]
     torch.cuda.synchronize()
-    gc.collect()  # a context that is destroyed during a capture ends it
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         out, lse = run["few"]()
@@ -140,3 +138,28 @@ def test_a_context_for_each_stream_and_one_context_on_ordered_streams(kvb):  # n
     check(run)
     kvb.kvb_ctx_check(P.ctx)
     kvb.kvb_ctx_check(other)
+
+
+def test_a_context_that_is_collected_during_a_capture_does_not_end_it(kvb):  # noqa: F811
+    P = Pool(kvb, 1, 2, 128, 16, 1, 3000)
+    P.fill([3000])
+    run = kinds(P)
+    want = [t.clone() for t in run["few"]()]
+    s = spec(1, 2, 128, 1e6)
+    gc.collect()
+    gc.disable()
+    try:
+        left = [kvb.kvb_ctx_create(s, s, 1, 64)]
+        left.append(left)
+        del left  # a cycle: only the collector finds the context
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out, lse = run["few"]()
+            assert gc.collect() > 0
+    finally:
+        gc.enable()
+    out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    kvb.kvb_ctx_check(P.ctx)
