@@ -1,3 +1,4 @@
+import gc
 import os
 import sys
 
@@ -11,6 +12,13 @@ if ROOT not in sys.path:
 def pytest_configure(config):
     config.addinivalue_line("markers", "gpu: needs a CUDA GPU (GB300, sm_103a)")
     config.addinivalue_line("markers", "slow: long-running CPU test")
+
+
+def pytest_runtest_setup(item):
+    # a test that catches an exception leaves a cycle with its frame, and so contexts and device
+    # memory, until the collector comes by: not in the middle of a test that compares free memory
+    if item.get_closest_marker("gpu"):
+        gc.collect()
 
 
 @pytest.fixture(scope="session")
