@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import sys
 
 import numpy as np
@@ -58,6 +59,10 @@ class kvb_seqs(ctypes.Structure):
                 ("max_kv", ctypes.c_int32), ("page_table", _P), ("seq_off", _P), ("seq_pos", _P), ("kv_len", _P)]
 
 
+class kvb_paged_cache(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("page_tokens", ctypes.c_int32), ("n_pages", ctypes.c_int64), ("k", _P), ("v", _P)]
+
+
 class kvb_kernel_time(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 32), ("launches", ctypes.c_int64), ("total_ms", ctypes.c_double)]
 
@@ -94,6 +99,13 @@ SIGNATURES = {
                                        ctypes.c_int64, _P]),
     "kvb_cache8_attention": (ctypes.c_int, [_P, _P, _P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int, _P,
                                             ctypes.c_int32, ctypes.c_int64, ctypes.c_double, _P, _P, _P]),
+    # the rows (kvb_rows) are passed as the bytes of the struct
+    "kvb_paged_append": (ctypes.c_int, [_P, _P, _P, ctypes.c_int32, ctypes.c_int32, _P, _P, _P, _P, ctypes.c_int32,
+                                        ctypes.c_int64, ctypes.c_int32, _P]),
+    "kvb_cache8_append": (ctypes.c_int, [_P, _P, _P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int, _P, _P, _P, _P,
+                                         ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, _P]),
+    "kvb_paged_attention": (ctypes.c_int, [_P, _P, _P, ctypes.c_int32, ctypes.c_int32, _P, ctypes.c_int32,
+                                           ctypes.c_int64, ctypes.c_double, _P, _P, _P]),
 }
 
 _lib = None
@@ -401,6 +413,7 @@ class Cache8:
                 raise ValueError(f"cache8 scales must be float32 [{L}][{n_pages}][{H}]")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.of = ctx.cache8_of  # the calls index with their context's sizes
+        self.device = k.get_device()
         self.n_pages, self.page_tokens = int(n_pages), int(page)
         self.struct = kvb_cache8(self.page_tokens, self.n_pages, _dev(k), _dev(v), _dev(k_scale), _dev(v_scale))
         self.ref = ctypes.addressof(self.struct)
@@ -438,6 +451,7 @@ class Seqs:
             if t.dtype != torch.int32 or tuple(t.shape) != shape:
                 raise ValueError(f"{name} must be int32 {list(shape)}, got {t.dtype} {list(t.shape)}")
         self.tensors = (page_table, seq_off, seq_pos, kv_len)
+        self.device = page_table.get_device()
         self.struct = kvb_seqs(n, int(page_table.shape[1]), int(max_tokens), int(max_kv), _dev(page_table),
                                _dev(seq_off), _dev(seq_pos), _dev(kv_len))
         self.ref = ctypes.addressof(self.struct)
@@ -524,5 +538,132 @@ def kvb_cache8_attention(ctx: Ctx, cache: Cache8, seqs: Seqs, q, out, lse=None, 
     status = load_library().kvb_cache8_attention(
         ctx.handle, cache.ref, seqs.ref, l_begin, shape[0], _dtype_of(q), _ptr(q), shape[1], shape[2], scale, _ptr(out),
         lse, _stream_of(ctx, stream))
+    if status:
+        _check(status)
+
+
+# ------------------------------------------------------------------ paged cache of the model's own type
+
+class PagedCache:
+    """The two tensors of a paged cache (see kvb_paged_cache in include/kvb.h).
+
+    k, v [L_t][n_pages][H][page_tokens][d], bf16 or fp32, on the context's device.
+    """
+
+    def __init__(self, ctx: Ctx, k, v):
+        if k.dim() != 5 or (k.shape[0], k.shape[2], k.shape[4]) != ctx.cache8_of:
+            raise ValueError(f"pages must be [{ctx.L_t}][n_pages][{ctx.H}][page_tokens][{ctx.d}], got {list(k.shape)}")
+        _same_as("v", v, k.shape, k.dtype)
+        dtype = _dtype_of(k)
+        for t in (k, v):
+            _on_device(ctx, "pages", t)
+        self.k, self.v, self.dtype = k, v, k.dtype
+        self.of = ctx.cache8_of  # the calls index with their context's sizes
+        self.device = ctx.device
+        self.n_pages, self.page_tokens = int(k.shape[1]), int(k.shape[3])
+        self.struct = kvb_paged_cache(dtype, self.page_tokens, self.n_pages, _dev(k), _dev(v))
+        self.ref = ctypes.addressof(self.struct)
+
+
+def kvb_paged_create(ctx: Ctx, n_pages: int, page_tokens: int = 64, dtype=None) -> PagedCache:
+    """Allocate n_pages pages (bf16, or torch.float32) for every target layer on the context's device; they are not set."""
+    import torch
+    shape = (ctx.L_t, int(n_pages), ctx.H, int(page_tokens), ctx.d)
+    page = lambda: torch.empty(shape, dtype=dtype or torch.bfloat16, device=torch.device("cuda", ctx.device))
+    return PagedCache(ctx, page(), page())
+
+
+_pack_rows = struct.Struct("=4q").pack
+
+
+def _on_device(ctx, name, t):
+    if t.get_device() != ctx.device:
+        raise ValueError(f"{name} must be on the context's device cuda:{ctx.device}, got {t.device}")
+
+
+def _rows(ctx, name, t, shape, dtype):
+    """The kvb_rows of a tensor [n_layers][heads][T][d] of any strides but the last, which is 1."""
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    if t.get_device() != ctx.device:
+        _on_device(ctx, name, t)
+    l, h, n, e = t.stride()
+    if e != 1:
+        raise ValueError(f"{name}: the elements of a row must lie next to each other, got a stride of {e}")
+    return _pack_rows(t.data_ptr(), l, h, n)
+
+
+def _fit(ctx: Ctx, cache, seqs: Seqs):
+    if cache.of != ctx.cache8_of:
+        raise _misfit(ctx, cache)
+    if seqs.device != ctx.device or cache.device != ctx.device:
+        raise ValueError(f"cache and seqs must be on the context's device cuda:{ctx.device}")
+
+
+def _append(ctx: Ctx, cache, seqs: Seqs, k, v, q, q_out, rotate):
+    _fit(ctx, cache, seqs)
+    shape, dtype = k.shape, k.dtype
+    if len(shape) != 4 or shape[1] != ctx.H or shape[3] != ctx.d:
+        raise ValueError(f"k must be [n_layers][{ctx.H}][T][{ctx.d}], got {list(shape)}")
+    rk, rv = _rows(ctx, "k", k, shape, dtype), _rows(ctx, "v", v, shape, dtype)
+    if q is None and q_out is None:
+        return shape[0], rk, rv, None, None, 0, shape[2], 1 if rotate else 0
+    if q is None or q_out is None:
+        raise ValueError("q and q_out go together")
+    rows = q.shape
+    if len(rows) != 4 or rows[0] != shape[0] or rows[2:] != shape[2:]:
+        raise ValueError(f"q must be [{shape[0]}][Hq][{shape[2]}][{ctx.d}], got {list(rows)}")
+    return (shape[0], rk, rv, _rows(ctx, "q", q, rows, dtype), _rows(ctx, "q_out", q_out, rows, dtype), rows[1], shape[2],
+            1 if rotate else 0)
+
+
+def kvb_paged_append(ctx: Ctx, cache: PagedCache, seqs: Seqs, k, v, q=None, q_out=None, l_begin: int = 0,
+                     rotate: bool = True, stream=None):
+    """Append the tokens k, v [n_layers][H][T][d] to layers l_begin .. of the cache, keys rotated to their positions.
+
+    The tensors are in the cache's dtype and may have any strides (multiples of 16 bytes) but
+    the last.  rotate=False stores keys as they are.  q [n_layers][Hq][T][d], the queries of the
+    same tokens, is rotated into q_out (which may be q).
+    """
+    if k.dtype != cache.dtype:
+        raise ValueError(f"k must be {cache.dtype} as the cache is, got {k.dtype}")
+    n, rk, rv, rq, ro, heads, T, turn = _append(ctx, cache, seqs, k, v, q, q_out, rotate)
+    status = load_library().kvb_paged_append(ctx.handle, cache.ref, seqs.ref, l_begin, n, rk, rv, rq, ro, heads, T, turn,
+                                             _stream_of(ctx, stream))
+    if status:
+        _check(status)
+
+
+def kvb_cache8_append(ctx: Ctx, cache: Cache8, seqs: Seqs, k, v, q=None, q_out=None, l_begin: int = 0,
+                      rotate: bool = True, stream=None):
+    """kvb_paged_append into the 8-bit cache: keys are rotated in fp32, then quantised; k and v are bf16 or fp32."""
+    n, rk, rv, rq, ro, heads, T, turn = _append(ctx, cache, seqs, k, v, q, q_out, rotate)
+    status = load_library().kvb_cache8_append(ctx.handle, cache.ref, seqs.ref, l_begin, n, _dtype_of(k), rk, rv, rq, ro,
+                                              heads, T, turn, _stream_of(ctx, stream))
+    if status:
+        _check(status)
+
+
+def kvb_paged_attention(ctx: Ctx, cache: PagedCache, seqs: Seqs, q, out, lse=None, l_begin: int = 0, scale: float = 0.0,
+                        stream=None):
+    """out [n_layers][Hq][T][d] = attention of the queries q over the cache; lse float32 [n_layers][Hq][T] or None.
+
+    q and out are in the cache's dtype, with any strides (multiples of 16 bytes) but the last.
+    Otherwise as kvb_cache8_attention, whose workspace it shares: attention calls with one ctx must not
+    overlap on the GPU.
+    """
+    _fit(ctx, cache, seqs)
+    shape, dtype = q.shape, cache.dtype
+    if len(shape) != 4 or shape[3] != ctx.d:
+        raise ValueError(f"q must be [n_layers][Hq][T][{ctx.d}], got {list(shape)}")
+    rq, ro = _rows(ctx, "q", q, shape, dtype), _rows(ctx, "out", out, shape, dtype)
+    if lse is not None:
+        import torch
+        _same_as("lse", lse, shape[:3], torch.float32)
+        if lse.get_device() != ctx.device:
+            _on_device(ctx, "lse", lse)
+        lse = _ptr(lse)
+    status = load_library().kvb_paged_attention(ctx.handle, cache.ref, seqs.ref, l_begin, shape[0], rq, shape[1], shape[2],
+                                                scale, ro, lse, _stream_of(ctx, stream))
     if status:
         _check(status)

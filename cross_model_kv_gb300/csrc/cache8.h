@@ -45,6 +45,11 @@ struct Seqs {
     int64_t T;
 };
 
+// Pages that one sequence of a call can touch, wherever its first token lies in a page.
+inline int items_of(const Cache& c, const Seqs& q) {
+    return static_cast<int>((static_cast<int64_t>(q.max_tokens) + c.page - 2) / c.page + 1);
+}
+
 // ------------------------------------------------------------ launchers
 cudaError_t launch_write(const Cache& c, const Seqs& q, kvb_dtype dtype, const void* k, const void* v, const Err& err,
                          cudaStream_t s);
@@ -159,6 +164,23 @@ __device__ __forceinline__ SeqView seq_view(const Seqs& q, int s, const Err& err
         v.tok0 = v.n = 0;
     }
     return v;
+}
+
+// The first n8 eights of a block's codes rounded again under a scale 2^-by times as large, by threads t, t + gs, ..:
+// what the slots before the new tokens hold.
+__device__ __forceinline__ void lower_codes(uint8_t* codes, int n8, int by, int t, int gs) {
+    const float f = pow2(max(by, -126));
+    for (int c = t; c < n8; c += gs) {
+        uint2* p = reinterpret_cast<uint2*>(codes) + c;
+        const uint2 u = *p;
+        uint32_t r[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float2 a = float2_of(half2_of_lo(i ? u.y : u.x)), b = float2_of(half2_of_hi(i ? u.y : u.x));
+            r[i] = e4m3x2(a.x * f, a.y * f) | (e4m3x2(b.x * f, b.y * f) << 16);
+        }
+        *p = make_uint2(r[0], r[1]);
+    }
 }
 
 #endif  // __CUDACC__

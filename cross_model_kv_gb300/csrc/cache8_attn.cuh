@@ -1,4 +1,5 @@
-// Paged 8-bit cache: what its two attention kernels share.
+// Attention over paged caches: what the two kernels of the 8-bit cache share.  The row blocks, the
+// line of tiles and the pieces serve the pages of the model's own type too (Params: its AttnParams).
 #pragma once
 
 #include "cache8.h"
@@ -37,18 +38,21 @@ struct RowBlock {
     int pos_lo;            // position of the block's first row
     int kv_end;            // keys that its last row may see
     // index of a row in [n_layers][Hq][T]
-    __device__ __forceinline__ int64_t row_of(const AttnParams& P, int64_t hq0, int row) const {
+    template <class Params>
+    __device__ __forceinline__ int64_t row_of(const Params& P, int64_t hq0, int row) const {
         const int gr = row0 + row, i = gr / P.g;
         return (hq0 + (gr - i * P.g)) * P.q.T + tok0 + i;
     }
 };
 
 // Rows of q, out and lse.
-__device__ __forceinline__ int64_t rows_of(const AttnParams& P) {
+template <class Params>
+__device__ __forceinline__ int64_t rows_of(const Params& P) {
     return static_cast<int64_t>(P.c.n_layers) * P.c.H * P.g * P.q.T;
 }
 
-__device__ __forceinline__ RowBlock row_block(const AttnParams& P, int s, int rb, int rows) {
+template <class Params>
+__device__ __forceinline__ RowBlock row_block(const Params& P, int s, int rb, int rows) {
     RowBlock B{};
     const SeqView sv = seq_view(P.q, s, P.err);
     const int total = sv.n * P.g;  // and rows of a call, and tiles of its line, stay below 2^30
@@ -106,8 +110,8 @@ struct LineStart {
 // The units' tiles form one line: layer, then entry (sequence, row block), then
 // head.  This CTA takes tiles [at, stop) of it, the first of them tile `first` of unit
 // (l, e, h); share is every CTA's number.  false: nothing is left for this CTA.
-template <int ROWS, int TILE, int NTHREADS>
-__device__ __forceinline__ bool line_start(const AttnParams& P, int* scratch, LineStart* found, int& at, int& stop, int& share,
+template <int ROWS, int TILE, int NTHREADS, class Params>
+__device__ __forceinline__ bool line_start(const Params& P, int* scratch, LineStart* found, int& at, int& stop, int& share,
                                            int& l, int& e, int& h, int& first) {
     const int entries = P.q.n_seq * P.row_blocks;
     auto tiles_of = [&](int i) { return unit_tiles<TILE>(row_block(P, i / P.row_blocks, i % P.row_blocks, ROWS)); };
@@ -175,7 +179,8 @@ struct Pieces {
 };
 
 // All of them (the checked build).
-__device__ __forceinline__ bool pieces_in_bounds(const AttnParams& P, const Pieces& pieces) {
+template <class Params>
+__device__ __forceinline__ bool pieces_in_bounds(const Params& P, const Pieces& pieces) {
     return KVB_IN_BOUNDS(P.err, pieces.slot(0), 1, P.slots) && KVB_IN_BOUNDS(P.err, pieces.slot(pieces.n - 1), 1, P.slots);
 }
 

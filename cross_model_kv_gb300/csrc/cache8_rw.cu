@@ -226,20 +226,7 @@ __global__ void __launch_bounds__(GS > NT ? GS : NT) write_kernel(const __grid_c
                 *reinterpret_cast<uint2*>(codes + (at.lo << P.c.d_log2) + 8 * (c * GS + t)) =
                     make_uint2(__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[2], w[3], 0x5410));
             }
-        if (at.lo > 0 && e > e_old[kv]) {  // the slots before the new tokens, under the larger scale
-            const float f = pow2(max(e_old[kv] - e, -126));
-            for (int c = t; c < (at.lo << P.c.d_log2) >> 3; c += GS) {
-                uint2* p = reinterpret_cast<uint2*>(codes) + c;
-                const uint2 u = *p;
-                uint32_t r[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float2 a = float2_of(half2_of_lo(i ? u.y : u.x)), b = float2_of(half2_of_hi(i ? u.y : u.x));
-                    r[i] = e4m3x2(a.x * f, a.y * f) | (e4m3x2(b.x * f, b.y * f) << 16);
-                }
-                *p = make_uint2(r[0], r[1]);
-            }
-        }
+        if (at.lo > 0 && e > e_old[kv]) lower_codes(codes, (at.lo << P.c.d_log2) >> 3, e_old[kv] - e, t, GS);
     }
 }
 
@@ -296,11 +283,6 @@ __global__ void __launch_bounds__(NT) read_kernel(const __grid_constant__ RwPara
             for (int j = 0; j < AHEAD; ++j)
                 if (c0 + j * GS < n) store_values(dst[kv] + VEC * (c0 + j * GS), u[kv][j], f[kv]);
     }
-}
-
-// Pages that one sequence of a call can touch, wherever its first token lies in a page.
-int items_of(const Cache& c, const Seqs& q) {
-    return static_cast<int>((static_cast<int64_t>(q.max_tokens) + c.page - 2) / c.page + 1);
 }
 
 // Threads for an item: enough to hold the most new values that a block can get, so

@@ -426,6 +426,89 @@ kvb_status kvb_cache8_attention(kvb_ctx* ctx, const kvb_cache8* cache, const kvb
                                 int32_t n_layers, kvb_dtype dtype, const void* q, int32_t n_q_heads, int64_t T,
                                 double scale, void* out, float* lse, void* stream);
 
+/*
+ * Rows of heads with strides of their own (in elements): element e of (layer l,
+ * head h, token t) is data[l * layer + h * head + t * token + e].  So the slices of a
+ * fused projection's output [T][q heads, k heads, v heads][d] are rows as they are.
+ * data is 16-byte aligned; the stride of an axis with more than one index is a
+ * multiple of 16 bytes.  Outputs overlap neither themselves nor anything that the call
+ * reads, with one exception: q_out may be q with the same strides.
+ */
+typedef struct {
+    void* data;
+    int64_t layer, head, token;
+} kvb_rows;
+
+/*
+ * Paged cache of the target model in the model's own type:
+ *   k, v  device [L_tgt][n_pages][H][page_tokens][d] in dtype, 16-byte aligned
+ * page_tokens is 16, 32, 64 or 128 and d (the context's) 16, 32, 64 or 128.  The caller
+ * owns the buffers; they need no initial value, since only slots that are visible to a
+ * query are read.
+ */
+typedef struct {
+    kvb_dtype dtype;
+    int32_t page_tokens;
+    int64_t n_pages;
+    void* k;
+    void* v;
+} kvb_paged_cache;
+
+/*
+ * Append tokens to layers [l_begin, l_begin + n_layers) of the cache, with the target's
+ * RoPE applied on the way.  Token i of sequence s goes to position p = seq_pos[s] + i:
+ *   k, v      rows of H heads in the cache's dtype; k without RoPE where rotate is 1,
+ *             stored as it is where rotate is 0 (the outputs of kvb_map_apply)
+ *   q, q_out  rows of n_q_heads heads, or both NULL: queries of the same tokens, rotated
+ *             to the same positions into q_out; they need rotate = 1
+ *       x'_i = x_i c - x_(i+d/2) s,  x'_(i+d/2) = x_(i+d/2) c + x_i s
+ * with c and s of position p from the context's fp32 table (reduced in float64).  Every
+ * product and sum is rounded to fp32 by itself (no fused multiply-add) and the result
+ * once to dtype, so elementary fp32 operations give the same bits.  A position outside
+ * [0, max_pos) is recorded on the context (KVB_ERR_INVALID_ARG) and its rows, where they
+ * have a place, are written as 0; a token without a page is recorded and not stored.
+ * Values are not looked at: infinities and NaN are stored.  Several sequences of a call
+ * may write to one page, not to one slot.
+ */
+kvb_status kvb_paged_append(kvb_ctx* ctx, const kvb_paged_cache* cache, const kvb_seqs* seqs, int32_t l_begin,
+                            int32_t n_layers, const kvb_rows* k, const kvb_rows* v, const kvb_rows* q,
+                            const kvb_rows* q_out, int32_t n_q_heads, int64_t T, int32_t rotate, void* stream);
+
+/*
+ * The same into the 8-bit cache: blocks, scales and codes as kvb_cache8_write makes
+ * them, of the keys rotated in fp32 (not rounded to dtype between).  Where the position
+ * is outside [0, max_pos) keys and values count as 0; a value that is not finite, after
+ * the rotation for keys, is stored as 0 and recorded as KVB_ERR_NUMERIC.  One call writes
+ * to a page from one sequence only.  dtype is that of the rows.
+ */
+kvb_status kvb_cache8_append(kvb_ctx* ctx, const kvb_cache8* cache, const kvb_seqs* seqs, int32_t l_begin,
+                             int32_t n_layers, kvb_dtype dtype, const kvb_rows* k, const kvb_rows* v,
+                             const kvb_rows* q, const kvb_rows* q_out, int32_t n_q_heads, int64_t T, int32_t rotate,
+                             void* stream);
+
+/*
+ * Attention of new tokens over the cache: for one token a sequence, or the few of a
+ * draft that is checked (any number is right; keys are read once for 32 query rows, a
+ * head's tokens times n_q_heads / H, of bf16 and once for 8 of fp32):
+ *     out_i = sum over visible j of softmax_j(scale * q_i . k_j) v_j,
+ *     lse_i = log sum over visible j of exp(scale * q_i . k_j),
+ * with seqs, visibility, n_q_heads, scale and lse as for kvb_cache8_attention; q and out
+ * are rows of n_q_heads heads in the cache's dtype, queries with the target's RoPE.  A row
+ * that sees nothing is 0 with lse -infinity; rows of tokens that no sequence owns are
+ * left as they are.  Products of bf16 numbers are exact and summed in fp32; bf16 calls
+ * carry a weight as a bf16 pair (16 bits) into its product with v, fp32 calls as fp32.
+ * Statistics and sums are fp32.  What slots past kv_len or the query's position hold is
+ * never used, and a page outside [0, n_pages) counts as absent and is recorded.
+ * The result does not depend on timing.
+ *
+ * Workspace: the context's attention workspace, with the rules of kvb_cache8_attention:
+ * attention calls on one context, of both kinds of cache, never overlap on the GPU; make a
+ * call once before capturing it.
+ */
+kvb_status kvb_paged_attention(kvb_ctx* ctx, const kvb_paged_cache* cache, const kvb_seqs* seqs, int32_t l_begin,
+                               int32_t n_layers, const kvb_rows* q, int32_t n_q_heads, int64_t T, double scale,
+                               const kvb_rows* out, float* lse, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
