@@ -48,6 +48,7 @@ struct AttnParams {
     int g;       // query heads of a KV head
     int row_blocks;
     int min_tiles;     // a CTA's least share of the line of tiles
+    int cluster;       // CTAs of a unit's cluster, a power of two, or 0: the line
     float scale_log2;  // scale * log2(e)
     int* counters;     // [units], 0 before and after a call
     float* partial;    // [slots][rows][d]
@@ -58,7 +59,7 @@ struct AttnParams {
 
 // How a call is cut: blocks of `rows` query rows, and their keys over CTAs.
 struct AttnPlan {
-    int rows, row_blocks, min_tiles, ctas;
+    int rows, row_blocks, min_tiles, cluster, ctas;
     int64_t units, slots;
     double tiles;
     size_t counter_bytes, partial_bytes;

@@ -172,7 +172,7 @@ kvb_status kvb_paged_attention(kvb_ctx* c, const kvb_paged_cache* cache, const k
         constexpr double most = 1 << 30;
         if (static_cast<double>(p.units) > most || p.tiles > most || static_cast<double>(a.q.max_tokens) * a.g > most)
             return fail(KVB_ERR_UNSUPPORTED, "kvb_paged_attention: more query rows, sequences, layers or keys than one call takes (2^30 tiles of 64 keys)");
-        if ((st = c8::ensure_attn_ws(c, p.counter_bytes, p.partial_bytes, what, s)) != KVB_OK) return st;
+        if (!p.cluster && (st = c8::ensure_attn_ws(c, p.counter_bytes, p.partial_bytes, what, s)) != KVB_OK) return st;
         a.counters = static_cast<int*>(c->attn_counters);
         a.partial = static_cast<float*>(c->attn_parts);
         a.part_stat = reinterpret_cast<float2*>(a.partial + static_cast<size_t>(p.slots) * p.rows * c->d);
@@ -180,6 +180,7 @@ kvb_status kvb_paged_attention(kvb_ctx* c, const kvb_paged_cache* cache, const k
         a.slots = p.slots;
         a.row_blocks = p.row_blocks;
         a.min_tiles = p.min_tiles;
+        a.cluster = p.cluster;
         ProfScope ps(c, s, "paged_attention");
         const cudaError_t e = paged::launch_attention(a, cache->dtype, p, s);
         return e == cudaSuccess ? KVB_OK : cuda_fail(e, "paged attention launch");

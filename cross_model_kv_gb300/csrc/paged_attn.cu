@@ -34,12 +34,13 @@ using c8::LineStart;
 using c8::Pieces;
 using c8::RowBlock;
 
-constexpr int WARPS = 4, NT = 32 * WARPS;
+constexpr int WARPS = 4;              // of a CTA of the line
 constexpr int STEP = 16;              // keys of a warp's step
-constexpr int TILE = STEP * WARPS;    // of a CTA's
+constexpr int TILE = STEP * WARPS;    // a tile of the line
 constexpr float MARGIN = 8.f;         // a reference is raised past this much (base 2)
 constexpr float LOWEST = -FLT_MAX;    // reference of a row that has seen nothing
 constexpr int MIN_TILES = 2;
+constexpr int FEW_SHARES = 32;          // steps of a warp up to which a cluster takes a unit
 
 // A step's K or V rows in shared memory: 16-byte chunks, chunk c of row r at c ^ swizzle(r), so that
 // eight rows' chunks of one number, and a row's chunks, lie in different banks.
@@ -62,28 +63,30 @@ __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Ring of one warp: steps of K and V rows.
+// Ring of one warp: the K rows of a step and its V rows, in turn, each a part.
 template <typename T, int D>
 struct Ring {
-    static constexpr int CH = D * sizeof(T) / 16;          // chunks of a row
-    static constexpr int PART = STEP * D * sizeof(T);      // bytes of K, and of V
-    static constexpr int FIT = 24576 * (sizeof(T) / 2) / (2 * PART);
-    static constexpr int DEPTH = FIT > 8 ? 8 : FIT;        // bf16 d 128: 3 steps of 8 KB
-    static constexpr int BYTES = DEPTH * 2 * PART;
+    static constexpr int CH = D * sizeof(T) / 16;       // 16-byte chunks of a row
+    static constexpr int PART = STEP * D * sizeof(T);   // bytes
+    static constexpr int FIT = 24576 / PART;            // four warps' rings twice on an SM
+    static constexpr int DEPTH = FIT > 16 ? 16 : FIT;   // d 128: 6 parts in bf16, 3 in fp32
+    static constexpr int BYTES = DEPTH * PART;
 };
 
-// What one warp reads in one unit: steps n = 0, 1, .. of keys first + TILE * n up to end.
-template <typename T, int D>
+// What one of NW warps reads in one unit: steps n = 0, 1, .. of keys first + TILE * n up to end.
+template <typename T, int D, int NW>
 struct Feeder {
     using R = Ring<T, D>;
+    static constexpr int TILE = STEP * NW;            // keys between a warp's steps
     static constexpr int AT_ONCE = 32 / R::CH;        // rows that the warp copies at once
-    static constexpr int COPIES = STEP / AT_ONCE;     // of a lane, for K and for V
+    static constexpr int COPIES = STEP / AT_ONCE;     // of a lane, for a part
     int s, first, end, steps;
     int64_t slab;     // block of page 0
     uint32_t ring;    // this warp's
     int now, next;    // pages of 32 steps, one a lane: those in use, and the 32 after them; -1: none
-    int stage;        // that the next step is copied to
-    uint32_t absent;  // bit of a stage: its page is not there
+    int stage;        // that the next part is copied to
+    int64_t row0;     // first row of the step that is asked for, in the pages; negative: its page is not there
+    uint32_t absent;  // bit of a stage: likewise
 
     __device__ __forceinline__ int page_of(const AttnParams& P, int n0) const {
         const int n = n0 + (threadIdx.x & 31);
@@ -110,29 +113,33 @@ struct Feeder {
         next = -1;
         now = page_of(P, 0);
     }
-    // Asks for step n's rows, n = 0, 1, .. in turn: one group of copies, empty past the last step.
+    // Asks for the rows of part m = 0, 1, .. in turn (K of step m / 2, then V): one group of copies, empty
+    // past the last step.
+    template <int KV>
     __device__ __forceinline__ void ask(const AttnParams& P, int n) {
         if (n < steps) {
-            if ((n & 31) == 0) {
-                if (n > 0) now = next;
-                if (n + 32 < steps) next = page_of(P, n + 32);
-            }
-            const int pid = __shfl_sync(0xffffffffu, now, n & 31);
             const int j = first + TILE * n;
-            const int lane = threadIdx.x & 31, row = lane / R::CH, chunk = lane % R::CH;
-            const int64_t at = ((slab + static_cast<int64_t>(max(pid, 0)) * P.c.H) << P.c.page_log2) + (j & (P.c.page - 1)) + row;
-            const uint32_t dst = ring + stage * 2 * R::PART;
-            const bool whole = pid >= 0 && j + STEP <= end;
-            absent = pid < 0 ? absent | (1u << stage) : absent & ~(1u << stage);
-#pragma unroll
-            for (int kv = 0; kv < 2; ++kv) {
-                const T* from = static_cast<const T*>(P.c.kv[kv]) + at * D + chunk * (16 / static_cast<int>(sizeof(T)));
-#pragma unroll
-                for (int i = 0; i < COPIES; ++i) {
-                    const uint32_t to = dst + kv * R::PART + 16 * swizzled<R::CH>(row + i * AT_ONCE, chunk);
-                    if (whole) copy16(to, from + i * AT_ONCE * D);
-                    else copy16_or_zero(to, from + i * AT_ONCE * D, P.c.kv[kv], pid >= 0 && j + row + i * AT_ONCE < end);
+            if constexpr (KV == 0) {
+                if ((n & 31) == 0) {
+                    if (n > 0) now = next;
+                    if (n + 32 < steps) next = page_of(P, n + 32);
                 }
+                const int pid = __shfl_sync(0xffffffffu, now, n & 31);
+                row0 = pid < 0 ? -1 : ((slab + static_cast<int64_t>(pid) * P.c.H) << P.c.page_log2) + (j & (P.c.page - 1));
+                absent = pid < 0 ? absent | (1u << stage) : absent & ~(1u << stage);
+            }
+            const int lane = threadIdx.x & 31, row = lane / R::CH, chunk = lane % R::CH;
+            const uint32_t dst = ring + stage * R::PART;
+            const T* from = static_cast<const T*>(P.c.kv[KV]) + (row0 + row) * D + chunk * (16 / static_cast<int>(sizeof(T)));
+            if (row0 >= 0 && j + STEP <= end) {
+#pragma unroll
+                for (int i = 0; i < COPIES; ++i)
+                    copy16(dst + 16 * swizzled<R::CH>(row + i * AT_ONCE, chunk), from + i * AT_ONCE * D);
+            } else {
+#pragma unroll
+                for (int i = 0; i < COPIES; ++i)
+                    copy16_or_zero(dst + 16 * swizzled<R::CH>(row + i * AT_ONCE, chunk), from + i * AT_ONCE * D, P.c.kv[KV],
+                                   row0 >= 0 && j + row + i * AT_ONCE < end);
             }
             stage = stage + 1 == R::DEPTH ? 0 : stage + 1;
         }
@@ -167,17 +174,18 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 
 // The arithmetic of a warp.  Lane (r, c): keys r and r + 8 of a step, query rows 2c and 2c + 1 of
 // each block of 8.
-template <typename T, int D, int NB>
+template <typename T, int D, int NB, int NW>
 struct Math;
 
-template <int D, int NB>
-struct Math<__nv_bfloat16, D, NB> {
+template <int D, int NB, int NW>
+struct Math<__nv_bfloat16, D, NB, NW> {
     static constexpr int ROWS = 8 * NB, KS = D / 16, SHARED = 0;
     using R = Ring<__nv_bfloat16, D>;
     uint32_t q[NB][KS][2];
     float o[NB][KS][4];
     float m[NB][2], sum[NB][2];
     int qpos[NB][2];
+    uint32_t hi[NB][2], lo[NB][2];  // the step's weights
 
     static __device__ __forceinline__ int r() { return (threadIdx.x & 31) >> 2; }
     static __device__ __forceinline__ int c() { return threadIdx.x & 3; }
@@ -209,19 +217,32 @@ struct Math<__nv_bfloat16, D, NB> {
             }
         }
     }
-    // The step of keys j .. j + 15 at `at` in shared memory; f = scale * log2(e).  whole: all rows see all keys.
-    __device__ __forceinline__ void step(uint32_t at, float*, int j, int end, bool whole, bool absent, float f) {
+    // Weights of keys j .. j + 15, whose rows are at `at` in shared memory; f = scale * log2(e).
+    // whole: all rows see all keys.
+    __device__ __forceinline__ void keys(uint32_t at, float*, int j, int end, bool whole, bool absent, float f) {
         const int lane = threadIdx.x & 31;
-        float sc[NB][4];
+        // products in a few chains, so that one need not wait for the last
+        constexpr int CHAINS = NB * 4 <= KS ? 4 / NB : 1;
+        float sc[NB][4], part[CHAINS][NB][4];
 #pragma unroll
-        for (int b = 0; b < NB; ++b) sc[b][0] = sc[b][1] = sc[b][2] = sc[b][3] = 0.f;
+        for (int x = 0; x < CHAINS; ++x)
+#pragma unroll
+            for (int b = 0; b < NB; ++b) part[x][b][0] = part[x][b][1] = part[x][b][2] = part[x][b][3] = 0.f;
 #pragma unroll
         for (int t = 0; t < KS; ++t) {
             uint32_t a[4];
             ldmatrix4(a, at + 16 * swizzled<R::CH>(lane & 15, 2 * t + (lane >> 4)));
 #pragma unroll
-            for (int b = 0; b < NB; ++b) mma16816(sc[b], a, q[b][t][0], q[b][t][1]);
+            for (int b = 0; b < NB; ++b) mma16816(part[t % CHAINS][b], a, q[b][t][0], q[b][t][1]);
         }
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                sc[b][u] = part[0][b][u];
+#pragma unroll
+                for (int x = 1; x < CHAINS; ++x) sc[b][u] += part[x][b][u];
+            }
         bool raise = false;
 #pragma unroll
         for (int b = 0; b < NB; ++b)
@@ -251,7 +272,6 @@ struct Math<__nv_bfloat16, D, NB> {
                     }
                 }
         }
-        uint32_t hi[NB][2], lo[NB][2];
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -266,10 +286,14 @@ struct Math<__nv_bfloat16, D, NB> {
                 hi[b][hf] = transpose8x8(x);
                 lo[b][hf] = transpose8x8(pack_bf16x2(w[0] - __uint_as_float(x << 16), w[1] - __uint_as_float(x & 0xffff0000u)));
             }
+    }
+    // Their weighted value rows, at `at`, are added.
+    __device__ __forceinline__ void values(uint32_t at, float*) {
+        const int lane = threadIdx.x & 31;
 #pragma unroll
         for (int i = 0; i < KS; ++i) {
             uint32_t a[4];
-            ldmatrix4_trans(a, at + R::PART + 16 * swizzled<R::CH>((lane & 7) + 8 * (lane >> 4), 2 * i + ((lane >> 3) & 1)));
+            ldmatrix4_trans(a, at + 16 * swizzled<R::CH>((lane & 7) + 8 * (lane >> 4), 2 * i + ((lane >> 3) & 1)));
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
                 mma16816(o[b][i], a, hi[b][0], hi[b][1]);
@@ -314,25 +338,29 @@ __device__ __forceinline__ float4 shared4(uint32_t p) {
     return v;
 }
 
-// Scores: lane (r, c) takes quarter c of the dims for keys r and r + 8 and all 8 rows; the quarters
-// are added by exchanging halves, which leaves rows 2c and 2c + 1.  Outputs: a lane takes 4 dims of
-// all rows for every 32 / (D / 4)-th key.
-template <int D>
-struct Math<float, D, 1> {
-    static constexpr int ROWS = 8, QUARTER = D / 4 + 4;  // 4 floats between: the quarters lie in different banks
+// Scores: lane (r, c) takes quarter c of the dims for keys r and r + 8 and all rows; the quarters are
+// added by exchanging halves, which leaves each lane RL rows, RL * c on.  Outputs: a lane takes 4
+// dims of all rows for every 32 / (D / 4)-th key.  NB: rows, of which there are 4 or 8.
+template <int D, int NB, int NW>
+struct Math<float, D, NB, NW> {
+    static constexpr int ROWS = NB, RL = ROWS / 4;
+    static constexpr int QUARTER = D / 4 + 4;  // 4 floats between: the quarters lie in different banks
     static constexpr int DL = D / 4, KP = 32 / DL;
-    static constexpr int SHARED = ROWS * 4 * QUARTER + WARPS * STEP * ROWS;  // floats: queries, weights
+    static constexpr int SHARED = ROWS * 4 * QUARTER + NW * STEP * ROWS;  // floats: queries, weights
     using R = Ring<float, D>;
-    float2 o[4][4];  // rows 2i, 2i + 1; dim
-    float m[2], sum[2];
-    int qpos[2];
+    float2 o[ROWS / 2][4];  // rows 2i, 2i + 1; dim
+    float m[RL], sum[RL];
+    int qpos[RL];
 
     static __device__ __forceinline__ int r() { return threadIdx.x & 7; }
     static __device__ __forceinline__ int c() { return (threadIdx.x & 31) >> 3; }
+    static __device__ __forceinline__ float* weights(float* shared) {
+        return shared + ROWS * 4 * QUARTER + (threadIdx.x >> 5) * STEP * ROWS;
+    }
 
     template <class Row>
     __device__ __forceinline__ void load(float* shared, int nrows, Row row) {
-        for (int i = threadIdx.x; i < ROWS * (D / 4); i += NT) {
+        for (int i = threadIdx.x; i < ROWS * (D / 4); i += 32 * NW) {
             const int y = i / (D / 4), d4 = i % (D / 4);
             const float4 v = y < nrows ? __ldg(reinterpret_cast<const float4*>(row(y)) + d4) : make_float4(0.f, 0.f, 0.f, 0.f);
             *reinterpret_cast<float4*>(shared + (y * 4 + d4 / (D / 16)) * QUARTER + 4 * (d4 % (D / 16))) = v;
@@ -340,32 +368,31 @@ struct Math<float, D, 1> {
     }
     __device__ __forceinline__ void reset(const RowBlock& B, int g) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < ROWS / 2; ++i)
 #pragma unroll
             for (int x = 0; x < 4; ++x) o[i][x] = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int row = 2 * c() + j;
+        for (int j = 0; j < RL; ++j) {
+            const int row = RL * c() + j;
             m[j] = LOWEST;
             sum[j] = 0.f;
             qpos[j] = row < B.nrows ? B.pos + (B.row0 + row) / g : INT32_MIN;
         }
     }
-    __device__ __forceinline__ void step(uint32_t at, float* shared, int j, int end, bool whole, bool absent, float f) {
+    __device__ __forceinline__ void keys(uint32_t at, float* shared, int j, int end, bool whole, bool absent, float f) {
         const uint32_t sq = smem_u32(shared) + c() * QUARTER * 4;
-        float* weights = shared + ROWS * 4 * QUARTER + (threadIdx.x >> 5) * STEP * ROWS;
-        float2 acc[2][8];
+        float2 acc[2][ROWS];
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int y = 0; y < 8; ++y) acc[k][y] = make_float2(0.f, 0.f);
+            for (int y = 0; y < ROWS; ++y) acc[k][y] = make_float2(0.f, 0.f);
 #pragma unroll
         for (int x = 0; x < D / 16; ++x) {
             float4 k[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) k[i] = shared4(at + 16 * swizzled<R::CH>(r() + 8 * i, c() * (D / 16) + x));
 #pragma unroll
-            for (int y = 0; y < 8; ++y) {
+            for (int y = 0; y < ROWS; ++y) {
                 const float4 v = shared4(sq + (y * 4 * QUARTER + 4 * x) * 4);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -374,19 +401,19 @@ struct Math<float, D, 1> {
                 }
             }
         }
-        float sc[2][2];  // key, row
+        float sc[2][RL];  // key, row
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            float h[4];
+            float h[ROWS / 2];
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                const float a = acc[i][y].x + acc[i][y].y, b = acc[i][4 + y].x + acc[i][4 + y].y;
+            for (int y = 0; y < ROWS / 2; ++y) {
+                const float a = acc[i][y].x + acc[i][y].y, b = acc[i][ROWS / 2 + y].x + acc[i][ROWS / 2 + y].y;
                 const float keep = c() & 2 ? b : a, give = c() & 2 ? a : b;
                 h[y] = keep + __shfl_xor_sync(0xffffffffu, give, 16);
             }
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                const float keep = c() & 1 ? h[2 + y] : h[y], give = c() & 1 ? h[y] : h[2 + y];
+            for (int y = 0; y < RL; ++y) {
+                const float keep = c() & 1 ? h[RL + y] : h[y], give = c() & 1 ? h[y] : h[RL + y];
                 sc[i][y] = keep + __shfl_xor_sync(0xffffffffu, give, 8);
             }
         }
@@ -394,7 +421,7 @@ struct Math<float, D, 1> {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
+            for (int y = 0; y < RL; ++y) {
                 if (!whole) {
                     const int key = j + r() + 8 * i;
                     if (absent || key >= end || key > qpos[y]) sc[i][y] = -INFINITY;
@@ -402,9 +429,9 @@ struct Math<float, D, 1> {
                 raise |= sc[i][y] * f > m[y] + MARGIN;
             }
         if (__any_sync(0xffffffffu, raise)) {
-            float lower[2];
+            float lower[RL];
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
+            for (int y = 0; y < RL; ++y) {
                 float top = fmaxf(sc[0][y], sc[1][y]) * f;
 #pragma unroll
                 for (int x = 1; x < 8; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
@@ -414,51 +441,55 @@ struct Math<float, D, 1> {
                 sum[y] *= lower[y];
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float a = __shfl_sync(0xffffffffu, lower[0], 8 * i), b = __shfl_sync(0xffffffffu, lower[1], 8 * i);
+            for (int y = 0; y < ROWS; ++y) {
+                const float a = __shfl_sync(0xffffffffu, lower[y % RL], 8 * (y / RL));
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    o[i][x].x *= a;
-                    o[i][x].y *= b;
+                    if (y % 2 == 0) o[y / 2][x].x *= a;
+                    else o[y / 2][x].y *= a;
                 }
             }
         }
+        float* w = weights(shared) + r() * ROWS + RL * c();
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            float2 w;
-            w.x = ex2(fmaf(sc[i][0], f, -m[0]));
-            w.y = ex2(fmaf(sc[i][1], f, -m[1]));
-            sum[0] += w.x;
-            sum[1] += w.y;
-            *reinterpret_cast<float2*>(weights + (r() + 8 * i) * ROWS + 2 * c()) = w;
-        }
-        __syncwarp();
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int y = 0; y < RL; ++y) {
+                const float x = ex2(fmaf(sc[i][y], f, -m[y]));
+                sum[y] += x;
+                w[8 * i * ROWS + y] = x;
+            }
+    }
+    __device__ __forceinline__ void values(uint32_t at, float* shared) {  // after the warp has met
         const int lane = threadIdx.x & 31;
-        const uint32_t sw = smem_u32(weights);
+        const uint32_t sw = smem_u32(weights(shared));
 #pragma unroll
         for (int i = 0; i < STEP / KP; ++i) {
             const int key = i * KP + lane / DL;
-            const float4 v = shared4(at + R::PART + 16 * swizzled<R::CH>(key, lane % DL));
-            const float4 a = shared4(sw + key * ROWS * 4), b = shared4(sw + key * ROWS * 4 + 16);
-            const float2 w[4] = {make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)};
+            const float4 v = shared4(at + 16 * swizzled<R::CH>(key, lane % DL));
             const float vx[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int y = 0; y < 4; ++y)
+            for (int y = 0; y < ROWS / 4; ++y) {
+                const float4 a = shared4(sw + (key * ROWS + 4 * y) * 4);
 #pragma unroll
-                for (int x = 0; x < 4; ++x) o[y][x] = fma2(w[y], make_float2(vx[x], vx[x]), o[y][x]);
+                for (int x = 0; x < 4; ++x) {
+                    o[2 * y][x] = fma2(make_float2(a.x, a.y), make_float2(vx[x], vx[x]), o[2 * y][x]);
+                    o[2 * y + 1][x] = fma2(make_float2(a.z, a.w), make_float2(vx[x], vx[x]), o[2 * y + 1][x]);
+                }
+            }
         }
     }
     __device__ __forceinline__ void finish(float* out, float2* stat) {
         const int lane = threadIdx.x & 31;
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
+        for (int y = 0; y < RL; ++y) {
             float t = sum[y];
 #pragma unroll
             for (int x = 1; x < 8; x <<= 1) t += __shfl_xor_sync(0xffffffffu, t, x);
-            if (r() == 0) stat[2 * c() + y] = make_float2(m[y], t);
+            if (r() == 0) stat[RL * c() + y] = make_float2(m[y], t);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < ROWS / 2; ++i) {
 #pragma unroll
             for (int x = 0; x < 4; ++x)
 #pragma unroll
@@ -474,14 +505,20 @@ struct Math<float, D, 1> {
     }
 };
 
-// ------------------------------------------------------------------ the kernel
+// ------------------------------------------------------------------ the kernels
 
-template <typename T, int D, int NB>
-constexpr size_t smem_bytes() {
-    using M = Math<T, D, NB>;
-    static_assert(M::ROWS * D * 4 <= Ring<T, D>::BYTES, "a warp's outputs take its ring's place");
-    return WARPS * Ring<T, D>::BYTES + M::SHARED * 4 + WARPS * M::ROWS * sizeof(float2);
-}
+// Shared memory: the warps' rings, which later hold their outputs; queries and weights (fp32); the
+// warps' statistics; in a cluster what the CTAs hand to this one: a slice of the columns, 16 parts at
+// most of a share that gets smaller with their number, and every part's statistics.
+template <typename T, int D, int NB, int NW>
+struct Shared {
+    using M = Math<T, D, NB, NW>;
+    static constexpr int ROWS = M::ROWS, RING = Ring<T, D>::BYTES;
+    static_assert(ROWS * D * 4 <= RING, "a warp's outputs take its ring's place");
+    static constexpr int MORE = NW * RING, STAT = MORE + M::SHARED * 4, JOIN = STAT + NW * ROWS * 8;
+    static constexpr int NT = 32 * NW, JOIN_STAT = JOIN + (ROWS * (D / 4) + NT - 1) / NT * NT * 16;
+    static constexpr int bytes(bool cluster) { return cluster ? JOIN_STAT + 16 * ROWS * 8 : JOIN; }
+};
 
 // Outputs and statistics of one row's parts, each with a reference.
 struct Joined {
@@ -491,6 +528,9 @@ struct Joined {
     __device__ __forceinline__ void add(float2 st, float4 o) {
         const float w = ex2(st.x - m);
         sum = fmaf(w, st.y, sum);
+        weigh(w, o);
+    }
+    __device__ __forceinline__ void weigh(float w, float4 o) {
         acc.x = fmaf(w, o.x, acc.x);
         acc.y = fmaf(w, o.y, acc.y);
         acc.z = fmaf(w, o.z, acc.z);
@@ -523,10 +563,72 @@ __device__ __forceinline__ void write_row(const AttnParams& P, int l, RowPlace a
     if (d4 == 0 && P.lse) P.lse[row] = z.lse();
 }
 
-// After a piece of a unit is written: the last CTA of the unit to arrive joins the pieces, in order.
-template <typename T, int D, int ROWS>
+// A CTA's NW warps over keys [k0, k1) of a unit; their outputs and statistics are in shared memory
+// afterwards, for every thread to read.
+template <typename T, int D, int NB, int NW>
+__device__ __forceinline__ void attend(const AttnParams& P, const RowBlock& B, int s, int l, int h, int k0, int k1, uint8_t* smem) {
+    using M = Math<T, D, NB, NW>;
+    using R = Ring<T, D>;
+    using S = Shared<T, D, NB, NW>;
+    const int warp = threadIdx.x >> 5;
+    uint8_t* mine = smem + warp * R::BYTES;
+    float* shared = reinterpret_cast<float*>(smem + S::MORE);
+    Feeder<T, D, NW> feed;
+    feed.ring = smem_u32(mine);
+    feed.begin(P, s, (static_cast<int64_t>(P.c.l_begin) + l) * P.c.n_pages * P.c.H + h, k0 + STEP * warp, k1);
+    M math;
+    math.load(shared, B.nrows, [&](int row) { return address<T>(P.query, l, place_of(P, B, h, row)); });
+    static_assert(R::DEPTH >= 3, "a step's K, its V and the next K");
+#pragma unroll
+    for (int m = 0; m < R::DEPTH - 1; ++m) {
+        if (m % 2 == 0) feed.template ask<0>(P, m / 2);
+        else feed.template ask<1>(P, m / 2);
+    }
+    math.reset(B, P.g);
+    if constexpr (M::SHARED > 0) __syncthreads();  // the queries
+    // the part that is asked for while part m is used is m + DEPTH - 1, in the place of part m - 1
+    constexpr int NEXT_K = (R::DEPTH - 1) % 2, NEXT_V = R::DEPTH % 2;
+    int stage = 0;
+    for (int n = 0; n < feed.steps; ++n) {
+        copies_wait<R::DEPTH - 2>();
+        const bool absent = (feed.absent >> stage) & 1;
+        __syncwarp();  // every lane's copies of the part are there, and the part before it has been used
+        feed.template ask<NEXT_K>(P, n + (R::DEPTH - 1) / 2);
+        const int j = feed.first + feed.TILE * n;
+        const bool whole = !absent && j + STEP <= k1 && j + STEP - 1 <= B.pos_lo;
+        math.keys(feed.ring + stage * R::PART, shared, j, k1, whole, absent, P.scale_log2);
+        stage = stage + 1 == R::DEPTH ? 0 : stage + 1;
+        copies_wait<R::DEPTH - 2>();
+        __syncwarp();
+        feed.template ask<NEXT_V>(P, n + R::DEPTH / 2);
+        math.values(feed.ring + stage * R::PART, shared);
+        stage = stage + 1 == R::DEPTH ? 0 : stage + 1;
+    }
+    copies_wait<0>();
+    __syncwarp();
+    math.finish(reinterpret_cast<float*>(mine), reinterpret_cast<float2*>(smem + S::STAT) + warp * S::ROWS);
+    __syncthreads();
+}
+
+// Four columns of a row over a CTA's warps.
+template <typename T, int D, int NB, int NW>
+__device__ __forceinline__ Joined join_warps(const uint8_t* smem, int row, int d4) {
+    using S = Shared<T, D, NB, NW>;
+    const float2* stat = reinterpret_cast<const float2*>(smem + S::STAT) + row;
+    Joined z;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) z.reference(stat[w * S::ROWS]);
+#pragma unroll
+    for (int w = 0; w < NW; ++w) z.add(stat[w * S::ROWS], reinterpret_cast<const float4*>(smem + w * S::RING + row * D * 4)[d4]);
+    return z;
+}
+
+// After a piece of a unit is written: the last CTA of the unit to arrive joins the pieces, in
+// order.  A warp takes a row's references and sum, the weights of all pieces go to shared memory (`buf`,
+// `cap` floats, free), then each thread adds its columns with its loads in flight together.
+template <typename T, int D, int ROWS, int NT>
 __device__ __forceinline__ void join_pieces(const AttnParams& P, const RowBlock& B, const Pieces& pieces, int64_t unit, int l, int h,
-                                            int* s_last) {
+                                            int* s_last, float* buf, int cap) {
     __threadfence();
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -540,32 +642,54 @@ __device__ __forceinline__ void join_pieces(const AttnParams& P, const RowBlock&
     __syncthreads();
     if (!*s_last) return;
     __threadfence();
+    const int n = pieces.n, lane = threadIdx.x & 31;
+    float2* whole = reinterpret_cast<float2*>(buf);  // [ROWS] reference, sum
+    float* weight = buf + 2 * ROWS;                  // [row][piece]
+    const bool listed = n <= (cap - 2 * ROWS) / ROWS;
+    auto stat = [&](int row, int i) { return __ldcg(P.part_stat + pieces.slot(i) * ROWS + row); };
+    for (int row = threadIdx.x >> 5; row < B.nrows; row += NT / 32) {
+        float m = LOWEST, sum = 0.f;
+        float2 st[2];  // of 64 pieces; more are read again
+#pragma unroll
+        for (int i = 0; i < 2; ++i) st[i] = lane + 32 * i < n ? stat(row, lane + 32 * i) : make_float2(LOWEST, 0.f);
+        m = fmaxf(st[0].x, st[1].x);
+        for (int i = lane + 64; i < n; i += 32) m = fmaxf(m, stat(row, i).x);
+#pragma unroll
+        for (int x = 1; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+        for (int i = lane, c = 0; i < n; i += 32, ++c) {
+            const float2 y = c == 0 ? st[0] : c == 1 ? st[1] : stat(row, i);
+            const float w = ex2(y.x - m);
+            sum = fmaf(w, y.y, sum);
+            if (listed) weight[row * n + i] = w;
+        }
+#pragma unroll
+        for (int x = 1; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+        if (lane == 0) whole[row] = make_float2(m, sum);
+    }
+    __syncthreads();
     for (int i = threadIdx.x; i < B.nrows * (D / 4); i += NT) {
         const int row = i / (D / 4), d4 = i % (D / 4);
         Joined z;
-#pragma unroll 8
-        for (int p = 0; p < pieces.n; ++p) z.reference(__ldcg(P.part_stat + pieces.slot(p) * ROWS + row));
-#pragma unroll 8
-        for (int p = 0; p < pieces.n; ++p)
-            z.add(__ldcg(P.part_stat + pieces.slot(p) * ROWS + row),
-                  __ldcg(reinterpret_cast<const float4*>(P.partial + (pieces.slot(p) * ROWS + row) * D) + d4));
+        z.m = whole[row].x;
+        z.sum = whole[row].y;
+#pragma unroll 16
+        for (int p = 0; p < n; ++p)
+            z.weigh(listed ? weight[row * n + p] : ex2(stat(row, p).x - z.m),
+                    __ldcg(reinterpret_cast<const float4*>(P.partial + (pieces.slot(p) * ROWS + row) * D) + d4));
         write_row<T>(P, l, place_of(P, B, h, row), d4, z);
     }
 }
 
+// Many keys: the line of tiles, shared evenly by the CTAs that fit the GPU.
 template <typename T, int D, int NB>
-__global__ void __launch_bounds__(NT) attention_kernel(const __grid_constant__ AttnParams P) {
-    using M = Math<T, D, NB>;
-    using R = Ring<T, D>;
-    constexpr int ROWS = M::ROWS;
+__global__ void __launch_bounds__(32 * WARPS) line_kernel(const __grid_constant__ AttnParams P) {
+    constexpr int NT = 32 * WARPS;
+    using S = Shared<T, D, NB, WARPS>;
+    constexpr int ROWS = S::ROWS;
     extern __shared__ __align__(128) uint8_t smem[];
-    float* shared = reinterpret_cast<float*>(smem + WARPS * R::BYTES);
-    float2* stat = reinterpret_cast<float2*>(shared + M::SHARED);  // [WARPS][ROWS]
     __shared__ int s_last;
     __shared__ LineStart s_start;
     __shared__ int s_scan[WARPS];
-    const int warp = threadIdx.x >> 5;
-    float* mine = reinterpret_cast<float*>(smem + warp * R::BYTES);  // the warp's ring, and later its outputs
 
     int at, stop, share, l, e, h, first;
     if (!c8::line_start<ROWS, TILE, NT>(P, s_scan, &s_start, at, stop, share, l, e, h, first)) return;
@@ -576,33 +700,8 @@ __global__ void __launch_bounds__(NT) attention_kernel(const __grid_constant__ A
 
     for (;;) {  // one unit, or a piece of one, after another
         const int last = min(tiles, first + (stop - at));  // tiles [first, last)
-        const int k0 = first * TILE, k1 = min(B.kv_end, last * TILE);
         const int64_t unit = (static_cast<int64_t>(l) * entries + e) * P.c.H + h;
-
-        Feeder<T, D> feed;
-        feed.ring = smem_u32(mine);
-        feed.begin(P, e / P.row_blocks, (static_cast<int64_t>(P.c.l_begin) + l) * P.c.n_pages * P.c.H + h, k0 + STEP * warp, k1);
-        M math;
-        math.load(shared, B.nrows, [&](int row) { return address<T>(P.query, l, place_of(P, B, h, row)); });
-#pragma unroll
-        for (int n = 0; n < R::DEPTH - 1; ++n) feed.ask(P, n);
-        math.reset(B, P.g);
-        if constexpr (M::SHARED > 0) __syncthreads();  // the queries
-        int stage = 0;
-        for (int n = 0; n < feed.steps; ++n) {
-            copies_wait<R::DEPTH - 2>();
-            const bool absent = (feed.absent >> stage) & 1;
-            __syncwarp();  // every lane's copies of step n are there, and step n - 1 has been used
-            feed.ask(P, n + R::DEPTH - 1);
-            const int j = feed.first + TILE * n;
-            const bool whole = !absent && j + STEP <= k1 && j + STEP - 1 <= B.pos_lo;
-            math.step(feed.ring + stage * 2 * R::PART, shared, j, k1, whole, absent, P.scale_log2);
-            stage = stage + 1 == R::DEPTH ? 0 : stage + 1;
-        }
-        copies_wait<0>();
-        __syncwarp();
-        math.finish(mine, stat + warp * ROWS);
-        __syncthreads();
+        attend<T, D, NB, WARPS>(P, B, e / P.row_blocks, l, h, first * TILE, min(B.kv_end, last * TILE), smem);
 
         // the CTAs that share this unit, and this one's slot
         const int u0 = at - first, c0 = u0 / share;
@@ -610,12 +709,7 @@ __global__ void __launch_bounds__(NT) attention_kernel(const __grid_constant__ A
         const int64_t part0 = (2 * static_cast<int64_t>(blockIdx.x) + (first == 0)) * ROWS;
         for (int i = threadIdx.x; i < B.nrows * (D / 4); i += NT) {
             const int row = i / (D / 4), d4 = i % (D / 4);
-            Joined z;
-#pragma unroll
-            for (int w = 0; w < WARPS; ++w) z.reference(stat[w * ROWS + row]);
-#pragma unroll
-            for (int w = 0; w < WARPS; ++w)
-                z.add(stat[w * ROWS + row], reinterpret_cast<const float4*>(smem + w * R::BYTES + row * D * 4)[d4]);
+            const Joined z = join_warps<T, D, NB, WARPS>(smem, row, d4);
             if (pieces == 1) {
                 write_row<T>(P, l, place_of(P, B, h, row), d4, z);
             } else if (KVB_IN_BOUNDS(P.err, part0 + row, 1, P.slots * ROWS)) {
@@ -623,7 +717,8 @@ __global__ void __launch_bounds__(NT) attention_kernel(const __grid_constant__ A
                 if (d4 == 0) P.part_stat[part0 + row] = make_float2(z.m, z.sum);
             }
         }
-        if (pieces > 1) join_pieces<T, D, ROWS>(P, B, Pieces{pieces, c0}, unit, l, h, &s_last);
+        if (pieces > 1)
+            join_pieces<T, D, ROWS, NT>(P, B, Pieces{pieces, c0}, unit, l, h, &s_last, reinterpret_cast<float*>(smem), S::MORE / 4);
 
         at += last - first;
         if (at >= stop) return;
@@ -643,46 +738,166 @@ __global__ void __launch_bounds__(NT) attention_kernel(const __grid_constant__ A
     }
 }
 
-// One instance: CTAs of it that fit an SM (P null), or its launch.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// Shared memory of CTA `rank` of the cluster, at the address that p has in this one.
+__device__ __forceinline__ uint32_t of_rank(uint32_t p, int rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(p), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void hand4(uint32_t p, float4 v) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(p), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+}
+__device__ __forceinline__ void hand2(uint32_t p, float2 v) {
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1,%2};" ::"r"(p), "f"(v.x), "f"(v.y) : "memory");
+}
+
+// Few keys: a cluster of CTAs for each unit, an even share of its keys each.  Every CTA hands each of
+// the others its part of the columns that the other joins, through distributed shared memory: no
+// global scratch, no atomics.
 template <typename T, int D, int NB>
-cudaError_t instance(const AttnParams* P, int ctas, cudaStream_t s, int* fit) {
-    constexpr size_t smem = smem_bytes<T, D, NB>();
-    const auto kernel = attention_kernel<T, D, NB>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+__global__ void __launch_bounds__(32 * WARPS) cluster_kernel(const __grid_constant__ AttnParams P) {
+    constexpr int NT = 32 * WARPS;
+    using S = Shared<T, D, NB, WARPS>;
+    constexpr int ROWS = S::ROWS;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int parts = P.cluster, part = static_cast<int>(blockIdx.x) % parts;  // a power of two, at most 16
+    if (parts > 1) cluster_arrive();  // the others may be written to once all have come here
+    int unit = static_cast<int>(blockIdx.x) / parts;
+    const int h = unit % P.c.H;
+    unit /= P.c.H;
+    const int entries = P.q.n_seq * P.row_blocks;
+    const int e = unit % entries, l = unit / entries;
+    const RowBlock B = c8::row_block(P, e / P.row_blocks, e % P.row_blocks, ROWS);
+    const int items = B.nrows * (D / 4);  // 0: none of the cluster has rows
+    if (items > 0) {
+        const int tiles = (B.kv_end + TILE - 1) / TILE;
+        const int share = (tiles + parts - 1) / parts * TILE;
+        attend<T, D, NB, WARPS>(P, B, e / P.row_blocks, l, h, min(B.kv_end, part * share), min(B.kv_end, (part + 1) * share), smem);
+    }
+    if (parts > 1) cluster_wait();
+    // item i = four columns of a row: joined by CTA (i / per) % parts, as number i / NT * per + i % per of its own
+    const int per = NT / parts;
+    const uint32_t join = smem_u32(smem + S::JOIN), join_stat = smem_u32(smem + S::JOIN_STAT);
+    for (int i = threadIdx.x; i < items; i += NT) {
+        const int row = i / (D / 4), d4 = i % (D / 4);
+        const Joined z = join_warps<T, D, NB, WARPS>(smem, row, d4);
+        if (parts == 1) {
+            write_row<T>(P, l, place_of(P, B, h, row), d4, z);
+        } else {
+            hand4(of_rank(join + 16 * ((i / NT * per + i % per) * parts + part), i / per % parts), z.acc);
+            for (int x = d4; x < parts; x += D / 4) hand2(of_rank(join_stat + 8 * (row * parts + part), x), make_float2(z.m, z.sum));
+        }
+    }
+    if (parts == 1) return;
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+    // `parts` lanes take an item's parts, one each, and add them in a tree
+    const float4* acc = reinterpret_cast<const float4*>(smem + S::JOIN);
+    const float2* stat = reinterpret_cast<const float2*>(smem + S::JOIN_STAT);
+    const int from = threadIdx.x % parts;
+    for (int round = 0; round * NT + part * per < items; ++round) {
+        const int y = round * per + static_cast<int>(threadIdx.x) / parts, i = round * NT + part * per + static_cast<int>(threadIdx.x) / parts;
+        const int row = min(i, items - 1) / (D / 4), d4 = min(i, items - 1) % (D / 4);
+        Joined z;
+        const float2 st = stat[row * parts + from];
+        z.m = st.x;
+        for (int x = 1; x < parts; x <<= 1) z.m = fmaxf(z.m, __shfl_xor_sync(0xffffffffu, z.m, x));
+        z.add(st, i < items ? acc[y * parts + from] : make_float4(0.f, 0.f, 0.f, 0.f));
+        for (int x = 1; x < parts; x <<= 1) {
+            z.sum += __shfl_xor_sync(0xffffffffu, z.sum, x);
+            z.acc.x += __shfl_xor_sync(0xffffffffu, z.acc.x, x);
+            z.acc.y += __shfl_xor_sync(0xffffffffu, z.acc.y, x);
+            z.acc.z += __shfl_xor_sync(0xffffffffu, z.acc.z, x);
+            z.acc.w += __shfl_xor_sync(0xffffffffu, z.acc.w, x);
+        }
+        if (i < items && from == 0) write_row<T>(P, l, place_of(P, B, h, row), d4, z);
+    }
+}
+
+// One instance of the line: CTAs of it that fit an SM (P null), or its launch.
+template <typename T, int D, int NB>
+cudaError_t line_instance(const AttnParams* P, int ctas, cudaStream_t s, int* fit) {
+    constexpr int smem = Shared<T, D, NB, WARPS>::bytes(false);
+    const auto kernel = line_kernel<T, D, NB>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     if (!P) {
         static const int resident = [&] {
             int n = 0;
-            return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, NT, smem) == cudaSuccess ? n : 0;
+            return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, 32 * WARPS, smem) == cudaSuccess ? n : 0;
         }();
         *fit = resident;
         return cudaSuccess;
     }
-    kernel<<<ctas, NT, smem, s>>>(*P);
+    kernel<<<ctas, 32 * WARPS, smem, s>>>(*P);
     return cudaGetLastError();
 }
 
-template <typename T, int D>
-cudaError_t instance_rows(int rows, const AttnParams* P, int ctas, cudaStream_t s, int* fit) {
-    if constexpr (sizeof(T) == 2) {
-        if (rows == 32) return instance<T, D, 4>(P, ctas, s, fit);
-        if (rows == 16) return instance<T, D, 2>(P, ctas, s, fit);
+// One instance of the clusters: how many of each size are resident at once (P null), or its launch.
+template <typename T, int D, int NB>
+cudaError_t cluster_instance(const AttnParams* P, int cluster, int ctas, cudaStream_t s, int* fit) {
+    constexpr int smem = Shared<T, D, NB, WARPS>::bytes(true);
+    const auto kernel = cluster_kernel<T, D, NB>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.blockDim = dim3(32 * WARPS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (!P) {
+        struct Resident {
+            int n[5];
+        };
+        static const Resident resident = [&] {
+            Resident r{};
+            for (int i = 0; i < 5; ++i) {
+                attr.val.clusterDim.x = 1u << i;
+                cfg.gridDim = dim3(1u << i);
+                if (cudaOccupancyMaxActiveClusters(&r.n[i], kernel, &cfg) != cudaSuccess) r.n[i] = 0;
+            }
+            (void)cudaGetLastError();
+            return r;
+        }();
+        for (int i = 0; i < 5; ++i) fit[i] = resident.n[i];
+        return cudaSuccess;
     }
-    return instance<T, D, 1>(P, ctas, s, fit);
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    return cudaLaunchKernelEx(&cfg, kernel, *P);
+}
+
+template <typename T, int D, int NB>
+cudaError_t instance(const AttnParams* P, const AttnPlan& p, cudaStream_t s, int* fit) {
+    return p.cluster ? cluster_instance<T, D, NB>(P, p.cluster, p.ctas, s, fit) : line_instance<T, D, NB>(P, p.ctas, s, fit);
+}
+
+template <typename T, int D>
+cudaError_t instance_rows(const AttnPlan& p, const AttnParams* P, cudaStream_t s, int* fit) {
+    if constexpr (sizeof(T) == 4) return p.rows == 4 ? instance<T, D, 4>(P, p, s, fit) : instance<T, D, 8>(P, p, s, fit);
+    else return p.rows == 32 ? instance<T, D, 4>(P, p, s, fit) : p.rows == 16 ? instance<T, D, 2>(P, p, s, fit) : instance<T, D, 1>(P, p, s, fit);
 }
 
 template <typename T>
-cudaError_t instance_dim(int d, int rows, const AttnParams* P, int ctas, cudaStream_t s, int* fit) {
+cudaError_t instance_dim(int d, const AttnPlan& p, const AttnParams* P, cudaStream_t s, int* fit) {
     switch (d) {
-        case 16: return instance_rows<T, 16>(rows, P, ctas, s, fit);
-        case 32: return instance_rows<T, 32>(rows, P, ctas, s, fit);
-        case 64: return instance_rows<T, 64>(rows, P, ctas, s, fit);
-        default: return instance_rows<T, 128>(rows, P, ctas, s, fit);
+        case 16: return instance_rows<T, 16>(p, P, s, fit);
+        case 32: return instance_rows<T, 32>(p, P, s, fit);
+        case 64: return instance_rows<T, 64>(p, P, s, fit);
+        default: return instance_rows<T, 128>(p, P, s, fit);
     }
 }
 
-cudaError_t pick(kvb_dtype dtype, int d, int rows, const AttnParams* P, int ctas, cudaStream_t s, int* fit) {
-    return dtype == KVB_BF16 ? instance_dim<__nv_bfloat16>(d, rows, P, ctas, s, fit) : instance_dim<float>(d, rows, P, ctas, s, fit);
+cudaError_t pick(kvb_dtype dtype, int d, const AttnPlan& p, const AttnParams* P, cudaStream_t s, int* fit) {
+    return dtype == KVB_BF16 ? instance_dim<__nv_bfloat16>(d, p, P, s, fit) : instance_dim<float>(d, p, P, s, fit);
 }
 
 }  // namespace
@@ -691,15 +906,27 @@ AttnPlan plan_attention(const Pages& c, const Seqs& q, kvb_dtype dtype, int g, i
     AttnPlan p{};
     const int64_t most = static_cast<int64_t>(q.max_tokens) * g;  // rows of one sequence and head
     const int64_t max_kv = q.max_kv > 0 ? q.max_kv : 1;
-    p.rows = dtype == KVB_F32 || most <= 8 ? 8 : most <= 16 ? 16 : 32;
+    p.rows = dtype == KVB_F32 ? (most <= 4 ? 4 : 8) : most <= 8 ? 8 : most <= 16 ? 16 : 32;
     const double blocks = static_cast<double>((most + p.rows - 1) / p.rows);
     const double units = blocks * c.n_layers * q.n_seq * c.H;
     p.tiles = units * ((max_kv + TILE - 1) / TILE);
     if (p.tiles > static_cast<double>(1 << 30)) return p;  // refused
     p.row_blocks = static_cast<int>(blocks);
     p.units = static_cast<int64_t>(units);
+    const int64_t shares = (max_kv + TILE - 1) / TILE;  // steps of a unit, by a CTA
+    if (p.units <= num_sms && shares <= FEW_SHARES * 16) {
+        int most_of[5] = {};
+        p.cluster = 1;
+        pick(dtype, c.d, p, nullptr, nullptr, most_of);
+        // the largest cluster of which all are resident at once, no larger than the keys have steps for
+        for (int i = 1; i < 5; ++i)
+            if (p.units <= most_of[i] && (1 << i) < 2 * shares) p.cluster = 1 << i;
+        p.ctas = static_cast<int>(p.units) * p.cluster;
+        if (p.units <= most_of[0] && shares <= static_cast<int64_t>(FEW_SHARES) * p.cluster) return p;
+        p.cluster = 0;
+    }
     int fit = 1;
-    pick(dtype, c.d, p.rows, nullptr, 0, nullptr, &fit);
+    pick(dtype, c.d, p, nullptr, nullptr, &fit);
     // the CTAs that fit the GPU, no more than the keys give the least share to
     p.min_tiles = MIN_TILES;
     const double need = (p.tiles + p.min_tiles - 1) / p.min_tiles;
@@ -712,7 +939,7 @@ AttnPlan plan_attention(const Pages& c, const Seqs& q, kvb_dtype dtype, int g, i
 }
 
 cudaError_t launch_attention(const AttnParams& P, kvb_dtype dtype, const AttnPlan& p, cudaStream_t s) {
-    return pick(dtype, P.c.d, p.rows, &P, p.ctas, s, nullptr);
+    return pick(dtype, P.c.d, p, &P, s, nullptr);
 }
 
 }  // namespace paged

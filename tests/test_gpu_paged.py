@@ -684,11 +684,11 @@ def test_contexts_of_their_own_on_two_streams(kvb):
 
 
 def test_growing_on_a_captured_stream_is_refused(kvb):
-    P = Pool(kvb, 1, 2, 128, 64, 1, 5000, BF)
-    P.fill([5000])
+    P = Pool(kvb, 1, 2, 128, 64, 1, 70000, BF)  # few keys have no workspace
+    P.fill([70000])
     q = P.rows(1, 16, 1)
     out = torch.empty_like(q)
-    seqs = P.seqs([0, 1], [4999])
+    seqs = P.seqs([0, 1], [69999])
     side = torch.cuda.Stream()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph, stream=side):
@@ -696,7 +696,7 @@ def test_growing_on_a_captured_stream_is_refused(kvb):
         out.zero_()
     kvb.kvb_paged_attention(P.ctx, P.cache, seqs, q, out)
     kvb.kvb_ctx_check(P.ctx)
-    check_attention(P, q, [0, 1], [4999], out, None)
+    check_attention(P, q, [0, 1], [69999], out, None)
 
 
 # ------------------------------------------------------------------ refusals
