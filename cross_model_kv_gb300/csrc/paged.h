@@ -59,6 +59,7 @@ struct AttnParams {
 
 // How a call is cut: blocks of `rows` query rows, and their keys over CTAs.
 struct AttnPlan {
+    bool tensor;  // the tcgen05 kernel
     int rows, row_blocks, min_tiles, cluster, ctas;
     int64_t units, slots;
     double tiles;
@@ -66,6 +67,8 @@ struct AttnPlan {
 };
 AttnPlan plan_attention(const Pages& c, const Seqs& q, kvb_dtype dtype, int g, int num_sms);
 cudaError_t launch_attention(const AttnParams& P, kvb_dtype dtype, const AttnPlan& p, cudaStream_t s);
+constexpr int TENSOR_ROWS = 128;  // of a unit in the tcgen05 kernel
+cudaError_t launch_attention_rows(const AttnParams& P, const AttnPlan& p, cudaStream_t s, std::string* why);  // bf16, d 64 and 128
 
 }  // namespace paged
 }  // namespace kvb

@@ -181,8 +181,10 @@ kvb_status kvb_paged_attention(kvb_ctx* c, const kvb_paged_cache* cache, const k
         a.row_blocks = p.row_blocks;
         a.min_tiles = p.min_tiles;
         a.cluster = p.cluster;
-        ProfScope ps(c, s, "paged_attention");
-        const cudaError_t e = paged::launch_attention(a, cache->dtype, p, s);
+        std::string why;
+        ProfScope ps(c, s, p.tensor ? "paged_attention_tcgen05" : "paged_attention");
+        const cudaError_t e = p.tensor ? paged::launch_attention_rows(a, p, s, &why) : paged::launch_attention(a, cache->dtype, p, s);
+        if (e != cudaSuccess && !why.empty()) return fail(KVB_ERR_CUDA, "paged attention launch: " + why);
         return e == cudaSuccess ? KVB_OK : cuda_fail(e, "paged attention launch");
     });
 }

@@ -19,27 +19,18 @@
 // The keys of all units (layer, sequence, row block, head) form one line of 64-key tiles that the
 // CTAs which fit the GPU share evenly; the last CTA to arrive at a unit that several share joins
 // its pieces in order, so results do not depend on timing.
-#include <cfloat>
-
-#include "cache8_attn.cuh"
-#include "paged.h"
+#include "paged_attn.cuh"
 
 namespace kvb {
 namespace paged {
 
 namespace {
 
-using c8::ex2;
-using c8::LineStart;
-using c8::Pieces;
-using c8::RowBlock;
-
 constexpr int WARPS = 4;              // of a CTA of the line
 constexpr int STEP = 16;              // keys of a warp's step
 constexpr int TILE = STEP * WARPS;    // a tile of the line
-constexpr float MARGIN = 8.f;         // a reference is raised past this much (base 2)
-constexpr float LOWEST = -FLT_MAX;    // reference of a row that has seen nothing
 constexpr int MIN_TILES = 2;
+constexpr int MMA_ROWS = 16;           // bf16 rows up to which mma.sync keeps up (d 64, 128)
 constexpr int FEW_SHARES = 32;          // steps of a warp up to which a cluster takes a unit
 
 // A step's K or V rows in shared memory: 16-byte chunks, chunk c of row r at c ^ swizzle(r), so that
@@ -323,15 +314,6 @@ struct Math<__nv_bfloat16, D, NB, NW> {
 
 // ------------------------------------------------------------------ fp32: CUDA cores
 
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {  // two in one instruction
-    float2 d;
-    asm("{\n\t.reg .b64 x, y, z, w;\n\t"
-        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
-        "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return d;
-}
 __device__ __forceinline__ float4 shared4(uint32_t p) {
     float4 v;
     asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(p) : "memory");
@@ -520,49 +502,6 @@ struct Shared {
     static constexpr int bytes(bool cluster) { return cluster ? JOIN_STAT + 16 * ROWS * 8 : JOIN; }
 };
 
-// Outputs and statistics of one row's parts, each with a reference.
-struct Joined {
-    float m = LOWEST, sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    __device__ __forceinline__ void reference(float2 st) { m = fmaxf(m, st.x); }
-    __device__ __forceinline__ void add(float2 st, float4 o) {
-        const float w = ex2(st.x - m);
-        sum = fmaf(w, st.y, sum);
-        weigh(w, o);
-    }
-    __device__ __forceinline__ void weigh(float w, float4 o) {
-        acc.x = fmaf(w, o.x, acc.x);
-        acc.y = fmaf(w, o.y, acc.y);
-        acc.z = fmaf(w, o.z, acc.z);
-        acc.w = fmaf(w, o.w, acc.w);
-    }
-    __device__ __forceinline__ float4 output() const {
-        const float f = sum == 0.f ? 0.f : 1.f / sum;
-        return make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
-    }
-    __device__ __forceinline__ float lse() const { return sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.693147180559945f; }
-};
-
-// Row `row` of a unit, in rows with strides and in [n_layers][Hq][T].
-struct RowPlace {
-    int head, token;
-};
-__device__ __forceinline__ RowPlace place_of(const AttnParams& P, const RowBlock& B, int h, int row) {
-    const int gr = B.row0 + row, i = gr / P.g;
-    return RowPlace{h * P.g + (gr - i * P.g), B.tok0 + i};
-}
-template <typename T>
-__device__ __forceinline__ T* address(const Rows& r, int l, RowPlace at) {
-    return static_cast<T*>(r.data) + (l * r.l + at.head * r.h + at.token * r.t);
-}
-template <typename T>
-__device__ __forceinline__ void write_row(const AttnParams& P, int l, RowPlace at, int d4, const Joined& z) {
-    const int64_t row = (static_cast<int64_t>(l) * P.c.H * P.g + at.head) * P.q.T + at.token;
-    if (!KVB_IN_BOUNDS(P.err, row, 1, c8::rows_of(P))) return;
-    c8::store_out(address<T>(P.out, l, at) + 4 * d4, z.output());
-    if (d4 == 0 && P.lse) P.lse[row] = z.lse();
-}
-
 // A CTA's NW warps over keys [k0, k1) of a unit; their outputs and statistics are in shared memory
 // afterwards, for every thread to read.
 template <typename T, int D, int NB, int NW>
@@ -623,63 +562,6 @@ __device__ __forceinline__ Joined join_warps(const uint8_t* smem, int row, int d
     return z;
 }
 
-// After a piece of a unit is written: the last CTA of the unit to arrive joins the pieces, in
-// order.  A warp takes a row's references and sum, the weights of all pieces go to shared memory (`buf`,
-// `cap` floats, free), then each thread adds its columns with its loads in flight together.
-template <typename T, int D, int ROWS, int NT>
-__device__ __forceinline__ void join_pieces(const AttnParams& P, const RowBlock& B, const Pieces& pieces, int64_t unit, int l, int h,
-                                            int* s_last, float* buf, int cap) {
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        *s_last = false;
-        if (KVB_IN_BOUNDS(P.err, unit, 1, P.units) && c8::pieces_in_bounds(P, pieces)) {
-            const int n = atomicAdd(P.counters + unit, 1);
-            *s_last = n == pieces.n - 1;
-            if (n == pieces.n - 1) P.counters[unit] = 0;
-        }
-    }
-    __syncthreads();
-    if (!*s_last) return;
-    __threadfence();
-    const int n = pieces.n, lane = threadIdx.x & 31;
-    float2* whole = reinterpret_cast<float2*>(buf);  // [ROWS] reference, sum
-    float* weight = buf + 2 * ROWS;                  // [row][piece]
-    const bool listed = n <= (cap - 2 * ROWS) / ROWS;
-    auto stat = [&](int row, int i) { return __ldcg(P.part_stat + pieces.slot(i) * ROWS + row); };
-    for (int row = threadIdx.x >> 5; row < B.nrows; row += NT / 32) {
-        float m = LOWEST, sum = 0.f;
-        float2 st[2];  // of 64 pieces; more are read again
-#pragma unroll
-        for (int i = 0; i < 2; ++i) st[i] = lane + 32 * i < n ? stat(row, lane + 32 * i) : make_float2(LOWEST, 0.f);
-        m = fmaxf(st[0].x, st[1].x);
-        for (int i = lane + 64; i < n; i += 32) m = fmaxf(m, stat(row, i).x);
-#pragma unroll
-        for (int x = 1; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-        for (int i = lane, c = 0; i < n; i += 32, ++c) {
-            const float2 y = c == 0 ? st[0] : c == 1 ? st[1] : stat(row, i);
-            const float w = ex2(y.x - m);
-            sum = fmaf(w, y.y, sum);
-            if (listed) weight[row * n + i] = w;
-        }
-#pragma unroll
-        for (int x = 1; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-        if (lane == 0) whole[row] = make_float2(m, sum);
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < B.nrows * (D / 4); i += NT) {
-        const int row = i / (D / 4), d4 = i % (D / 4);
-        Joined z;
-        z.m = whole[row].x;
-        z.sum = whole[row].y;
-#pragma unroll 16
-        for (int p = 0; p < n; ++p)
-            z.weigh(listed ? weight[row * n + p] : ex2(stat(row, p).x - z.m),
-                    __ldcg(reinterpret_cast<const float4*>(P.partial + (pieces.slot(p) * ROWS + row) * D) + d4));
-        write_row<T>(P, l, place_of(P, B, h, row), d4, z);
-    }
-}
-
 // Many keys: the line of tiles, shared evenly by the CTAs that fit the GPU.
 template <typename T, int D, int NB>
 __global__ void __launch_bounds__(32 * WARPS) line_kernel(const __grid_constant__ AttnParams P) {
@@ -718,7 +600,8 @@ __global__ void __launch_bounds__(32 * WARPS) line_kernel(const __grid_constant_
             }
         }
         if (pieces > 1)
-            join_pieces<T, D, ROWS, NT>(P, B, Pieces{pieces, c0}, unit, l, h, &s_last, reinterpret_cast<float*>(smem), S::MORE / 4);
+            join_pieces<T, D, ROWS, NT>(P, B, Pieces{pieces, c0}, unit, l, h, &s_last, reinterpret_cast<float*>(smem), S::MORE / 4,
+                                        [] { __syncthreads(); });
 
         at += last - first;
         if (at >= stop) return;
@@ -906,7 +789,9 @@ AttnPlan plan_attention(const Pages& c, const Seqs& q, kvb_dtype dtype, int g, i
     AttnPlan p{};
     const int64_t most = static_cast<int64_t>(q.max_tokens) * g;  // rows of one sequence and head
     const int64_t max_kv = q.max_kv > 0 ? q.max_kv : 1;
-    p.rows = dtype == KVB_F32 ? (most <= 4 ? 4 : 8) : most <= 8 ? 8 : most <= 16 ? 16 : 32;
+    const double all_blocks = (static_cast<double>(c.l_begin) + c.n_layers) * c.n_pages * c.H;
+    p.tensor = dtype == KVB_BF16 && c.d >= 64 && most > MMA_ROWS && c.n_pages > 0 && all_blocks < 2147483648.0;  // (blocks are TMA coordinates)
+    p.rows = p.tensor ? TENSOR_ROWS : dtype == KVB_F32 ? (most <= 4 ? 4 : 8) : most <= 8 ? 8 : most <= 16 ? 16 : 32;
     const double blocks = static_cast<double>((most + p.rows - 1) / p.rows);
     const double units = blocks * c.n_layers * q.n_seq * c.H;
     p.tiles = units * ((max_kv + TILE - 1) / TILE);
@@ -914,7 +799,7 @@ AttnPlan plan_attention(const Pages& c, const Seqs& q, kvb_dtype dtype, int g, i
     p.row_blocks = static_cast<int>(blocks);
     p.units = static_cast<int64_t>(units);
     const int64_t shares = (max_kv + TILE - 1) / TILE;  // steps of a unit, by a CTA
-    if (p.units <= num_sms && shares <= FEW_SHARES * 16) {
+    if (!p.tensor && p.units <= num_sms && shares <= FEW_SHARES * 16) {
         int most_of[5] = {};
         p.cluster = 1;
         pick(dtype, c.d, p, nullptr, nullptr, most_of);
@@ -926,7 +811,7 @@ AttnPlan plan_attention(const Pages& c, const Seqs& q, kvb_dtype dtype, int g, i
         p.cluster = 0;
     }
     int fit = 1;
-    pick(dtype, c.d, p, nullptr, nullptr, &fit);
+    if (!p.tensor) pick(dtype, c.d, p, nullptr, nullptr, &fit);
     // the CTAs that fit the GPU, no more than the keys give the least share to
     p.min_tiles = MIN_TILES;
     const double need = (p.tiles + p.min_tiles - 1) / p.min_tiles;

@@ -386,8 +386,25 @@ def test_several_tokens_are_causal(kvb, d, g, n, dtype):
     check_attention(P, q, offsets(n), lens - n, out, lse)
 
 
+@pytest.mark.parametrize("d,page,H,g,n,lens", [(128, 16, 2, 8, 3, [3, 70, 64, 129]), (128, 32, 1, 5, 5, [5, 63, 200, 1000]),
+                                               (128, 128, 3, 8, 5, [500, 5, 128, 127]), (64, 16, 2, 20, 1, [1, 16, 17, 300]),
+                                               (64, 64, 2, 4, 33, [33, 40, 400, 64]), (64, 128, 1, 17, 8, [8, 130, 640, 9]),
+                                               (128, 64, 1, 128, 1, [1, 65, 2000, 64]), (128, 64, 2, 3, 100, [100, 101, 1000, 333])])
+@pytest.mark.parametrize("layout", ["head", "token", "spaced"])
+def test_many_rows(kvb, d, page, H, g, n, lens, layout):
+    lens = np.asarray(lens)
+    P = Pool(kvb, 2, H, d, page, 4, int(lens.max()), BF, seed=d + g)
+    P.fill(lens)
+    q = P.rows(2, H * g, 4 * n, layout, 1.5)
+    out, lse = attend(P, q, offsets([n] * 4), lens - n, layout=layout)
+    kvb.kvb_ctx_check(P.ctx)
+    check_attention(P, q, offsets([n] * 4), lens - n, out, lse)
+    again, z = attend(P, q, offsets([n] * 4), lens - n, layout=layout)
+    assert torch.equal(out, again) and torch.equal(lse, z)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
-@pytest.mark.parametrize("d,g,n", [(128, 8, 1), (64, 4, 1), (128, 4, 4), (32, 3, 9)])
+@pytest.mark.parametrize("d,g,n", [(128, 8, 1), (64, 4, 1), (128, 4, 4), (32, 3, 9), (64, 8, 8), (128, 8, 5)])
 def test_long_cache_split_over_ctas_joins_and_repeats_bit_for_bit(kvb, d, g, n, dtype):
     P = Pool(kvb, 1, 1, d, 64, 3, 9000, dtype, seed=5)
     lens = np.asarray([9000, 4097, 8191])
@@ -402,11 +419,11 @@ def test_long_cache_split_over_ctas_joins_and_repeats_bit_for_bit(kvb, d, g, n, 
     kvb.kvb_ctx_check(P.ctx)
 
 
-@pytest.mark.parametrize("dtype", [BF, F32])
-def test_rows_that_see_nothing_and_cache_lengths(kvb, dtype):
+@pytest.mark.parametrize("dtype,g", [(BF, 3), (F32, 3), (BF, 10)])
+def test_rows_that_see_nothing_and_cache_lengths(kvb, dtype, g):
     P = Pool(kvb, 1, 2, 64, 32, 5, 100, dtype)
     P.fill([100] * 5)
-    q = P.rows(1, 6, 10)
+    q = P.rows(1, 2 * g, 10)
     off, pos = offsets([2] * 5), np.array([-1, 50, 50, -2, 98])
     for lens in ([100, 0, 20, 100, 100], [0, 0, 0, 0, 0], [1, 51, 52, 1, -3]):
         out, lse = attend(P, q, off, pos, kv_len=i32(lens))
@@ -427,9 +444,9 @@ def test_rows_of_tokens_that_no_sequence_owns_are_left_alone(kvb):
     assert np.abs(to_host64(out[:, :, 2:5]) - o).max() < 0.05
 
 
-@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("dtype,copies", [(BF, 1), (F32, 1), (BF, 10)])
 @pytest.mark.parametrize("sign", [1, -1])
-def test_scores_that_rise_and_fall_over_the_tiles(kvb, sign, dtype):
+def test_scores_that_rise_and_fall_over_the_tiles(kvb, sign, dtype, copies):
     # the reference is raised at every step, or never again after the first
     d, n = 64, 700
     P = Pool(kvb, 1, 1, d, 16, 1, n, dtype)
@@ -440,8 +457,8 @@ def test_scores_that_rise_and_fall_over_the_tiles(kvb, sign, dtype):
     kvb.kvb_paged_append(P.ctx, P.cache, P.seqs([0, n], [0]), dk, dv, rotate=False)
     for kv, x in enumerate((dk, dv)):
         P.ref.append(kv, to_host64(x), P.table, [0, n], [0])
-    q = np.zeros((1, 3, 1, d))
-    q[0, :, 0, 0] = [8.0, -8.0, 400.0]
+    q = np.zeros((1, 3 * copies, 1, d))
+    q[0, :, 0, 0] = [8.0, -8.0, 400.0] * copies
     q = laid_out(q, "head", dtype)
     out, lse = attend(P, q, [0, 1], [n - 1])
     check_attention(P, q, [0, 1], [n - 1], out, lse)
@@ -477,47 +494,47 @@ def test_scale_layers_and_no_lse(kvb):
     check_attention(P, q, [0, 1, 2], [149, 76], out, None, l_begin=1, scale=0.3)
 
 
-@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("dtype,g", [(BF, 8), (F32, 8), (BF, 40)])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
-def test_a_query_that_is_not_finite_stays_in_its_row(kvb, bad, dtype):
+def test_a_query_that_is_not_finite_stays_in_its_row(kvb, bad, dtype, g):
     P = Pool(kvb, 1, 1, 128, 64, 2, 300, dtype)
     P.fill([300, 300])
-    q = P.rows(1, 8, 2)
+    q = P.rows(1, g, 2)
     good, z = attend(P, q, [0, 1, 2], [299, 299])
     q2 = q.clone()
     q2[0, 3, 1, 5] = bad
     out, lse = attend(P, q2, [0, 1, 2], [299, 299])
-    keep = torch.ones(8, 2, dtype=torch.bool, device="cuda")
+    keep = torch.ones(g, 2, dtype=torch.bool, device="cuda")
     keep[3, 1] = False
     assert torch.equal(out[0][keep], good[0][keep]) and torch.equal(lse[0][keep], z[0][keep])
     assert torch.isnan(out[0, 3, 1]).any() or torch.isinf(lse[0, 3, 1])
 
 
-@pytest.mark.parametrize("dtype", [BF, F32])
-def test_a_bad_page_is_absent_and_reported(kvb, dtype):
+@pytest.mark.parametrize("dtype,g", [(BF, 4), (F32, 4), (BF, 20)])
+def test_a_bad_page_is_absent_and_reported(kvb, dtype, g):
     P = Pool(kvb, 1, 2, 64, 16, 3, 200, dtype)
     P.fill([200, 200, 200])
-    q = P.rows(1, 8, 3)
+    q = P.rows(1, 2 * g, 3)
     off, pos = [0, 1, 2, 3], [199, 199, 199]
     good, _ = attend(P, q, off, pos)
     for wrong in (P.n_pages, -1, 2 ** 31 - 1):
         tab = P.dtab.clone()
         tab[1] = wrong
         tab[2, 3:7] = wrong
-        out, lse = torch.empty_like(q), torch.empty(1, 8, 3, device="cuda")
+        out, lse = torch.empty_like(q), torch.empty(1, 2 * g, 3, device="cuda")
         kvb.kvb_paged_attention(P.ctx, P.cache, kvb.Seqs(tab, i32(off), i32(pos), max_tokens=1), q, out, lse)
         assert status_of(kvb, lambda: kvb.kvb_ctx_check(P.ctx)) == INVALID_ARG
         assert torch.equal(out[:, :, 0], good[:, :, 0])
         assert torch.all(out[:, :, 1] == 0) and torch.all(lse[:, :, 1] == -float("inf"))
         keys = np.r_[0:48, 112:200]  # sequence 2 without its pages 3 .. 6
-        for h in range(8):
-            k, v = (P.ref.sequence(x, P.table[2], 200, 0, h // 4)[keys] for x in (0, 1))
+        for h in range(2 * g):
+            k, v = (P.ref.sequence(x, P.table[2], 200, 0, h // g)[keys] for x in (0, 1))
             s = to_host64(q)[0, h, 2] @ k.T / 8
             w = np.exp(s - s.max())
             assert np.abs(to_host64(out)[0, h, 2] - (w / w.sum()) @ v).max() < (2.0 ** -6 if dtype == BF else 2.0 ** -17)
     kvb.kvb_ctx_check(P.ctx)
     # sequences outside the call
-    out, lse = torch.empty_like(q), torch.empty(1, 8, 3, device="cuda")
+    out, lse = torch.empty_like(q), torch.empty(1, 2 * g, 3, device="cuda")
     for off, pos, kw in (([0, 5, 4, 4], [0, 0, 0], {}), ([0, 0, 0, 9], [0, 0, 0], {}), ([-1, 0, 0, 0], [0, 0, 0], {}),
                          ([0, 1, 2, 3], [0, 0, 2 ** 31 - 1], {}), ([0, 1, 2, 3], [199, 199, 199], {"max_kv": 150})):
         kvb.kvb_paged_attention(P.ctx, P.cache, kvb.Seqs(P.dtab, i32(off), i32(pos), max_tokens=1, **kw), q, out, lse)
