@@ -67,7 +67,6 @@ struct AttnPlan {
 };
 AttnPlan plan_attention(const Pages& c, const Seqs& q, kvb_dtype dtype, int g, int num_sms);
 cudaError_t launch_attention(const AttnParams& P, kvb_dtype dtype, const AttnPlan& p, cudaStream_t s);
-constexpr int TENSOR_ROWS = 128;  // of a unit in the tcgen05 kernel
 cudaError_t launch_attention_rows(const AttnParams& P, const AttnPlan& p, cudaStream_t s, std::string* why);  // bf16, d 64 and 128
 
 }  // namespace paged

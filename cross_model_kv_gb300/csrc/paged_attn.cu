@@ -783,6 +783,13 @@ cudaError_t pick(kvb_dtype dtype, int d, const AttnPlan& p, const AttnParams* P,
     return dtype == KVB_BF16 ? instance_dim<__nv_bfloat16>(d, p, P, s, fit) : instance_dim<float>(d, p, P, s, fit);
 }
 
+// CTAs, at most `most`: where units of one length leave no CTA with parts of two, and not too few CTAs
+// with the others' keys too, that many.
+int even_share(int64_t units, int most) {
+    const int64_t n = units <= most ? units * (most / units) : (units + (units + most - 1) / most - 1) / ((units + most - 1) / most);
+    return n * 4 >= most * 3 ? static_cast<int>(n) : most;
+}
+
 }  // namespace
 
 AttnPlan plan_attention(const Pages& c, const Seqs& q, kvb_dtype dtype, int g, int num_sms) {
@@ -791,10 +798,12 @@ AttnPlan plan_attention(const Pages& c, const Seqs& q, kvb_dtype dtype, int g, i
     const int64_t max_kv = q.max_kv > 0 ? q.max_kv : 1;
     const double all_blocks = (static_cast<double>(c.l_begin) + c.n_layers) * c.n_pages * c.H;
     p.tensor = dtype == KVB_BF16 && c.d >= 64 && most > MMA_ROWS && c.n_pages > 0 && all_blocks < 2147483648.0;  // (blocks are TMA coordinates)
-    p.rows = p.tensor ? TENSOR_ROWS : dtype == KVB_F32 ? (most <= 4 ? 4 : 8) : most <= 8 ? 8 : most <= 16 ? 16 : 32;
+    // blocks of up to 64 rows in the tcgen05 kernel, as small as their number allows
+    const int64_t few = (most + 63) / 64, each = few > 0 ? (most + few - 1) / few : 1;
+    p.rows = p.tensor ? (each <= 16 ? 16 : each <= 32 ? 32 : each <= 48 ? 48 : 64) : dtype == KVB_F32 ? (most <= 4 ? 4 : 8) : most <= 8 ? 8 : most <= 16 ? 16 : 32;
     const double blocks = static_cast<double>((most + p.rows - 1) / p.rows);
     const double units = blocks * c.n_layers * q.n_seq * c.H;
-    p.tiles = units * ((max_kv + TILE - 1) / TILE);
+    p.tiles = units * ((max_kv + TILE - 1) / TILE);  // of 64 keys; the tcgen05 kernel's have 128
     if (p.tiles > static_cast<double>(1 << 30)) return p;  // refused
     p.row_blocks = static_cast<int>(blocks);
     p.units = static_cast<int64_t>(units);
@@ -813,9 +822,9 @@ AttnPlan plan_attention(const Pages& c, const Seqs& q, kvb_dtype dtype, int g, i
     int fit = 1;
     if (!p.tensor) pick(dtype, c.d, p, nullptr, nullptr, &fit);
     // the CTAs that fit the GPU, no more than the keys give the least share to
-    p.min_tiles = MIN_TILES;
-    const double need = (p.tiles + p.min_tiles - 1) / p.min_tiles;
-    p.ctas = num_sms * (fit > 0 ? fit : 1);
+    p.min_tiles = p.tensor ? 1 : MIN_TILES;
+    const double need = p.tensor ? units * ((max_kv + 127) / 128) : (p.tiles + p.min_tiles - 1) / p.min_tiles;
+    p.ctas = even_share(p.units, num_sms * (fit > 0 ? fit : 1));
     if (need < p.ctas) p.ctas = static_cast<int>(need) < 1 ? 1 : static_cast<int>(need);
     p.slots = 2 * static_cast<int64_t>(p.ctas);
     p.counter_bytes = (static_cast<size_t>(p.units) * sizeof(int) + 255) / 256 * 256;

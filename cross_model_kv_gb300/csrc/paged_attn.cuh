@@ -34,7 +34,8 @@ struct Joined {
         acc.w = fmaf(w, o.w, acc.w);
     }
     __device__ __forceinline__ float4 output() const {
-        const float f = sum == 0.f ? 0.f : 1.f / sum;
+        if (sum == 0.f) return make_float4(0.f, 0.f, 0.f, 0.f);  // whatever the values that it does not see are
+        const float f = 1.f / sum;
         return make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
     }
     __device__ __forceinline__ float lse() const { return sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.693147180559945f; }
@@ -61,8 +62,8 @@ __device__ __forceinline__ void write_row(const AttnParams& P, int l, RowPlace a
 }
 
 // After a piece of a unit is written: the last CTA of the unit to arrive joins the pieces, in
-// order.  A warp takes a row's references and sum, the weights of all pieces go to shared memory (`buf`,
-// `cap` floats, free), then each thread adds its columns with its loads in flight together.
+// order.  All pieces' statistics go to shared memory (`buf`, `cap` floats, free) and become their weights,
+// then each thread adds its columns, with the loads of each part in flight together.
 // meet(): the NT threads, numbered from 0, meet.
 template <typename T, int D, int ROWS, int NT, class Meet>
 __device__ __forceinline__ void join_pieces(const AttnParams& P, const RowBlock& B, const Pieces& pieces, int64_t unit, int l, int h,
@@ -82,40 +83,69 @@ __device__ __forceinline__ void join_pieces(const AttnParams& P, const RowBlock&
     if (!*s_last) return;
     __threadfence();
     const int n = pieces.n, lane = tid & 31;
-    float2* whole = reinterpret_cast<float2*>(buf);  // [ROWS] reference, sum
-    float* weight = buf + 2 * ROWS;                  // [row][piece]
-    const bool listed = n <= (cap - 2 * ROWS) / ROWS;
+    float2* whole = reinterpret_cast<float2*>(buf);      // [ROWS] reference, sum
+    float2* part = reinterpret_cast<float2*>(buf) + ROWS; // [row][piece] reference (then weight), sum
+    const bool listed = n <= (cap - 2 * ROWS) / (2 * ROWS);
     auto stat = [&](int row, int i) { return __ldcg(P.part_stat + pieces.slot(i) * ROWS + row); };
-    for (int row = tid >> 5; row < B.nrows; row += NT / 32) {
-        float m = LOWEST, sum = 0.f;
-        float2 st[2];  // of 64 pieces; more are read again
-#pragma unroll
-        for (int i = 0; i < 2; ++i) st[i] = lane + 32 * i < n ? stat(row, lane + 32 * i) : make_float2(LOWEST, 0.f);
-        m = fmaxf(st[0].x, st[1].x);
-        for (int i = lane + 64; i < n; i += 32) m = fmaxf(m, stat(row, i).x);
-#pragma unroll
-        for (int x = 1; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-        for (int i = lane, c = 0; i < n; i += 32, ++c) {
-            const float2 y = c == 0 ? st[0] : c == 1 ? st[1] : stat(row, i);
-            const float w = ex2(y.x - m);
-            sum = fmaf(w, y.y, sum);
-            if (listed) weight[row * n + i] = w;
+    if (listed) {
+#pragma unroll 4
+        for (int i = tid; i < B.nrows * n; i += NT) part[i] = stat(i / n, i % n);
+        meet();
+    }
+    if (listed && n <= 8) {  // a thread a row
+        for (int row = tid; row < B.nrows; row += NT) {
+            float2* mine = part + row * n;
+            float m = LOWEST, sum = 0.f;
+            for (int i = 0; i < n; ++i) m = fmaxf(m, mine[i].x);
+            for (int i = 0; i < n; ++i) {
+                const float w = ex2(mine[i].x - m);
+                sum = fmaf(w, mine[i].y, sum);
+                mine[i].x = w;
+            }
+            whole[row] = make_float2(m, sum);
         }
+    } else {  // a warp a row
+        for (int row = tid >> 5; row < B.nrows; row += NT / 32) {
+            auto at = [&](int i) { return listed ? part[row * n + i] : stat(row, i); };
+            float m = LOWEST, sum = 0.f;
+            for (int i = lane; i < n; i += 32) m = fmaxf(m, at(i).x);
 #pragma unroll
-        for (int x = 1; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-        if (lane == 0) whole[row] = make_float2(m, sum);
+            for (int x = 1; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+            for (int i = lane; i < n; i += 32) {
+                const float2 y = at(i);
+                const float w = ex2(y.x - m);
+                sum = fmaf(w, y.y, sum);
+                if (listed) part[row * n + i].x = w;
+            }
+#pragma unroll
+            for (int x = 1; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+            if (lane == 0) whole[row] = make_float2(m, sum);
+        }
     }
     meet();
-    for (int i = tid; i < B.nrows * (D / 4); i += NT) {
-        const int row = i / (D / 4), d4 = i % (D / 4);
-        Joined z;
-        z.m = whole[row].x;
-        z.sum = whole[row].y;
-#pragma unroll 16
-        for (int p = 0; p < n; ++p)
-            z.weigh(listed ? weight[row * n + p] : ex2(stat(row, p).x - z.m),
-                    __ldcg(reinterpret_cast<const float4*>(P.partial + (pieces.slot(p) * ROWS + row) * D) + d4));
-        write_row<T>(P, l, place_of(P, B, h, row), d4, z);
+    constexpr int AT_ONCE = 4;  // items of a thread: one after another their loads took 18000 cycles for 32 rows
+    for (int i0 = tid; i0 < B.nrows * (D / 4); i0 += AT_ONCE * NT) {
+        Joined z[AT_ONCE];
+        int row[AT_ONCE], d4[AT_ONCE];
+#pragma unroll
+        for (int x = 0; x < AT_ONCE; ++x) {
+            const int i = min(i0 + x * NT, B.nrows * (D / 4) - 1);
+            row[x] = i / (D / 4);
+            d4[x] = i % (D / 4);
+            z[x].m = whole[row[x]].x;
+            z[x].sum = whole[row[x]].y;
+        }
+#pragma unroll 4
+        for (int p = 0; p < n; ++p) {
+            const int64_t from = pieces.slot(p) * ROWS;
+#pragma unroll
+            for (int x = 0; x < AT_ONCE; ++x)
+                z[x].weigh(listed ? part[row[x] * n + p].x : ex2(stat(row[x], p).x - z[x].m),
+                           __ldcg(reinterpret_cast<const float4*>(P.partial + (from + row[x]) * D) + d4[x]));
+        }
+#pragma unroll
+        for (int x = 0; x < AT_ONCE; ++x)
+            if (i0 + x * NT < B.nrows * (D / 4)) write_row<T>(P, l, place_of(P, B, h, row[x]), d4[x], z[x]);
     }
 }
 

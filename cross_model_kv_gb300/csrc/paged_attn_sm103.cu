@@ -1,20 +1,29 @@
 // Attention over the paged cache on the 5th-generation tensor cores: more query rows than
 // mma.sync keeps up with (drafted tokens being checked), bf16, head_dim 64 and 128.
 //
-// The mathematics and the references are those of paged_attn.cu.  One CTA an SM takes up to 128 rows
-// of a unit (layer, sequence, row block, head) and walks its keys 64 at a time; the 64-key tiles
-// of all units form one line that the CTAs share evenly.
-//   warps 0..3  softmax, a row a thread: scores from TMEM to registers, P over them as a bf16
-//               pair (16 bits of a weight), the sum in fp32; O is rescaled in TMEM on the rare raise.
-//               They load the rows, write the outputs and join the pieces of shared units;
-//   warp 4      page numbers, and TMA loads of K and V into a ring of tiles, 128-byte swizzle, key
+// The mathematics and the references are those of paged_attn.cu.  A CTA an SM takes NR (up to 64)
+// rows of a unit (layer, sequence, row block, head) and walks its keys 128 at a time; the 128-key
+// tiles of all units form one line that the CTAs share evenly.  The keys are the M rows of the
+// products and the query rows N, so that few rows cost little:
+//   S^T = K Q^T     M = 128 keys, N = NR rows;
+//   O^T += V^T P^T  M = the dims, K = 128 keys, N = NR rows twice: P as a bf16 pair (hi, lo), the two
+//                   parts' outputs side by side, added at the end.
+// (Query rows as M, 128 of them whatever their number, 64 keys a tile: 122 us for 16 sequences of
+// 8192 keys, 8 heads, 32 rows each, 1860 cycles a tile, of which HBM takes 1400; the products' warps
+// took 900 to 1000 cycles to issue eight of 128 x 64 x 16 or 128 x 128 x 16.)
+//   warps 0..3  softmax, a key a thread: scores from TMEM to registers, the weights of its key to
+//               shared memory, every row's sum in registers until the piece ends.  No thread knows a row's
+//               maximum: they vote whether some score passes its reference by 2^8, and only then reduce,
+//               and rescale O in TMEM.  They load the rows, write the outputs and join the pieces of
+//               shared units;
+//   warp 4      page numbers, and TMA loads of K and V into rings of tiles, 128-byte swizzle, key
 //               rows: K-major for S, MN-major for O, as they lie in the pages;
-//   warp 5      one lane issues S = Q K^T;
-//   warp 6      and O += P V, the high parts and the low ones (P from TMEM).
-// TMEM: score buffer b at 64 b, O at 128.  P takes its scores' columns.
-// HBM bounds it (128 rows a key are 128 flop/byte, the machine has 280); a warp of the softmax whose rows
-// do not exist only passes the barriers.  Every role finds the CTA's pieces by itself, so that
-// the ring is filled (4 us of loads) while the softmax goes from one unit to the next.
+//   warp 5      one lane issues S^T = K Q^T;
+//   warp 6      and O^T += V^T P^T.
+// At head_dim 64 O^T has 64 rows and M is 128 all the same: the upper 64 are the lower ones again.
+// TMEM: score buffer b at 64 b, O's high part at 128, its low part NR columns on.
+// HBM bounds it.  Every role finds the CTA's pieces by itself, so that the rings are filled while the
+// softmax goes from one unit to the next.
 // Every wait is bounded; after one gives up, the softmax still arrives at the units that it shares,
 // so that their counters are left as the next call needs them, the loads and products that
 // were issued are waited for, and TMEM is freed.
@@ -26,20 +35,23 @@ namespace paged {
 
 namespace {
 
-constexpr int TR = TENSOR_ROWS;  // rows of a unit, TMEM lanes
-constexpr int TK = 64;           // keys of a tile
+constexpr int TK = 128;          // keys of a tile, TMEM lanes
 constexpr int SOFT = 128;        // threads of the softmax
 constexpr int NUM_THREADS = SOFT + 96;
 constexpr int GROUPS = TK / 16;  // 16 keys lie in one page
+constexpr int ATOM = TK * 128;   // 64 dims of a tile's keys, or 64 rows' weights of them
 constexpr uint32_t TM_S = 0, TM_O = 128, TM_COLUMNS = 256;
 constexpr uint64_t DRAIN_NS = 200ull * 1000 * 1000;
+constexpr uint32_t IDESC_A_MN = 1u << 15;  // A operand MN-major
 
-template <int HD>
+template <int HD, int NR>
 struct Layout {
-    static constexpr int Q_HALF = TR * 128, Q = HD / 64 * Q_HALF;      // 64 dims of all rows
-    static constexpr int HALF = TK * 128, TILE = HD / 64 * HALF;       // of K, and of V
-    static constexpr int STAGES = HD == 128 ? 5 : 8;
-    static constexpr int BYTES = 1024 + Q + STAGES * 2 * TILE + 2048;
+    static constexpr int Q_HALF = NR * 128, Q = HD / 64 * Q_HALF;  // 64 dims of all rows
+    static constexpr int TILE = HD / 64 * ATOM;                    // of K, and of V
+    static constexpr int STAGES = HD == 128 ? 2 : 4;
+    static constexpr int WEIGHTS = (2 * NR + 63) / 64 * ATOM;      // a buffer of two
+    static constexpr int BYTES = 1024 + (Q + 1023) / 1024 * 1024 + STAGES * 2 * TILE + 2 * WEIGHTS + 4096;
+    static_assert(BYTES <= 227 * 1024, "layout");
 };
 
 // A piece of a unit.
@@ -53,13 +65,14 @@ struct Segment {
 };
 
 // The CTA's place in the line of tiles.
+template <int NR>
 struct Walk {
     int at, stop, share, l, e, h, first;
     RowBlock B;
     int tiles;  // of unit (l, e, h); 0 before the first
 
     __device__ __forceinline__ RowBlock entry(const AttnParams& P) const {
-        return c8::row_block(P, e / P.row_blocks, e % P.row_blocks, TR);
+        return c8::row_block(P, e / P.row_blocks, e % P.row_blocks, NR);
     }
     // The next piece, if there is one.
     __device__ __forceinline__ bool next(const AttnParams& P, Segment& g) {
@@ -100,39 +113,59 @@ struct Walk {
 };
 
 struct Smem {
-    uint64_t k_full[8], k_empty[8], v_full[8], v_empty[8];
-    uint64_t s_full[2], p_full[2], pv_done[2], q_full, drain[2];
+    uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
+    uint64_t s_full[2], s_empty[2], p_full[2], pv_done[2], q_full, drain[2];
     uint32_t tmem;
     int abort;
-    uint32_t present[8];  // of a stage: bit of a 16-key group whose page is there
+    // bit of a tile's 16-key group whose page is there; a tile's place is written again 8 tiles later, when
+    // at most four tiles are behind the one that is loaded
+    uint64_t info_full[8];
+    uint32_t present[8];
     int scan[NUM_THREADS / 32];
     LineStart start;
     int last;
-    alignas(16) float join[2 * TR];
+    alignas(16) float ref[64];       // of every row
+    alignas(16) float by[64];        // factors of a raise, sums of a piece
+    alignas(16) float part[4][64];   // of a warp
+    int pos[64];                     // positions of the rows
+    int64_t to[64];                  // element of P.out that their outputs begin at
 };
-static_assert(sizeof(Smem) <= 2048, "layout");
+static_assert(sizeof(Smem) <= 4096, "layout");
 
 struct Maps {
     CUtensorMap kv[2];
 };
 
-template <int HD>
+// The 64-dim halves (or single half) of an operand of 128-byte rows, K-major: step kk of 16 dims.
+template <int HALF>
+__device__ __forceinline__ constexpr uint32_t step_k(int kk) {
+    return ((kk >> 2) * HALF + (kk & 3) * 32) / 16;
+}
+
+__device__ __forceinline__ float warp_max(float x) {  // NaN loses
+    float y;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <int HD, int NR>
 __global__ void __launch_bounds__(NUM_THREADS, 1) rows_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnParams P) {
-    using L = Layout<HD>;
+    using L = Layout<HD, NR>;
     constexpr int STAGES = L::STAGES;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    uint8_t* sQ = smem;
-    uint8_t* sK = sQ + L::Q;
+    uint8_t* sK = smem;
     uint8_t* sV = sK + STAGES * L::TILE;
-    Smem& M = *reinterpret_cast<Smem*>(sV + STAGES * L::TILE);
+    uint8_t* sP = sV + STAGES * L::TILE;  // [2]
+    uint8_t* sQ = sP + 2 * L::WEIGHTS;
+    Smem& M = *reinterpret_cast<Smem*>(sQ + (L::Q + 1023) / 1024 * 1024);
     volatile int* abort_flag = &M.abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const DevErr derr{P.err.word, P.err.timeout_ns};
 
-    Walk W;
+    Walk<NR> W;
     W.tiles = 0;
-    if (!c8::line_start<TR, TK, NUM_THREADS>(P, M.scan, &M.start, W.at, W.stop, W.share, W.l, W.e, W.h, W.first)) return;
+    if (!c8::line_start<NR, TK, NUM_THREADS>(P, M.scan, &M.start, W.at, W.stop, W.share, W.l, W.e, W.h, W.first)) return;
     if (threadIdx.x == 0) {
         for (int i = 0; i < STAGES; ++i) {
             mbar_init(&M.k_full[i], 1);
@@ -142,10 +175,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) rows_kernel(const __grid_const
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&M.s_full[b], 1);
+            mbar_init(&M.s_empty[b], SOFT);
             mbar_init(&M.p_full[b], SOFT);
             mbar_init(&M.pv_done[b], 1);
             mbar_init(&M.drain[b], 1);
         }
+        for (int i = 0; i < 8; ++i) mbar_init(&M.info_full[i], 1);
         mbar_init(&M.q_full, SOFT);
         M.abort = 0;
         fence_mbar_init();
@@ -161,170 +196,220 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) rows_kernel(const __grid_const
     auto wait_all = [&](uint64_t* b, uint32_t parity) {  // warp-uniform outcome
         return __all_sync(0xffffffffu, mbar_wait(b, parity, derr, abort_flag)) != 0;
     };
-    // t counts the tiles of all of the CTA's pieces: stage t % STAGES, score buffer t & 1
+    // t counts the tiles of all of the CTA's pieces: stage t % STAGES, buffers (scores, weights) t & 1
     uint32_t t = 0;
     Segment G;
 
-    if (warp < 4) {
+    if (warp < SOFT / 32) {
         // ------------------------------------------------------- softmax
-        const int row = threadIdx.x;  // of the unit, and TMEM lane
+        const int key = threadIdx.x;  // of the tile, and TMEM lane; the dim of an output
         const uint32_t tl = tmem_base + (static_cast<uint32_t>(32 * warp) << 16);
         const float f = P.scale_log2;
         bool ok = true;
         while (W.next(P, G)) {
             const int ntiles = G.tiles();
-            const bool valid = row < G.B.nrows, active = 32 * warp < G.B.nrows;
-            const RowPlace at = place_of(P, G.B, G.h, valid ? row : 0);
+            named_bar_sync(1, SOFT);  // ref, pos and by are free
+            // the rows: 16-byte chunks c of row r, by all threads
             {
-                const uint4* q = reinterpret_cast<const uint4*>(address<__nv_bfloat16>(P.query, G.l, at));
-                uint4 u[HD / 8];
+                constexpr int MINE = NR * (HD / 8) / SOFT;
+                uint4 u[MINE];
 #pragma unroll
-                for (int c = 0; c < HD / 8; ++c) u[c] = valid ? __ldg(q + c) : make_uint4(0, 0, 0, 0);
+                for (int i = 0; i < MINE; ++i) {
+                    const int r = (i * SOFT + key) / (HD / 8), c = key % (HD / 8);
+                    u[i] = r < G.B.nrows ? __ldg(reinterpret_cast<const uint4*>(address<__nv_bfloat16>(P.query, G.l, place_of(P, G.B, G.h, r))) + c)
+                                         : make_uint4(0, 0, 0, 0);
+                }
 #pragma unroll
-                for (int c = 0; c < HD / 8; ++c)
-                    *reinterpret_cast<uint4*>(sQ + (c >> 3) * L::Q_HALF + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = u[c];
-                fence_proxy_async_smem();
-                mbar_arrive(&M.q_full);
+                for (int i = 0; i < MINE; ++i) {
+                    const int r = (i * SOFT + key) / (HD / 8), c = key % (HD / 8);
+                    *reinterpret_cast<uint4*>(sQ + (c >> 3) * L::Q_HALF + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = u[i];
+                }
             }
-            const int see = valid ? min(G.k1, G.B.pos + (G.B.row0 + row) / P.g + 1) : 0;  // keys below are visible
-            float m = LOWEST, sum = 0.f;
+            if (key < NR) {
+                M.ref[key] = key < G.B.nrows ? LOWEST : 0.f;  // rows that do not exist: weights of 1, never raised
+                M.pos[key] = key < G.B.nrows ? G.B.pos + (G.B.row0 + key) / P.g : INT32_MAX;
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&M.q_full);
+            float sum[NR];
+#pragma unroll
+            for (int n = 0; n < NR; ++n) sum[n] = 0.f;
+            named_bar_sync(1, SOFT);
             for (int i = 0; i < ntiles; ++i, ++t) {
-                const uint32_t b = t & 1, stage = t % STAGES;
-                // V's barrier too: its stage, with what is noted of its pages, is not given away before P is there
-                ok = ok && wait_all(&M.v_full[stage], (t / STAGES) & 1);
-                ok = ok && wait_all(&M.s_full[b], (t >> 1) & 1);
-                if (!ok) break;
-                tc_fence_after();
-                const int j0 = G.k0 + i * TK;
-                const uint32_t present = M.present[stage];
-                const bool ragged = present != (1u << GROUPS) - 1 || j0 + TK > G.k1;  // the same for all
-                if (active) {
-                    const uint32_t cS = tl + TM_S + TK * b;
-                    uint32_t sv[TK];
-                    tmem_ld32(cS, sv);
-                    tmem_ld32(cS + 32, sv + 32);
-                    const int nvis = see - j0;
+                const uint32_t b = t & 1, use = t >> 1, stage = t % STAGES;
+                ok = ok && wait_all(&M.info_full[t % 8], (t / 8) & 1);
+                ok = ok && wait_all(&M.s_full[b], use & 1);
+                const int j = G.k0 + i * TK + key;
+                uint32_t sv[NR];
+                bool above = false, dead = false;
+                if (ok) {
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < NR; c += 16) tmem_ld16(tl + TM_S + 64 * b + c, *reinterpret_cast<uint32_t(*)[16]>(sv + c));
+                    const uint32_t present = M.present[t % 8];
+                    dead = j >= G.k1 || !((present >> (key / 16)) & 1u);  // nothing sees the key
                     tmem_ld_wait();
-                    if (!__all_sync(0xffffffffu, !ragged && nvis >= TK)) {
-#pragma unroll
-                        for (int j = 0; j < TK; ++j)
-                            if (j >= nvis || !((present >> (j / 16)) & 1u)) sv[j] = 0xff800000u;  // -inf
-                    }
-                    float top[4];
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const uint32_t* v = sv + 16 * x;
-                        float y[5];
-#pragma unroll
-                        for (int j = 0; j < 5; ++j)
-                            y[j] = max3(__uint_as_float(v[3 * j]), __uint_as_float(v[3 * j + 1]), __uint_as_float(v[3 * j + 2]));
-                        top[x] = fmaxf(max3(y[0], y[1], y[2]), max3(y[3], y[4], __uint_as_float(v[15])));
-                    }
-                    const float best = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * f;
-                    const bool raise = best > m + MARGIN;
-                    if (__any_sync(0xffffffffu, raise)) {
-                        float lower = 1.f;
-                        if (raise) {
-                            lower = ex2(m - best);
-                            sum *= lower;
-                            m = best;
-                        }
-                        __syncwarp();
-                        if (i > 0) {  // O is complete up to the tile before
-                            ok = wait_all(&M.pv_done[b ^ 1], ((t - 1) >> 1) & 1);
-                            if (ok) {
-                                tc_fence_after();
-#pragma unroll 1
-                                for (int c0 = 0; c0 < HD; c0 += 16) {
-                                    uint32_t o[16];
-                                    tmem_ld16(tl + TM_O + c0, o);
-                                    tmem_ld_wait();
-#pragma unroll
-                                    for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * lower);
-                                    tmem_st16(tl + TM_O + c0, o);
-                                }
-                                tmem_st_wait();
-                            }
-                        }
-                    }
-                    // the weights, 32 keys at a time: high parts to columns 0 .. 31 of the buffer, low ones to 32 .. 63
-                    const float2 f2 = make_float2(f, f), m2 = make_float2(-m, -m);
-                    float2 part = make_float2(0.f, 0.f);
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        uint32_t hi[16], lo[16];
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            float2 w = fma2(make_float2(__uint_as_float(sv[32 * x + 2 * j]), __uint_as_float(sv[32 * x + 2 * j + 1])), f2, m2);
-                            w = make_float2(ex2(w.x), ex2(w.y));
-                            part = add2(part, w);
-                            hi[j] = pack_bf16x2(w.x, w.y);
-                            lo[j] = pack_bf16x2(w.x - __uint_as_float(hi[j] << 16), w.y - __uint_as_float(hi[j] & 0xffff0000u));
-                        }
-                        tmem_st16(cS + 16 * x, hi);
-                        tmem_st16(cS + 32 + 16 * x, lo);
-                    }
-                    sum += part.x + part.y;
-                    __syncwarp();
-                    tmem_st_wait();
                     tc_fence_before();
-                }
-                if (ragged) {  // slots that nothing sees may hold anything: their value rows are zeros
-                    for (int y = threadIdx.x; y < L::TILE / 16; y += SOFT) {
-                        const int key = (y >> 3) % TK;
-                        if (j0 + key >= G.k1 || !((present >> (key / 16)) & 1u))
-                            *reinterpret_cast<uint4*>(sV + stage * L::TILE + 16 * y) = make_uint4(0, 0, 0, 0);
+                    mbar_arrive(&M.s_empty[b]);
+                    if (!__all_sync(0xffffffffu, !dead && j <= G.B.pos_lo)) {
+#pragma unroll
+                        for (int n = 0; n < NR; ++n)
+                            if (dead || j > M.pos[n]) sv[n] = 0xff800000u;  // -inf
                     }
-                    fence_proxy_async_smem();
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int n = 0; n < NR; n += 4) {
+                        const float4 r = *reinterpret_cast<const float4*>(M.ref + n);
+                        top = max3(top, fmaf(__uint_as_float(sv[n]), f, -r.x), fmaf(__uint_as_float(sv[n + 1]), f, -r.y));
+                        top = max3(top, fmaf(__uint_as_float(sv[n + 2]), f, -r.z), fmaf(__uint_as_float(sv[n + 3]), f, -r.w));
+                    }
+                    above = top > MARGIN;
                 }
+                if (!named_bar_and(1, SOFT, ok && !above)) {
+                    ok = named_bar_and(1, SOFT, ok);
+                    if (!ok) break;
+                    // some score passes its reference: every row's is raised to the tile's maximum
+#pragma unroll
+                    for (int n = 0; n < NR; ++n) {
+                        const float x = warp_max(__uint_as_float(sv[n]));
+                        if (lane == 0) M.part[warp][n] = x;
+                    }
+                    named_bar_sync(1, SOFT);
+                    if (key < NR) {
+                        const float x = fmaxf(fmaxf(M.part[0][key], M.part[1][key]), fmaxf(M.part[2][key], M.part[3][key]));
+                        const float old = M.ref[key], up = fmaxf(old, x * f);
+                        M.by[key] = ex2(old - up);
+                        M.ref[key] = up;
+                    }
+                    named_bar_sync(1, SOFT);
+#pragma unroll
+                    for (int n = 0; n < NR; ++n) sum[n] *= M.by[n];
+                    if (i > 0) {  // O is complete up to the tile before
+                        ok = wait_all(&M.pv_done[b ^ 1], ((t - 1) >> 1) & 1);
+                        if (ok) {
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int c = 0; c < 2 * NR; c += 16) {
+                                uint32_t o[16];
+                                tmem_ld16(tl + TM_O + c, o);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int n = 0; n < 16; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * M.by[(c + n) % NR]);
+                                tmem_st16(tl + TM_O + c, o);
+                            }
+                            tmem_st_wait();
+                            tc_fence_before();
+                        }
+                    }
+                }
+                // the weights' buffer is free when its products are done
+                if (ok && use > 0) ok = wait_all(&M.pv_done[b], (use - 1) & 1);
+                if (ok && __any_sync(0xffffffffu, dead)) ok = wait_all(&M.v_full[stage], (t / STAGES) & 1);
+                if (!ok) continue;  // to the next vote
+                uint8_t* mine = sP + b * L::WEIGHTS + key * 128;
+#pragma unroll
+                for (int c = 0; c < NR / 8; ++c) {
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        const int r = 8 * c + 2 * n;
+                        const float2 ref = *reinterpret_cast<const float2*>(M.ref + r);
+                        const float2 w = make_float2(ex2(fmaf(__uint_as_float(sv[r]), f, -ref.x)), ex2(fmaf(__uint_as_float(sv[r + 1]), f, -ref.y)));
+                        sum[r] += w.x;
+                        sum[r + 1] += w.y;
+                        hi[n] = pack_bf16x2(w.x, w.y);
+                        lo[n] = pack_bf16x2(w.x - __uint_as_float(hi[n] << 16), w.y - __uint_as_float(hi[n] & 0xffff0000u));
+                    }
+                    constexpr int LO = NR / 8;
+                    *reinterpret_cast<uint4*>(mine + (c >> 3) * ATOM + (((c & 7) ^ (key & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4*>(mine + ((LO + c) >> 3) * ATOM + ((((LO + c) & 7) ^ (key & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+                if (dead) {  // slots that nothing sees may hold anything: their value rows are zeros
+                    uint8_t* row = sV + stage * L::TILE + key * 128;
+#pragma unroll
+                    for (int c = 0; c < HD / 8; ++c) *reinterpret_cast<uint4*>(row + (c >> 3) * ATOM + 16 * (c & 7)) = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
                 mbar_arrive(&M.p_full[b]);
             }
             if (ok && ntiles > 0) ok = wait_all(&M.pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1);
-            const bool have = ok && ntiles > 0 && active;
+            const bool have = ok && ntiles > 0;
             if (have) tc_fence_after();
-            const int64_t part0 = G.slot * TR + row;
-            const float by = sum == 0.f ? 0.f : 1.f / sum;
-            const int64_t lse_row = (static_cast<int64_t>(G.l) * P.c.H * P.g + at.head) * P.q.T + at.token;
-            const bool write = valid && KVB_IN_BOUNDS(P.err, lse_row, 1, c8::rows_of(P));
-            if (active) {
+            // the rows' sums, and where their outputs go
+#pragma unroll
+            for (int n0 = 0; n0 < NR; n0 += 16) {  // 16 rows: a lane keeps half of them at each exchange
+                float x[16];
+#pragma unroll
+                for (int n = 0; n < 16; ++n) x[n] = sum[n0 + n];
+#pragma unroll
+                for (int z = 8; z > 0; z >>= 1)
+#pragma unroll
+                    for (int n = 0; n < z; ++n) {
+                        const float keep = lane & z ? x[n + z] : x[n], give = lane & z ? x[n] : x[n + z];
+                        x[n] = keep + __shfl_xor_sync(0xffffffffu, give, z);
+                    }
+                x[0] += __shfl_xor_sync(0xffffffffu, x[0], 16);
+                if (lane < 16) M.part[warp][n0 + lane] = x[0];
+            }
+            named_bar_sync(1, SOFT);
+            const bool alone = G.pieces.n == 1;
+            const int64_t part0 = G.slot * NR;
+            if (key < NR && key >= G.B.nrows) M.to[key] = -1;
+            if (key < G.B.nrows) {
+                const float total = have ? (M.part[0][key] + M.part[1][key]) + (M.part[2][key] + M.part[3][key]) : 0.f, m = M.ref[key];
+                const RowPlace at = place_of(P, G.B, G.h, key);
+                const int64_t lse_row = (static_cast<int64_t>(G.l) * P.c.H * P.g + at.head) * P.q.T + at.token;
+                const bool inside = KVB_IN_BOUNDS(P.err, lse_row, 1, c8::rows_of(P)) && KVB_IN_BOUNDS(P.err, G.slot, 1, P.slots);
+                M.by[key] = total == 0.f ? 0.f : 1.f / total;
+                M.to[key] = inside ? G.l * P.out.l + at.head * P.out.h + at.token * P.out.t : -1;
+                if (inside && !alone) P.part_stat[part0 + key] = make_float2(m, total);
+                if (inside && alone && P.lse) P.lse[lse_row] = total == 0.f ? -INFINITY : (m + log2f(total)) * 0.693147180559945f;
+            }
+            named_bar_sync(1, SOFT);
+            if (key < HD && (alone || KVB_IN_BOUNDS(P.err, G.slot, 1, P.slots))) {  // whole warps; lane = dim
 #pragma unroll 1
-                for (int c0 = 0; c0 < HD; c0 += 16) {
-                    uint32_t o[16];
+                for (int c = 0; c < G.B.nrows; c += 16) {
+                    uint32_t hi[16], lo[16];
                     if (have) {
-                        tmem_ld16(tl + TM_O + c0, o);
+                        tmem_ld16(tl + TM_O + c, hi);
+                        tmem_ld16(tl + TM_O + NR + c, lo);
                         tmem_ld_wait();
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) o[j] = 0u;
+                        for (int n = 0; n < 16; ++n) hi[n] = lo[n] = 0u;
                     }
-                    if (write && G.pieces.n == 1) {
-                        uint32_t w[8];
+                    float o[16];
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) w[j] = pack_bf16x2(__uint_as_float(o[2 * j]) * by, __uint_as_float(o[2 * j + 1]) * by);
-                        uint4* dst = reinterpret_cast<uint4*>(address<__nv_bfloat16>(P.out, G.l, at) + c0);
-                        dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                        dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-                    } else if (write && KVB_IN_BOUNDS(P.err, part0, 1, P.slots * TR)) {
-                        uint4* dst = reinterpret_cast<uint4*>(P.partial + part0 * HD + c0);
+                    for (int n = 0; n < 16; ++n) o[n] = __uint_as_float(hi[n]) + __uint_as_float(lo[n]);
+                    if (alone) {
+                        int64_t to[16];
+                        float by[16];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) dst[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                        for (int n = 0; n < 16; ++n) {
+                            to[n] = M.to[c + n];
+                            by[n] = M.by[c + n];
+                        }
+#pragma unroll
+                        for (int n = 0; n < 16; ++n)
+                            if (to[n] >= 0) static_cast<__nv_bfloat16*>(P.out.data)[to[n] + key] = __float2bfloat16_rn(by[n] == 0.f ? 0.f : o[n] * by[n]);
+                    } else {
+                        float* to = P.partial + (part0 + c) * HD + key;
+#pragma unroll
+                        for (int n = 0; n < 16; ++n)
+                            if (c + n < G.B.nrows) to[n * HD] = o[n];
                     }
                     __syncwarp();
                 }
-                if (write && G.pieces.n == 1) {
-                    if (P.lse) P.lse[lse_row] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.693147180559945f;
-                } else if (write && KVB_IN_BOUNDS(P.err, part0, 1, P.slots * TR)) {
-                    P.part_stat[part0] = make_float2(m, sum);
-                }
-                tc_fence_before();
             }
-            if (G.pieces.n > 1)
-                join_pieces<__nv_bfloat16, HD, TR, SOFT>(P, G.B, G.pieces, G.unit, G.l, G.h, &M.last, M.join, 2 * TR,
+            tc_fence_before();
+            if (!alone)
+                join_pieces<__nv_bfloat16, HD, NR, SOFT>(P, G.B, G.pieces, G.unit, G.l, G.h, &M.last, reinterpret_cast<float*>(sP), 2 * L::WEIGHTS / 4,
                                                          [] { named_bar_sync(1, SOFT); });
         }
-    } else if (warp == 4) {
+    } else if (warp == SOFT / 32) {
         // ------------------------------------------------------- pages and loads
-        const int rows = min(P.c.page, TK), per = TK / rows;  // keys of a load; loads of a tile
+        constexpr int HALVES = HD / 64;
+        const int rows = min(P.c.page, TK), per = TK / rows;  // keys of a load; loads of a tile, of 64 dims
         bool go = true;
         while (go && W.next(P, G)) {
             const int ntiles = G.tiles();
@@ -352,33 +437,30 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) rows_kernel(const __grid_const
                     now = next;
                     next = page_of(x0 + 32);
                 }
-                int z[GROUPS];  // blocks of the tile's loads, -1: none
-                uint32_t present = 0;
-#pragma unroll
-                for (int x = 0; x < GROUPS; ++x) {
-                    const int pid = __shfl_sync(0xffffffffu, now, (x0 + x) & 31);
-                    z[x] = x < per && pid >= 0 ? static_cast<int>(block0 + static_cast<int64_t>(pid) * P.c.H) : -1;
-                    if (z[x] >= 0) present |= ((1u << (rows / 16)) - 1) << (x * (rows / 16));
-                }
+                // lane x * HALVES + hf issues load x of 64 dims: one lane after another took 1300 cycles for K,
+                // the whole of a tile's loads 2600 of the 2700 that HBM takes for it
+                const int x = lane / HALVES, hf = lane % HALVES;
+                const int pid = __shfl_sync(0xffffffffu, now, (x0 + x) & 31), group_pid = __shfl_sync(0xffffffffu, now, (x0 + lane * 16 / rows) & 31);
+                const uint32_t present = __ballot_sync(0xffffffffu, lane < GROUPS && group_pid >= 0);
+                const bool mine = x < per && pid >= 0;
+                const int z = static_cast<int>(block0 + static_cast<int64_t>(max(pid, 0)) * P.c.H), y = (G.k0 + (x0 + x) * rows) & (P.c.page - 1);
                 const uint32_t bytes = static_cast<uint32_t>(__popc(present)) * 16 * HD * 2;
+                if (elect_one()) {
+                    M.present[t % 8] = present;
+                    mbar_arrive(&M.info_full[t % 8]);
+                }
+                __syncwarp();
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
                     uint64_t* full = kv ? &M.v_full[stage] : &M.k_full[stage];
                     if (go) go = wait_all(kv ? &M.v_empty[stage] : &M.k_empty[stage], (round & 1) ^ 1);
                     if (!go) break;
-                    if (lane == 0) {
-                        if (kv) M.present[stage] = present;
+                    if (elect_one()) {
                         if (bytes) mbar_arrive_expect_tx(full, bytes);
                         else mbar_arrive(full);
-                        uint8_t* tile = (kv ? sV : sK) + stage * L::TILE;
-#pragma unroll
-                        for (int x = 0; x < GROUPS; ++x)
-                            if (z[x] >= 0)
-#pragma unroll
-                                for (int hf = 0; hf < HD / 64; ++hf)
-                                    tma_load_3d(tile + hf * L::HALF + x * rows * 128, &maps.kv[kv], full, 64 * hf,
-                                                (G.k0 + (x0 + x) * rows) & (P.c.page - 1), z[x]);
                     }
+                    __syncwarp();
+                    if (mine) tma_load_3d((kv ? sV : sK) + stage * L::TILE + hf * ATOM + x * rows * 128, &maps.kv[kv], full, 64 * hf, y, z);
                     __syncwarp();
                 }
                 if (!go) break;
@@ -393,10 +475,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) rows_kernel(const __grid_const
         }
     } else {
         // ------------------------------------------------------- products
-        const bool scores = warp == 5;
+        const bool scores = warp == SOFT / 32 + 1;
         bool go = true;
-        const uint64_t q0 = sdesc_k_sw128(smem_u32(sQ)), k0 = sdesc_k_sw128(smem_u32(sK));
-        const uint64_t v0 = sdesc_mn_sw128(smem_u32(sV), L::HALF);
+        const uint64_t k0 = sdesc_k_sw128(smem_u32(sK)), q0 = sdesc_k_sw128(smem_u32(sQ));
+        const uint64_t v0 = sdesc_mn_sw128(smem_u32(sV), HD == 128 ? ATOM : 0), p0 = sdesc_mn_sw128(smem_u32(sP), ATOM);
         for (int n = 0; go && W.next(P, G); ++n) {
             const int ntiles = G.tiles();
             if (scores && ntiles > 0) {
@@ -409,36 +491,32 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) rows_kernel(const __grid_const
                 go = go && wait_all(&M.q_full, n & 1);
             }
             for (int i = 0; go && i < ntiles; ++i, ++t) {
-                const uint32_t b = t & 1, stage = t % STAGES, parity = (t / STAGES) & 1;
-                const uint32_t cS = tmem_base + TM_S + TK * b;
+                const uint32_t b = t & 1, use = t >> 1, stage = t % STAGES, parity = (t / STAGES) & 1;
                 if (scores) {
-                    constexpr uint32_t idesc = idesc_bf16_f32(TR, TK);
+                    constexpr uint32_t idesc = idesc_bf16_f32(TK, NR);
                     go = wait_all(&M.k_full[stage], parity);
-                    if (go && t >= 2) go = wait_all(&M.pv_done[b], ((t >> 1) - 1) & 1);  // P lies where these scores go
+                    if (go && use > 0) go = wait_all(&M.s_empty[b], (use - 1) & 1);
                     if (!go) break;
                     tc_fence_after();
-                    const uint64_t k = k0 + stage * L::TILE / 16;
+                    const uint64_t k = k0 + stage * (L::TILE / 16);
                     if (elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < HD / 16; ++kk)
-                            umma_bf16(cS, q0 + ((kk >> 2) * L::Q_HALF + (kk & 3) * 32) / 16, k + ((kk >> 2) * L::HALF + (kk & 3) * 32) / 16,
-                                      idesc, kk != 0);
+                            umma_bf16(tmem_base + TM_S + 64 * b, k + step_k<ATOM>(kk), q0 + step_k<L::Q_HALF>(kk), idesc, kk != 0);
                         umma_commit(&M.s_full[b]);
                         umma_commit(&M.k_empty[stage]);
                     }
                 } else {
-                    constexpr uint32_t idesc = idesc_bf16_f32(TR, HD) | IDESC_B_MN;
+                    constexpr uint32_t idesc = idesc_bf16_f32(TK, 2 * NR) | IDESC_A_MN | IDESC_B_MN;
                     go = wait_all(&M.v_full[stage], parity);
-                    go = go && wait_all(&M.p_full[b], (t >> 1) & 1);
+                    go = go && wait_all(&M.p_full[b], use & 1);
                     if (!go) break;
                     tc_fence_after();
-                    const uint64_t v = v0 + stage * L::TILE / 16;
+                    const uint64_t v = v0 + stage * (L::TILE / 16), p = p0 + b * (L::WEIGHTS / 16);
                     if (elect_one()) {
 #pragma unroll
-                        for (int part = 0; part < 2; ++part)
-#pragma unroll
-                            for (int kk = 0; kk < TK / 16; ++kk)
-                                umma_f16_ts(tmem_base + TM_O, cS + 32u * part + 8u * kk, v + kk * 16 * 128 / 16, idesc, (i | part | kk) != 0);
+                        for (int kk = 0; kk < TK / 16; ++kk)
+                            umma_bf16(tmem_base + TM_O, v + kk * (16 * 128 / 16), p + kk * (16 * 128 / 16), idesc, (i | kk) != 0);
                         umma_commit(&M.v_empty[stage]);
                         umma_commit(&M.pv_done[b]);
                     }
@@ -464,7 +542,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) rows_kernel(const __grid_const
     if (threadIdx.x == 0 && *abort_flag) *reinterpret_cast<volatile int*>(P.err.mirror) = DEV_ERR_TIMEOUT;
 }
 
-template <int HD>
+template <int HD, int NR>
 cudaError_t launch(const AttnParams& P, const AttnPlan& p, cudaStream_t s, std::string* why) {
     EncodeTiledFn enc = get_encode_tiled();
     if (!enc) {
@@ -486,16 +564,22 @@ cudaError_t launch(const AttnParams& P, const AttnPlan& p, cudaStream_t s, std::
             return cudaErrorInvalidValue;
         }
     }
-    cudaError_t e = cudaFuncSetAttribute(rows_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<HD>::BYTES);
+    cudaError_t e = cudaFuncSetAttribute(rows_kernel<HD, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<HD, NR>::BYTES);
     if (e != cudaSuccess) return e;
-    rows_kernel<HD><<<p.ctas, NUM_THREADS, Layout<HD>::BYTES, s>>>(maps, P);
+    rows_kernel<HD, NR><<<p.ctas, NUM_THREADS, Layout<HD, NR>::BYTES, s>>>(maps, P);
     return cudaGetLastError();
+}
+
+template <int HD>
+cudaError_t launch_rows(const AttnParams& P, const AttnPlan& p, cudaStream_t s, std::string* why) {
+    if (p.rows == 16) return launch<HD, 16>(P, p, s, why);
+    return p.rows == 32 ? launch<HD, 32>(P, p, s, why) : p.rows == 48 ? launch<HD, 48>(P, p, s, why) : launch<HD, 64>(P, p, s, why);
 }
 
 }  // namespace
 
 cudaError_t launch_attention_rows(const AttnParams& P, const AttnPlan& p, cudaStream_t s, std::string* why) {
-    return P.c.d == 64 ? launch<64>(P, p, s, why) : launch<128>(P, p, s, why);
+    return P.c.d == 64 ? launch_rows<64>(P, p, s, why) : launch_rows<128>(P, p, s, why);
 }
 
 }  // namespace paged
