@@ -43,16 +43,6 @@ __device__ __forceinline__ Item item_of(const RwParams& P, int64_t idx) {
 
 constexpr int INF_BITS = 0x7f800000;
 
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {  // two products in one instruction
-    float2 d;
-    asm("{\n\t.reg .b64 x, y, w;\n\t"
-        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-        "mul.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-
 // Eight elements as they lie in memory.  top(): the largest magnitude as the bits of
 // an fp32 number (non-negative floats order as their bits, infinities and NaN above
 // all others); get(): the elements as fp32.

@@ -41,19 +41,10 @@ __device__ __forceinline__ int swizzled(int row, int chunk) {
     else return row * CH + (chunk ^ ((row / (8 / CH)) & (CH - 1)));
 }
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
 // 16 zero bytes unless taken (`any`: an address of the buffer, not read)
 __device__ __forceinline__ void copy16_or_zero(uint32_t dst, const void* src, const void* any, bool take) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(take ? src : any), "r"(take ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // Ring of one warp: the K rows of a step and its V rows, in turn, each a part.
 template <typename T, int D>
 struct Ring {
@@ -784,10 +775,12 @@ cudaError_t pick(kvb_dtype dtype, int d, const AttnPlan& p, const AttnParams* P,
 }
 
 // CTAs, at most `most`: where units of one length leave no CTA with parts of two, and not too few CTAs
-// with the others' keys too, that many.
-int even_share(int64_t units, int most) {
+// with the others' keys too, that many.  With 304 CTAs of this file's kernel, 16 x 8192 / 16 x 32768 keys of one length
+// take 86 / 310 us so and 90 / 321 on all of them, unequal ones (16 x 1024 .. 8192) 54 either way.  The tcgen05 kernel
+// has 152 and longer ways from one unit to the next: 128 of them 86 and 152 93 us, but unequal lengths 94 and 78.
+int even_share(int64_t units, int most, bool tensor) {
     const int64_t n = units <= most ? units * (most / units) : (units + (units + most - 1) / most - 1) / ((units + most - 1) / most);
-    return n * 4 >= most * 3 ? static_cast<int>(n) : most;
+    return n * 20 >= most * (tensor ? 18 : 15) ? static_cast<int>(n) : most;
 }
 
 }  // namespace
@@ -824,7 +817,7 @@ AttnPlan plan_attention(const Pages& c, const Seqs& q, kvb_dtype dtype, int g, i
     // the CTAs that fit the GPU, no more than the keys give the least share to
     p.min_tiles = p.tensor ? 1 : MIN_TILES;
     const double need = p.tensor ? units * ((max_kv + 127) / 128) : (p.tiles + p.min_tiles - 1) / p.min_tiles;
-    p.ctas = even_share(p.units, num_sms * (fit > 0 ? fit : 1));
+    p.ctas = even_share(p.units, num_sms * (fit > 0 ? fit : 1), p.tensor);
     if (need < p.ctas) p.ctas = static_cast<int>(need) < 1 ? 1 : static_cast<int>(need);
     p.slots = 2 * static_cast<int64_t>(p.ctas);
     p.counter_bytes = (static_cast<size_t>(p.units) * sizeof(int) + 255) / 256 * 256;

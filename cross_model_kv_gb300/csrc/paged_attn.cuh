@@ -83,10 +83,22 @@ __device__ __forceinline__ void join_pieces(const AttnParams& P, const RowBlock&
     if (!*s_last) return;
     __threadfence();
     const int n = pieces.n, lane = tid & 31;
-    float2* whole = reinterpret_cast<float2*>(buf);      // [ROWS] reference, sum
-    float2* part = reinterpret_cast<float2*>(buf) + ROWS; // [row][piece] reference (then weight), sum
-    const bool listed = n <= (cap - 2 * ROWS) / (2 * ROWS);
+    float2* whole = reinterpret_cast<float2*>(buf);              // [ROWS] reference, 1 / sum
+    int64_t* to = reinterpret_cast<int64_t*>(buf + 2 * ROWS);    // [ROWS] element of P.out, or -1
+    float2* part = reinterpret_cast<float2*>(buf + 4 * ROWS);    // [row][piece] reference (then weight / sum), sum
+    const bool listed = n <= (cap - 4 * ROWS) / (2 * ROWS);
     auto stat = [&](int row, int i) { return __ldcg(P.part_stat + pieces.slot(i) * ROWS + row); };
+    // what a row needs once
+    auto finish = [&](int row, float m, float sum) {
+        const RowPlace at = place_of(P, B, h, row);
+        const int64_t r = (static_cast<int64_t>(l) * P.c.H * P.g + at.head) * P.q.T + at.token;
+        const bool inside = KVB_IN_BOUNDS(P.err, r, 1, c8::rows_of(P));
+        to[row] = inside ? l * P.out.l + at.head * P.out.h + at.token * P.out.t : -1;
+        if (inside && P.lse) P.lse[r] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.693147180559945f;
+        const float by = sum == 0.f ? 0.f : 1.f / sum;
+        whole[row] = make_float2(m, by);
+        return by;
+    };
     if (listed) {
 #pragma unroll 4
         for (int i = tid; i < B.nrows * n; i += NT) part[i] = stat(i / n, i % n);
@@ -102,7 +114,8 @@ __device__ __forceinline__ void join_pieces(const AttnParams& P, const RowBlock&
                 sum = fmaf(w, mine[i].y, sum);
                 mine[i].x = w;
             }
-            whole[row] = make_float2(m, sum);
+            const float by = finish(row, m, sum);
+            for (int i = 0; i < n; ++i) mine[i].x *= by;
         }
     } else {  // a warp a row
         for (int row = tid >> 5; row < B.nrows; row += NT / 32) {
@@ -119,33 +132,56 @@ __device__ __forceinline__ void join_pieces(const AttnParams& P, const RowBlock&
             }
 #pragma unroll
             for (int x = 1; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-            if (lane == 0) whole[row] = make_float2(m, sum);
+            float by = 0.f;
+            if (lane == 0) by = finish(row, m, sum);
+            by = __shfl_sync(0xffffffffu, by, 0);
+            if (listed)
+                for (int i = lane; i < n; i += 32) part[row * n + i].x *= by;
         }
     }
     meet();
-    constexpr int AT_ONCE = 4;  // items of a thread: one after another their loads took 18000 cycles for 32 rows
-    for (int i0 = tid; i0 < B.nrows * (D / 4); i0 += AT_ONCE * NT) {
-        Joined z[AT_ONCE];
-        int row[AT_ONCE], d4[AT_ONCE];
+    // a thread's items side by side, AT_ONCE loads and more in flight: one after another they took 1000
+    // cycles each
+    constexpr int AT_ONCE = 8;
+    const int items = B.nrows * (D / 4);
+    for (int i0 = tid; i0 < items; i0 += AT_ONCE * NT) {
+        float4 acc[AT_ONCE];
+        int row[AT_ONCE];
+        const float4* from[AT_ONCE];
 #pragma unroll
         for (int x = 0; x < AT_ONCE; ++x) {
-            const int i = min(i0 + x * NT, B.nrows * (D / 4) - 1);
+            const int i = min(i0 + x * NT, items - 1);
             row[x] = i / (D / 4);
-            d4[x] = i % (D / 4);
-            z[x].m = whole[row[x]].x;
-            z[x].sum = whole[row[x]].y;
+            from[x] = reinterpret_cast<const float4*>(P.partial) + i;
+            acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
-#pragma unroll 4
-        for (int p = 0; p < n; ++p) {
-            const int64_t from = pieces.slot(p) * ROWS;
+        auto add = [&](int p, auto weight) {
+            const int64_t slot = pieces.slot(p) * (ROWS * (D / 4));
+            float4 v[AT_ONCE];
 #pragma unroll
-            for (int x = 0; x < AT_ONCE; ++x)
-                z[x].weigh(listed ? part[row[x] * n + p].x : ex2(stat(row[x], p).x - z[x].m),
-                           __ldcg(reinterpret_cast<const float4*>(P.partial + (from + row[x]) * D) + d4[x]));
+            for (int x = 0; x < AT_ONCE; ++x) v[x] = __ldcg(from[x] + slot);
+#pragma unroll
+            for (int x = 0; x < AT_ONCE; ++x) {
+                const float w = weight(x);
+                acc[x].x = fmaf(w, v[x].x, acc[x].x);
+                acc[x].y = fmaf(w, v[x].y, acc[x].y);
+                acc[x].z = fmaf(w, v[x].z, acc[x].z);
+                acc[x].w = fmaf(w, v[x].w, acc[x].w);
+            }
+        };
+        if (listed) {
+#pragma unroll 2
+            for (int p = 0; p < n; ++p) add(p, [&](int x) { return part[row[x] * n + p].x; });
+        } else {
+            for (int p = 0; p < n; ++p) add(p, [&](int x) { return ex2(stat(row[x], p).x - whole[row[x]].x) * whole[row[x]].y; });
         }
 #pragma unroll
         for (int x = 0; x < AT_ONCE; ++x)
-            if (i0 + x * NT < B.nrows * (D / 4)) write_row<T>(P, l, place_of(P, B, h, row[x]), d4[x], z[x]);
+            if (i0 + x * NT < items && to[row[x]] >= 0) {
+                const bool seen = whole[row[x]].y != 0.f;  // else 0, whatever the values that it does not see are
+                const float4 o = seen ? acc[x] : make_float4(0.f, 0.f, 0.f, 0.f);
+                c8::store_out(static_cast<T*>(P.out.data) + to[row[x]] + 4 * ((i0 + x * NT) % (D / 4)), o);
+            }
     }
 }
 
