@@ -126,20 +126,31 @@ __device__ __forceinline__ bool line_start(const Params& P, int* scratch, LineSt
         want = at - l * per_layer;
         return true;
     };
-    if (entries <= 32) {  // every warp for itself: no barrier
-        const int lane = threadIdx.x & 31;
-        const int mine = lane < entries ? tiles_of(lane) * P.c.H : 0;
-        int incl = mine;
+    if (entries <= 128) {  // every warp for itself, up to four entries a lane: no barrier
+        const int lane = threadIdx.x & 31, per = (entries + 31) / 32;
+        int mine[4], sum = 0;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) mine[x] = x < per && lane * per + x < entries ? tiles_of(lane * per + x) * P.c.H : 0;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) sum += mine[x];
+        int incl = sum;
 #pragma unroll
         for (int x = 1; x < 32; x <<= 1) {
             const int o = __shfl_up_sync(0xffffffffu, incl, x);
             if (lane >= x) incl += o;
         }
         if (!place(__shfl_sync(0xffffffffu, incl, 31))) return false;
-        const uint32_t hit = __ballot_sync(0xffffffffu, want >= incl - mine && want < incl);
+        const uint32_t hit = __ballot_sync(0xffffffffu, want >= incl - sum && want < incl);
         if (hit == 0) return false;  // not reached while the call's arrays stay as they are
-        e = __ffs(hit) - 1;
-        before = __shfl_sync(0xffffffffu, incl - mine, e);
+        int first_of = incl - sum, at_entry = lane * per;  // the lane's entry that holds `want`
+#pragma unroll
+        for (int x = 0; x < 3; ++x)
+            if (x + 1 < per && want >= first_of + mine[x] && at_entry == lane * per + x) {
+                first_of += mine[x];
+                ++at_entry;
+            }
+        e = __shfl_sync(0xffffffffu, at_entry, __ffs(hit) - 1);
+        before = __shfl_sync(0xffffffffu, first_of, __ffs(hit) - 1);
     } else {
         const int mine0 = static_cast<int>(threadIdx.x) < entries ? tiles_of(threadIdx.x) : 0;
         int per_layer = mine0;

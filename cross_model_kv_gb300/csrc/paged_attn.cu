@@ -776,9 +776,11 @@ cudaError_t pick(kvb_dtype dtype, int d, const AttnPlan& p, const AttnParams* P,
 
 // CTAs, at most `most`: where units of one length leave no CTA with parts of two, and not too few CTAs
 // with the others' keys too, that many.  With 304 CTAs of this file's kernel, 16 x 8192 / 16 x 32768 keys of one length
-// take 86 / 310 us so and 90 / 321 on all of them, unequal ones (16 x 1024 .. 8192) 54 either way.  The tcgen05 kernel
+// take 86 / 310 us so and 90 / 321 on all of them, unequal ones (16 x 1024 .. 8192) 54 either way; more
+// units than CTAs, unequal ones, 186 and 184.  The tcgen05 kernel
 // has 152 and longer ways from one unit to the next: 128 of them 86 and 152 93 us, but unequal lengths 94 and 78.
 int even_share(int64_t units, int most, bool tensor) {
+    if (units > most && !tensor) return most;
     const int64_t n = units <= most ? units * (most / units) : (units + (units + most - 1) / most - 1) / ((units + most - 1) / most);
     return n * 20 >= most * (tensor ? 18 : 15) ? static_cast<int>(n) : most;
 }

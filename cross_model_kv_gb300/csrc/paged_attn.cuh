@@ -69,19 +69,19 @@ template <typename T, int D, int ROWS, int NT, class Meet>
 __device__ __forceinline__ void join_pieces(const AttnParams& P, const RowBlock& B, const Pieces& pieces, int64_t unit, int l, int h,
                                             int* s_last, float* buf, int cap, Meet meet) {
     const int tid = threadIdx.x;
-    __threadfence();
     meet();
-    if (tid == 0) {
+    if (tid == 0) {  // its fences, with the barriers, order what all threads wrote and will read
         *s_last = false;
+        __threadfence();
         if (KVB_IN_BOUNDS(P.err, unit, 1, P.units) && c8::pieces_in_bounds(P, pieces)) {
             const int n = atomicAdd(P.counters + unit, 1);
             *s_last = n == pieces.n - 1;
             if (n == pieces.n - 1) P.counters[unit] = 0;
         }
+        __threadfence();
     }
     meet();
     if (!*s_last) return;
-    __threadfence();
     const int n = pieces.n, lane = tid & 31;
     float2* whole = reinterpret_cast<float2*>(buf);              // [ROWS] reference, 1 / sum
     int64_t* to = reinterpret_cast<int64_t*>(buf + 2 * ROWS);    // [ROWS] element of P.out, or -1
