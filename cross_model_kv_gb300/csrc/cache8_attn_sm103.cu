@@ -71,15 +71,6 @@ constexpr uint32_t step_v(int kk) { return (kk * 16 * 128) >> 4; }
 constexpr uint32_t idesc_f16_f32(uint32_t M, uint32_t N) {
     return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
-template <int N>
-__device__ __forceinline__ void regs_up() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_down() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
 // The issuing warps run converged and elect the lane at the products only: under `lane == 0` eight
 // of them and their commit took 840 to 1160 cycles to issue, so 400 to 600 (1024 tokens over 16K: 526
 // -> 503 us).  Row maxima are taken of three numbers an instruction (by fmaxf: 503 us, not 495).

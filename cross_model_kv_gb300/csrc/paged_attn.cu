@@ -592,7 +592,7 @@ __global__ void __launch_bounds__(32 * WARPS) line_kernel(const __grid_constant_
         }
         if (pieces > 1)
             join_pieces<T, D, ROWS, NT>(P, B, Pieces{pieces, c0}, unit, l, h, &s_last, reinterpret_cast<float*>(smem), S::MORE / 4,
-                                        [] { __syncthreads(); });
+                                        threadIdx.x, [] { __syncthreads(); });
 
         at += last - first;
         if (at >= stop) return;
@@ -757,7 +757,8 @@ cudaError_t instance(const AttnParams* P, const AttnPlan& p, cudaStream_t s, int
 template <typename T, int D>
 cudaError_t instance_rows(const AttnPlan& p, const AttnParams* P, cudaStream_t s, int* fit) {
     if constexpr (sizeof(T) == 4) return p.rows == 4 ? instance<T, D, 4>(P, p, s, fit) : instance<T, D, 8>(P, p, s, fit);
-    else return p.rows == 32 ? instance<T, D, 4>(P, p, s, fit) : p.rows == 16 ? instance<T, D, 2>(P, p, s, fit) : instance<T, D, 1>(P, p, s, fit);
+    else if constexpr (D < 64) return p.rows == 32 ? instance<T, D, 4>(P, p, s, fit) : p.rows == 16 ? instance<T, D, 2>(P, p, s, fit) : instance<T, D, 1>(P, p, s, fit);
+    else return p.rows == 16 ? instance<T, D, 2>(P, p, s, fit) : instance<T, D, 1>(P, p, s, fit);
 }
 
 template <typename T>
@@ -795,7 +796,7 @@ AttnPlan plan_attention(const Pages& c, const Seqs& q, kvb_dtype dtype, int g, i
     p.tensor = dtype == KVB_BF16 && c.d >= 64 && most > MMA_ROWS && c.n_pages > 0 && all_blocks < 2147483648.0;  // (blocks are TMA coordinates)
     // blocks of up to 64 rows in the tcgen05 kernel, as small as their number allows
     const int64_t few = (most + 63) / 64, each = few > 0 ? (most + few - 1) / few : 1;
-    p.rows = p.tensor ? (each <= 16 ? 16 : each <= 32 ? 32 : each <= 48 ? 48 : 64) : dtype == KVB_F32 ? (most <= 4 ? 4 : 8) : most <= 8 ? 8 : most <= 16 ? 16 : 32;
+    p.rows = p.tensor ? (each <= 32 ? 32 : each <= 48 ? 48 : 64) : dtype == KVB_F32 ? (most <= 4 ? 4 : 8) : most <= 8 ? 8 : most <= 16 || c.d >= 64 ? 16 : 32;
     const double blocks = static_cast<double>((most + p.rows - 1) / p.rows);
     const double units = blocks * c.n_layers * q.n_seq * c.H;
     p.tiles = units * ((max_kv + TILE - 1) / TILE);  // of 64 keys; the tcgen05 kernel's have 128

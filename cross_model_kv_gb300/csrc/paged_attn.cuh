@@ -64,11 +64,10 @@ __device__ __forceinline__ void write_row(const AttnParams& P, int l, RowPlace a
 // After a piece of a unit is written: the last CTA of the unit to arrive joins the pieces, in
 // order.  All pieces' statistics go to shared memory (`buf`, `cap` floats, free) and become their weights,
 // then each thread adds its columns, with the loads of each part in flight together.
-// meet(): the NT threads, numbered from 0, meet.
+// meet(): the NT threads, numbered from 0 by tid, meet.
 template <typename T, int D, int ROWS, int NT, class Meet>
 __device__ __forceinline__ void join_pieces(const AttnParams& P, const RowBlock& B, const Pieces& pieces, int64_t unit, int l, int h,
-                                            int* s_last, float* buf, int cap, Meet meet) {
-    const int tid = threadIdx.x;
+                                            int* s_last, float* buf, int cap, int tid, Meet meet) {
     meet();
     if (tid == 0) {  // its fences, with the barriers, order what all threads wrote and will read
         *s_last = false;

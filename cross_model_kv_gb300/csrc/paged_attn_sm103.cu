@@ -11,17 +11,18 @@
 // (Query rows as M, 128 of them whatever their number, 64 keys a tile: 122 us for 16 sequences of
 // 8192 keys, 8 heads, 32 rows each, 1860 cycles a tile, of which HBM takes 1400; the products' warps
 // took 900 to 1000 cycles to issue eight of 128 x 64 x 16 or 128 x 128 x 16.)
-//   warps 0..3  softmax, a key a thread: scores from TMEM to registers, the weights of its key to
-//               shared memory, every row's sum in registers until the piece ends.  No thread knows a row's
-//               maximum: they vote whether some score passes its reference by 2^8, and only then reduce,
-//               and rescale O in TMEM.  They load the rows, write the outputs and join the pieces of
-//               shared units;
-//   warp 4      page numbers, and TMA loads of K and V into rings of tiles, 128-byte swizzle, key
+//   warps 0..3, 4..7  softmax of every other piece of a unit, a key a thread: scores from TMEM to
+//               registers, the weights of its key to shared memory, every row's sum in registers until the
+//               piece ends.  No thread knows a row's maximum: they vote whether some score passes its
+//               reference by 2^8, and only then reduce, and rescale O in TMEM.  They load the rows, write
+//               the outputs and join the pieces of shared units, 10000 cycles and more for each piece,
+//               while the other four warps are in the next one;
+//   warp 8      page numbers, and TMA loads of K and V into rings of tiles, 128-byte swizzle, key
 //               rows: K-major for S, MN-major for O, as they lie in the pages;
-//   warp 5      one lane issues S^T = K Q^T;
-//   warp 6      and O^T += V^T P^T.
+//   warp 9      one lane issues S^T = K Q^T;
+//   warp 10     and O^T += V^T P^T.
 // At head_dim 64 O^T has 64 rows and M is 128 all the same: the upper 64 are the lower ones again.
-// TMEM: score buffer b at 64 b, O's high part at 128, its low part NR columns on.
+// TMEM: score buffer b at 64 b, O's high part at 128 and 256 (even and odd pieces), its low part NR columns on.
 // HBM bounds it.  Every role finds the CTA's pieces by itself, so that the rings are filled while the
 // softmax goes from one unit to the next.
 // Every wait is bounded; after one gives up, the softmax still arrives at the units that it shares,
@@ -36,21 +37,48 @@ namespace paged {
 namespace {
 
 constexpr int TK = 128;          // keys of a tile, TMEM lanes
-constexpr int SOFT = 128;        // threads of the softmax
-constexpr int NUM_THREADS = SOFT + 96;
+constexpr int SOFT = 128;        // threads of the softmax of a piece
+constexpr int NUM_THREADS = 2 * SOFT + 128;  // the last warp only makes up a warpgroup
+// Registers a thread: 168 at launch, then by role.  256 * 192 + 128 * 96 = 61440 of the launch's 384 * 168 = 64512.
+constexpr int REGS_SOFTMAX = 192, REGS_OTHERS = 96;
 constexpr int GROUPS = TK / 16;  // 16 keys lie in one page
 constexpr int ATOM = TK * 128;   // 64 dims of a tile's keys, or 64 rows' weights of them
-constexpr uint32_t TM_S = 0, TM_O = 128, TM_COLUMNS = 256;
+constexpr uint32_t TM_S = 0, TM_O = 128, TM_COLUMNS = 512;
 constexpr uint64_t DRAIN_NS = 200ull * 1000 * 1000;
 constexpr uint32_t IDESC_A_MN = 1u << 15;  // A operand MN-major
 
+// What the softmax of even, or of odd, pieces notes.
+struct Rows {
+    alignas(16) float ref[64];       // of every row
+    alignas(16) float by[64];        // factors of a raise; 1 / sum of a piece
+    alignas(16) float part[4][64];   // of a warp
+    int pos[64];                     // positions of the rows
+    int64_t to[64];                  // element of P.out that their outputs begin at
+    int last;
+};
+struct Smem {
+    uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
+    uint64_t s_full[2], s_empty[2], p_full[2], pv_done[2], q_full[2], o_full[2], handed[2], drain[2];
+    uint32_t tmem;
+    int abort;
+    // bit of a tile's 16-key group whose page is there; a tile's place is written again 8 tiles later, when
+    // at most four tiles are behind the one that is loaded
+    uint64_t info_full[8];
+    uint32_t present[8];
+    int scan[NUM_THREADS / 32];
+    LineStart start;
+    Rows rows[2];
+};
+
 template <int HD, int NR>
 struct Layout {
-    static constexpr int Q_HALF = NR * 128, Q = HD / 64 * Q_HALF;  // 64 dims of all rows
+    static constexpr int Q_HALF = NR * 128, Q = HD / 64 * Q_HALF;  // 64 dims of all rows; even and odd pieces
     static constexpr int TILE = HD / 64 * ATOM;                    // of K, and of V
     static constexpr int STAGES = HD == 128 ? 2 : 4;
-    static constexpr int WEIGHTS = (2 * NR + 63) / 64 * ATOM;      // a buffer of two
-    static constexpr int BYTES = 1024 + (Q + 1023) / 1024 * 1024 + STAGES * 2 * TILE + 2 * WEIGHTS + 4096;
+    static constexpr int WEIGHTS = (2 * NR + 63) / 64 * ATOM;      // a buffer of weights
+    static constexpr int BUFFERS = HD == 128 && NR == 64 ? 1 : 2;  // two where there is room
+    static constexpr int BYTES = 1024 + 2 * Q + STAGES * 2 * TILE + BUFFERS * WEIGHTS + sizeof(Smem);
+    static_assert(Q % 1024 == 0, "layout");
     static_assert(BYTES <= 227 * 1024, "layout");
 };
 
@@ -112,26 +140,6 @@ struct Walk {
     }
 };
 
-struct Smem {
-    uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
-    uint64_t s_full[2], s_empty[2], p_full[2], pv_done[2], q_full, drain[2];
-    uint32_t tmem;
-    int abort;
-    // bit of a tile's 16-key group whose page is there; a tile's place is written again 8 tiles later, when
-    // at most four tiles are behind the one that is loaded
-    uint64_t info_full[8];
-    uint32_t present[8];
-    int scan[NUM_THREADS / 32];
-    LineStart start;
-    int last;
-    alignas(16) float ref[64];       // of every row
-    alignas(16) float by[64];        // factors of a raise, sums of a piece
-    alignas(16) float part[4][64];   // of a warp
-    int pos[64];                     // positions of the rows
-    int64_t to[64];                  // element of P.out that their outputs begin at
-};
-static_assert(sizeof(Smem) <= 4096, "layout");
-
 struct Maps {
     CUtensorMap kv[2];
 };
@@ -156,9 +164,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) rows_kernel(const __grid_const
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t* sK = smem;
     uint8_t* sV = sK + STAGES * L::TILE;
-    uint8_t* sP = sV + STAGES * L::TILE;  // [2]
-    uint8_t* sQ = sP + 2 * L::WEIGHTS;
-    Smem& M = *reinterpret_cast<Smem*>(sQ + (L::Q + 1023) / 1024 * 1024);
+    uint8_t* sP = sV + STAGES * L::TILE;
+    uint8_t* sQ = sP + L::BUFFERS * L::WEIGHTS;
+    Smem& M = *reinterpret_cast<Smem*>(sQ + 2 * L::Q);
     volatile int* abort_flag = &M.abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const DevErr derr{P.err.word, P.err.timeout_ns};
@@ -179,13 +187,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) rows_kernel(const __grid_const
             mbar_init(&M.p_full[b], SOFT);
             mbar_init(&M.pv_done[b], 1);
             mbar_init(&M.drain[b], 1);
+            mbar_init(&M.q_full[b], SOFT);
+            mbar_init(&M.o_full[b], 1);
+            mbar_init(&M.handed[b], SOFT);
         }
         for (int i = 0; i < 8; ++i) mbar_init(&M.info_full[i], 1);
-        mbar_init(&M.q_full, SOFT);
         M.abort = 0;
         fence_mbar_init();
     }
-    if (warp == 5) {
+    if (warp == 9) {
         tmem_alloc(&M.tmem, TM_COLUMNS);
         tmem_relinquish();
     }
@@ -196,19 +206,29 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) rows_kernel(const __grid_const
     auto wait_all = [&](uint64_t* b, uint32_t parity) {  // warp-uniform outcome
         return __all_sync(0xffffffffu, mbar_wait(b, parity, derr, abort_flag)) != 0;
     };
-    // t counts the tiles of all of the CTA's pieces: stage t % STAGES, buffers (scores, weights) t & 1
+    // t counts the tiles of all of the CTA's pieces: stage t % STAGES, scores t & 1, weights t % BUFFERS
     uint32_t t = 0;
     Segment G;
 
-    if (warp < SOFT / 32) {
+    if (warp < 2 * SOFT / 32) {
         // ------------------------------------------------------- softmax
-        const int key = threadIdx.x;  // of the tile, and TMEM lane; the dim of an output
-        const uint32_t tl = tmem_base + (static_cast<uint32_t>(32 * warp) << 16);
+        regs_up<REGS_SOFTMAX>();
+        const int half = warp / 4, w4 = warp & 3;  // even or odd pieces; warp of them
+        const int key = threadIdx.x % SOFT;        // of the tile, and TMEM lane; the dim of an output
+        const uint32_t tl = tmem_base + (static_cast<uint32_t>(32 * w4) << 16);
+        const uint32_t tO = tl + TM_O + 128u * half;
+        uint8_t* const myQ = sQ + half * L::Q;
+        Rows& N = M.rows[half];
+        const int id = 1 + half;  // of the barrier
         const float f = P.scale_log2;
         bool ok = true;
-        while (W.next(P, G)) {
+        for (int n = 0; W.next(P, G); ++n) {
             const int ntiles = G.tiles();
-            named_bar_sync(1, SOFT);  // ref, pos and by are free
+            if ((n & 1) != half) {
+                t += ntiles;
+                continue;
+            }
+            named_bar_sync(id, SOFT);  // ref, pos and by are free
             // the rows: 16-byte chunks c of row r, by all threads
             {
                 constexpr int MINE = NR * (HD / 8) / SOFT;
@@ -222,19 +242,22 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) rows_kernel(const __grid_const
 #pragma unroll
                 for (int i = 0; i < MINE; ++i) {
                     const int r = (i * SOFT + key) / (HD / 8), c = key % (HD / 8);
-                    *reinterpret_cast<uint4*>(sQ + (c >> 3) * L::Q_HALF + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = u[i];
+                    *reinterpret_cast<uint4*>(myQ + (c >> 3) * L::Q_HALF + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = u[i];
                 }
             }
             if (key < NR) {
-                M.ref[key] = key < G.B.nrows ? LOWEST : 0.f;  // rows that do not exist: weights of 1, never raised
-                M.pos[key] = key < G.B.nrows ? G.B.pos + (G.B.row0 + key) / P.g : INT32_MAX;
+                N.ref[key] = key < G.B.nrows ? LOWEST : 0.f;  // rows that do not exist: weights of 1, never raised
+                N.pos[key] = key < G.B.nrows ? G.B.pos + (G.B.row0 + key) / P.g : INT32_MAX;
             }
             fence_proxy_async_smem();
-            mbar_arrive(&M.q_full);
+            mbar_arrive(&M.q_full[half]);
             float sum[NR];
 #pragma unroll
             for (int n = 0; n < NR; ++n) sum[n] = 0.f;
-            named_bar_sync(1, SOFT);
+            named_bar_sync(id, SOFT);
+            // The piece before has its last weights: a wait for a phase of a barrier is only right when the
+            // phase before it is over, and those of the tiles are waited for by one half after the other.
+            if (n > 0) ok = ok && wait_all(&M.handed[half ^ 1], ((n - 1) >> 1) & 1);
             for (int i = 0; i < ntiles; ++i, ++t) {
                 const uint32_t b = t & 1, use = t >> 1, stage = t % STAGES;
                 ok = ok && wait_all(&M.info_full[t % 8], (t / 8) & 1);
@@ -254,36 +277,36 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) rows_kernel(const __grid_const
                     if (!__all_sync(0xffffffffu, !dead && j <= G.B.pos_lo)) {
 #pragma unroll
                         for (int n = 0; n < NR; ++n)
-                            if (dead || j > M.pos[n]) sv[n] = 0xff800000u;  // -inf
+                            if (dead || j > N.pos[n]) sv[n] = 0xff800000u;  // -inf
                     }
                     float top = -INFINITY;
 #pragma unroll
                     for (int n = 0; n < NR; n += 4) {
-                        const float4 r = *reinterpret_cast<const float4*>(M.ref + n);
+                        const float4 r = *reinterpret_cast<const float4*>(N.ref + n);
                         top = max3(top, fmaf(__uint_as_float(sv[n]), f, -r.x), fmaf(__uint_as_float(sv[n + 1]), f, -r.y));
                         top = max3(top, fmaf(__uint_as_float(sv[n + 2]), f, -r.z), fmaf(__uint_as_float(sv[n + 3]), f, -r.w));
                     }
                     above = top > MARGIN;
                 }
-                if (!named_bar_and(1, SOFT, ok && !above)) {
-                    ok = named_bar_and(1, SOFT, ok);
+                if (!named_bar_and(id, SOFT, ok && !above)) {
+                    ok = named_bar_and(id, SOFT, ok);
                     if (!ok) break;
                     // some score passes its reference: every row's is raised to the tile's maximum
 #pragma unroll
                     for (int n = 0; n < NR; ++n) {
                         const float x = warp_max(__uint_as_float(sv[n]));
-                        if (lane == 0) M.part[warp][n] = x;
+                        if (lane == 0) N.part[w4][n] = x;
                     }
-                    named_bar_sync(1, SOFT);
+                    named_bar_sync(id, SOFT);
                     if (key < NR) {
-                        const float x = fmaxf(fmaxf(M.part[0][key], M.part[1][key]), fmaxf(M.part[2][key], M.part[3][key]));
-                        const float old = M.ref[key], up = fmaxf(old, x * f);
-                        M.by[key] = ex2(old - up);
-                        M.ref[key] = up;
+                        const float x = fmaxf(fmaxf(N.part[0][key], N.part[1][key]), fmaxf(N.part[2][key], N.part[3][key]));
+                        const float old = N.ref[key], up = fmaxf(old, x * f);
+                        N.by[key] = ex2(old - up);
+                        N.ref[key] = up;
                     }
-                    named_bar_sync(1, SOFT);
+                    named_bar_sync(id, SOFT);
 #pragma unroll
-                    for (int n = 0; n < NR; ++n) sum[n] *= M.by[n];
+                    for (int n = 0; n < NR; ++n) sum[n] *= N.by[n];
                     if (i > 0) {  // O is complete up to the tile before
                         ok = wait_all(&M.pv_done[b ^ 1], ((t - 1) >> 1) & 1);
                         if (ok) {
@@ -291,11 +314,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) rows_kernel(const __grid_const
 #pragma unroll 1
                             for (int c = 0; c < 2 * NR; c += 16) {
                                 uint32_t o[16];
-                                tmem_ld16(tl + TM_O + c, o);
+                                tmem_ld16(tO + c, o);
                                 tmem_ld_wait();
 #pragma unroll
-                                for (int n = 0; n < 16; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * M.by[(c + n) % NR]);
-                                tmem_st16(tl + TM_O + c, o);
+                                for (int n = 0; n < 16; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * N.by[(c + n) % NR]);
+                                tmem_st16(tO + c, o);
                             }
                             tmem_st_wait();
                             tc_fence_before();
@@ -303,17 +326,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) rows_kernel(const __grid_const
                     }
                 }
                 // the weights' buffer is free when its products are done
-                if (ok && use > 0) ok = wait_all(&M.pv_done[b], (use - 1) & 1);
+                if (ok && t >= L::BUFFERS) ok = wait_all(&M.pv_done[(t - L::BUFFERS) & 1], ((t - L::BUFFERS) >> 1) & 1);
                 if (ok && __any_sync(0xffffffffu, dead)) ok = wait_all(&M.v_full[stage], (t / STAGES) & 1);
                 if (!ok) continue;  // to the next vote
-                uint8_t* mine = sP + b * L::WEIGHTS + key * 128;
+                uint8_t* mine = sP + (t % L::BUFFERS) * L::WEIGHTS + key * 128;
 #pragma unroll
                 for (int c = 0; c < NR / 8; ++c) {
                     uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int n = 0; n < 4; ++n) {
                         const int r = 8 * c + 2 * n;
-                        const float2 ref = *reinterpret_cast<const float2*>(M.ref + r);
+                        const float2 ref = *reinterpret_cast<const float2*>(N.ref + r);
                         const float2 w = make_float2(ex2(fmaf(__uint_as_float(sv[r]), f, -ref.x)), ex2(fmaf(__uint_as_float(sv[r + 1]), f, -ref.y)));
                         sum[r] += w.x;
                         sum[r + 1] += w.y;
@@ -332,7 +355,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) rows_kernel(const __grid_const
                 fence_proxy_async_smem();
                 mbar_arrive(&M.p_full[b]);
             }
-            if (ok && ntiles > 0) ok = wait_all(&M.pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1);
+            mbar_arrive(&M.handed[half]);
+            // (a barrier of its own: those of the tiles go on with the next piece)
+            ok = ok && wait_all(&M.o_full[half], (n >> 1) & 1);
             const bool have = ok && ntiles > 0;
             if (have) tc_fence_after();
             // the rows' sums, and where their outputs go
@@ -349,30 +374,30 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) rows_kernel(const __grid_const
                         x[n] = keep + __shfl_xor_sync(0xffffffffu, give, z);
                     }
                 x[0] += __shfl_xor_sync(0xffffffffu, x[0], 16);
-                if (lane < 16) M.part[warp][n0 + lane] = x[0];
+                if (lane < 16) N.part[w4][n0 + lane] = x[0];
             }
-            named_bar_sync(1, SOFT);
+            named_bar_sync(id, SOFT);
             const bool alone = G.pieces.n == 1;
             const int64_t part0 = G.slot * NR;
-            if (key < NR && key >= G.B.nrows) M.to[key] = -1;
+            if (key < NR && key >= G.B.nrows) N.to[key] = -1;
             if (key < G.B.nrows) {
-                const float total = have ? (M.part[0][key] + M.part[1][key]) + (M.part[2][key] + M.part[3][key]) : 0.f, m = M.ref[key];
+                const float total = have ? (N.part[0][key] + N.part[1][key]) + (N.part[2][key] + N.part[3][key]) : 0.f, m = N.ref[key];
                 const RowPlace at = place_of(P, G.B, G.h, key);
                 const int64_t lse_row = (static_cast<int64_t>(G.l) * P.c.H * P.g + at.head) * P.q.T + at.token;
                 const bool inside = KVB_IN_BOUNDS(P.err, lse_row, 1, c8::rows_of(P)) && KVB_IN_BOUNDS(P.err, G.slot, 1, P.slots);
-                M.by[key] = total == 0.f ? 0.f : 1.f / total;
-                M.to[key] = inside ? G.l * P.out.l + at.head * P.out.h + at.token * P.out.t : -1;
+                N.by[key] = total == 0.f ? 0.f : 1.f / total;
+                N.to[key] = inside ? G.l * P.out.l + at.head * P.out.h + at.token * P.out.t : -1;
                 if (inside && !alone) P.part_stat[part0 + key] = make_float2(m, total);
                 if (inside && alone && P.lse) P.lse[lse_row] = total == 0.f ? -INFINITY : (m + log2f(total)) * 0.693147180559945f;
             }
-            named_bar_sync(1, SOFT);
+            named_bar_sync(id, SOFT);
             if (key < HD && (alone || KVB_IN_BOUNDS(P.err, G.slot, 1, P.slots))) {  // whole warps; lane = dim
 #pragma unroll 1
                 for (int c = 0; c < G.B.nrows; c += 16) {
                     uint32_t hi[16], lo[16];
                     if (have) {
-                        tmem_ld16(tl + TM_O + c, hi);
-                        tmem_ld16(tl + TM_O + NR + c, lo);
+                        tmem_ld16(tO + c, hi);
+                        tmem_ld16(tO + NR + c, lo);
                         tmem_ld_wait();
                     } else {
 #pragma unroll
@@ -386,8 +411,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) rows_kernel(const __grid_const
                         float by[16];
 #pragma unroll
                         for (int n = 0; n < 16; ++n) {
-                            to[n] = M.to[c + n];
-                            by[n] = M.by[c + n];
+                            to[n] = N.to[c + n];
+                            by[n] = N.by[c + n];
                         }
 #pragma unroll
                         for (int n = 0; n < 16; ++n)
@@ -403,11 +428,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) rows_kernel(const __grid_const
             }
             tc_fence_before();
             if (!alone)
-                join_pieces<__nv_bfloat16, HD, NR, SOFT>(P, G.B, G.pieces, G.unit, G.l, G.h, &M.last, reinterpret_cast<float*>(sP), 2 * L::WEIGHTS / 4,
-                                                         [] { named_bar_sync(1, SOFT); });
+                join_pieces<__nv_bfloat16, HD, NR, SOFT>(P, G.B, G.pieces, G.unit, G.l, G.h, &N.last, reinterpret_cast<float*>(myQ), L::Q / 4,
+                                                         key, [&] { named_bar_sync(id, SOFT); });
         }
-    } else if (warp == SOFT / 32) {
+    } else if (warp == 2 * SOFT / 32) {
         // ------------------------------------------------------- pages and loads
+        regs_down<REGS_OTHERS>();
         constexpr int HALVES = HD / 64;
         const int rows = min(P.c.page, TK), per = TK / rows;  // keys of a load; loads of a tile, of 64 dims
         bool go = true;
@@ -473,9 +499,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) rows_kernel(const __grid_const
                 mbar_wait_drain(&M.v_full[stage], parity, DRAIN_NS / 16);
             }
         }
+    } else if (warp == 2 * SOFT / 32 + 3) {
+        regs_down<REGS_OTHERS>();
     } else {
         // ------------------------------------------------------- products
-        const bool scores = warp == SOFT / 32 + 1;
+        regs_down<REGS_OTHERS>();
+        const bool scores = warp == 2 * SOFT / 32 + 1;
         bool go = true;
         const uint64_t k0 = sdesc_k_sw128(smem_u32(sK)), q0 = sdesc_k_sw128(smem_u32(sQ));
         const uint64_t v0 = sdesc_mn_sw128(smem_u32(sV), HD == 128 ? ATOM : 0), p0 = sdesc_mn_sw128(smem_u32(sP), ATOM);
@@ -488,7 +517,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) rows_kernel(const __grid_const
                     *abort_flag = 1;
                     go = false;
                 }
-                go = go && wait_all(&M.q_full, n & 1);
+                go = go && wait_all(&M.q_full[n & 1], (n >> 1) & 1);
             }
             for (int i = 0; go && i < ntiles; ++i, ++t) {
                 const uint32_t b = t & 1, use = t >> 1, stage = t % STAGES, parity = (t / STAGES) & 1;
@@ -502,7 +531,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) rows_kernel(const __grid_const
                     if (elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < HD / 16; ++kk)
-                            umma_bf16(tmem_base + TM_S + 64 * b, k + step_k<ATOM>(kk), q0 + step_k<L::Q_HALF>(kk), idesc, kk != 0);
+                            umma_bf16(tmem_base + TM_S + 64 * b, k + step_k<ATOM>(kk), q0 + (n & 1) * (L::Q / 16) + step_k<L::Q_HALF>(kk), idesc, kk != 0);
                         umma_commit(&M.s_full[b]);
                         umma_commit(&M.k_empty[stage]);
                     }
@@ -512,17 +541,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) rows_kernel(const __grid_const
                     go = go && wait_all(&M.p_full[b], use & 1);
                     if (!go) break;
                     tc_fence_after();
-                    const uint64_t v = v0 + stage * (L::TILE / 16), p = p0 + b * (L::WEIGHTS / 16);
+                    const uint64_t v = v0 + stage * (L::TILE / 16), p = p0 + (t % L::BUFFERS) * (L::WEIGHTS / 16);
                     if (elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < TK / 16; ++kk)
-                            umma_bf16(tmem_base + TM_O, v + kk * (16 * 128 / 16), p + kk * (16 * 128 / 16), idesc, (i | kk) != 0);
+                            umma_bf16(tmem_base + TM_O + 128 * (n & 1), v + kk * (16 * 128 / 16), p + kk * (16 * 128 / 16), idesc, (i | kk) != 0);
                         umma_commit(&M.v_empty[stage]);
                         umma_commit(&M.pv_done[b]);
                     }
                 }
                 __syncwarp();
             }
+            if (go && !scores && elect_one()) umma_commit(&M.o_full[n & 1]);  // the piece's outputs are complete
             __syncwarp();
         }
         if (elect_one()) {
@@ -534,7 +564,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) rows_kernel(const __grid_const
 
     tc_fence_before();
     __syncthreads();
-    if (warp == 5) {
+    if (warp == 9) {
         __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem_base, TM_COLUMNS);
@@ -572,7 +602,6 @@ cudaError_t launch(const AttnParams& P, const AttnPlan& p, cudaStream_t s, std::
 
 template <int HD>
 cudaError_t launch_rows(const AttnParams& P, const AttnPlan& p, cudaStream_t s, std::string* why) {
-    if (p.rows == 16) return launch<HD, 16>(P, p, s, why);
     return p.rows == 32 ? launch<HD, 32>(P, p, s, why) : p.rows == 48 ? launch<HD, 48>(P, p, s, why) : launch<HD, 64>(P, p, s, why);
 }
 
