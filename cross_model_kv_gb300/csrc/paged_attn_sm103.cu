@@ -11,7 +11,7 @@
 // (Query rows as M, 128 of them whatever their number, 64 keys a tile: 122 us for 16 sequences of
 // 8192 keys, 8 heads, 32 rows each, 1860 cycles a tile, of which HBM takes 1400; the products' warps
 // took 900 to 1000 cycles to issue eight of 128 x 64 x 16 or 128 x 128 x 16.)
-//   warps 0..3, 4..7  softmax of every other piece of a unit, a key a thread: scores from TMEM to
+//   warps 0..3, 4..7  softmax of every other piece of a unit (64 rows: one set, of every piece), a key a thread: scores from TMEM to
 //               registers, the weights of its key to shared memory, every row's sum in registers until the
 //               piece ends.  No thread knows a row's maximum: they vote whether some score passes its
 //               reference by 2^8, and only then reduce, and rescale O in TMEM.  They load the rows, write
@@ -22,7 +22,7 @@
 //   warp 9      one lane issues S^T = K Q^T;
 //   warp 10     and O^T += V^T P^T.
 // At head_dim 64 O^T has 64 rows and M is 128 all the same: the upper 64 are the lower ones again.
-// TMEM: score buffer b at 64 b, O's high part at 128 and 256 (even and odd pieces), its low part NR columns on.
+// TMEM: score buffer b at 64 b, O's high part at 128 (and 256, odd pieces), its low part NR columns on.
 // HBM bounds it.  Every role finds the CTA's pieces by itself, so that the rings are filled while the
 // softmax goes from one unit to the next.
 // Every wait is bounded; after one gives up, the softmax still arrives at the units that it shares,
@@ -38,7 +38,10 @@ namespace {
 
 constexpr int TK = 128;          // keys of a tile, TMEM lanes
 constexpr int SOFT = 128;        // threads of the softmax of a piece
-constexpr int NUM_THREADS = 2 * SOFT + 128;  // the last warp only makes up a warpgroup
+// Two sets of softmax warps where their registers suffice: 64 rows take more than 200 a thread (16 x 8192 keys:
+// 99 us with one set, 121 with two).
+constexpr int sets_of(int NR) { return NR <= 48 ? 2 : 1; }
+constexpr int threads_of(int NR) { return sets_of(NR) * SOFT + 128; }  // the last warp only makes up a warpgroup
 // Registers a thread: 168 at launch, then by role.  256 * 192 + 128 * 96 = 61440 of the launch's 384 * 168 = 64512.
 constexpr int REGS_SOFTMAX = 192, REGS_OTHERS = 96;
 constexpr int GROUPS = TK / 16;  // 16 keys lie in one page
@@ -65,19 +68,19 @@ struct Smem {
     // at most four tiles are behind the one that is loaded
     uint64_t info_full[8];
     uint32_t present[8];
-    int scan[NUM_THREADS / 32];
+    int scan[12];
     LineStart start;
     Rows rows[2];
 };
 
 template <int HD, int NR>
 struct Layout {
-    static constexpr int Q_HALF = NR * 128, Q = HD / 64 * Q_HALF;  // 64 dims of all rows; even and odd pieces
+    static constexpr int Q_HALF = NR * 128, Q = HD / 64 * Q_HALF;  // 64 dims of all rows
     static constexpr int TILE = HD / 64 * ATOM;                    // of K, and of V
     static constexpr int STAGES = HD == 128 ? 2 : 4;
-    static constexpr int WEIGHTS = (2 * NR + 63) / 64 * ATOM;      // a buffer of weights
-    static constexpr int BUFFERS = HD == 128 && NR == 64 ? 1 : 2;  // two where there is room
-    static constexpr int BYTES = 1024 + 2 * Q + STAGES * 2 * TILE + BUFFERS * WEIGHTS + sizeof(Smem);
+    static constexpr int WEIGHTS = (2 * NR + 63) / 64 * ATOM;      // a buffer of two
+    static constexpr int SETS = sets_of(NR);
+    static constexpr int BYTES = 1024 + STAGES * 2 * TILE + 2 * WEIGHTS + SETS * Q + sizeof(Smem);  // rows of every set
     static_assert(Q % 1024 == 0, "layout");
     static_assert(BYTES <= 227 * 1024, "layout");
 };
@@ -157,16 +160,16 @@ __device__ __forceinline__ float warp_max(float x) {  // NaN loses
 }
 
 template <int HD, int NR>
-__global__ void __launch_bounds__(NUM_THREADS, 1) rows_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnParams P) {
+__global__ void __launch_bounds__(threads_of(NR), 1) rows_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnParams P) {
     using L = Layout<HD, NR>;
-    constexpr int STAGES = L::STAGES;
+    constexpr int STAGES = L::STAGES, SETS = L::SETS, NUM_THREADS = threads_of(NR);
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t* sK = smem;
     uint8_t* sV = sK + STAGES * L::TILE;
     uint8_t* sP = sV + STAGES * L::TILE;
-    uint8_t* sQ = sP + L::BUFFERS * L::WEIGHTS;
-    Smem& M = *reinterpret_cast<Smem*>(sQ + 2 * L::Q);
+    uint8_t* sQ = sP + 2 * L::WEIGHTS;
+    Smem& M = *reinterpret_cast<Smem*>(sQ + SETS * L::Q);
     volatile int* abort_flag = &M.abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const DevErr derr{P.err.word, P.err.timeout_ns};
@@ -195,7 +198,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) rows_kernel(const __grid_const
         M.abort = 0;
         fence_mbar_init();
     }
-    if (warp == 9) {
+    if (warp == 4 * SETS + 1) {
         tmem_alloc(&M.tmem, TM_COLUMNS);
         tmem_relinquish();
     }
@@ -206,14 +209,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) rows_kernel(const __grid_const
     auto wait_all = [&](uint64_t* b, uint32_t parity) {  // warp-uniform outcome
         return __all_sync(0xffffffffu, mbar_wait(b, parity, derr, abort_flag)) != 0;
     };
-    // t counts the tiles of all of the CTA's pieces: stage t % STAGES, scores t & 1, weights t % BUFFERS
+    // t counts the tiles of all of the CTA's pieces: stage t % STAGES, scores and weights t & 1
     uint32_t t = 0;
     Segment G;
 
-    if (warp < 2 * SOFT / 32) {
+    if (warp < 4 * SETS) {
         // ------------------------------------------------------- softmax
-        regs_up<REGS_SOFTMAX>();
-        const int half = warp / 4, w4 = warp & 3;  // even or odd pieces; warp of them
+        if constexpr (SETS == 2) regs_up<REGS_SOFTMAX>();
+        const int half = warp / 4, w4 = warp & 3;  // even or odd pieces; warp of the set
         const int key = threadIdx.x % SOFT;        // of the tile, and TMEM lane; the dim of an output
         const uint32_t tl = tmem_base + (static_cast<uint32_t>(32 * w4) << 16);
         const uint32_t tO = tl + TM_O + 128u * half;
@@ -222,9 +225,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) rows_kernel(const __grid_const
         const int id = 1 + half;  // of the barrier
         const float f = P.scale_log2;
         bool ok = true;
-        for (int n = 0; W.next(P, G); ++n) {
+        for (int piece = 0; W.next(P, G); ++piece) {
             const int ntiles = G.tiles();
-            if ((n & 1) != half) {
+            if (piece % SETS != half) {
                 t += ntiles;
                 continue;
             }
@@ -256,8 +259,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) rows_kernel(const __grid_const
             for (int n = 0; n < NR; ++n) sum[n] = 0.f;
             named_bar_sync(id, SOFT);
             // The piece before has its last weights: a wait for a phase of a barrier is only right when the
-            // phase before it is over, and those of the tiles are waited for by one half after the other.
-            if (n > 0) ok = ok && wait_all(&M.handed[half ^ 1], ((n - 1) >> 1) & 1);
+            // phase before it is over, and those of the tiles are waited for by one set of warps after the other.
+            if (SETS == 2 && piece > 0) ok = ok && wait_all(&M.handed[half ^ 1], ((piece - 1) >> 1) & 1);
             for (int i = 0; i < ntiles; ++i, ++t) {
                 const uint32_t b = t & 1, use = t >> 1, stage = t % STAGES;
                 ok = ok && wait_all(&M.info_full[t % 8], (t / 8) & 1);
@@ -326,10 +329,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) rows_kernel(const __grid_const
                     }
                 }
                 // the weights' buffer is free when its products are done
-                if (ok && t >= L::BUFFERS) ok = wait_all(&M.pv_done[(t - L::BUFFERS) & 1], ((t - L::BUFFERS) >> 1) & 1);
+                if (ok && use > 0) ok = wait_all(&M.pv_done[b], (use - 1) & 1);
                 if (ok && __any_sync(0xffffffffu, dead)) ok = wait_all(&M.v_full[stage], (t / STAGES) & 1);
                 if (!ok) continue;  // to the next vote
-                uint8_t* mine = sP + (t % L::BUFFERS) * L::WEIGHTS + key * 128;
+                uint8_t* mine = sP + b * L::WEIGHTS + key * 128;
 #pragma unroll
                 for (int c = 0; c < NR / 8; ++c) {
                     uint32_t hi[4], lo[4];
@@ -355,9 +358,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) rows_kernel(const __grid_const
                 fence_proxy_async_smem();
                 mbar_arrive(&M.p_full[b]);
             }
-            mbar_arrive(&M.handed[half]);
+            if (SETS == 2) mbar_arrive(&M.handed[half]);
             // (a barrier of its own: those of the tiles go on with the next piece)
-            ok = ok && wait_all(&M.o_full[half], (n >> 1) & 1);
+            ok = ok && wait_all(&M.o_full[half], (piece / SETS) & 1);
             const bool have = ok && ntiles > 0;
             if (have) tc_fence_after();
             // the rows' sums, and where their outputs go
@@ -431,9 +434,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) rows_kernel(const __grid_const
                 join_pieces<__nv_bfloat16, HD, NR, SOFT>(P, G.B, G.pieces, G.unit, G.l, G.h, &N.last, reinterpret_cast<float*>(myQ), L::Q / 4,
                                                          key, [&] { named_bar_sync(id, SOFT); });
         }
-    } else if (warp == 2 * SOFT / 32) {
+    } else if (warp == 4 * SETS) {
         // ------------------------------------------------------- pages and loads
-        regs_down<REGS_OTHERS>();
+        if constexpr (SETS == 2) regs_down<REGS_OTHERS>();
         constexpr int HALVES = HD / 64;
         const int rows = min(P.c.page, TK), per = TK / rows;  // keys of a load; loads of a tile, of 64 dims
         bool go = true;
@@ -499,12 +502,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) rows_kernel(const __grid_const
                 mbar_wait_drain(&M.v_full[stage], parity, DRAIN_NS / 16);
             }
         }
-    } else if (warp == 2 * SOFT / 32 + 3) {
-        regs_down<REGS_OTHERS>();
+    } else if (warp == 4 * SETS + 3) {
+        if constexpr (SETS == 2) regs_down<REGS_OTHERS>();
     } else {
         // ------------------------------------------------------- products
-        regs_down<REGS_OTHERS>();
-        const bool scores = warp == 2 * SOFT / 32 + 1;
+        if constexpr (SETS == 2) regs_down<REGS_OTHERS>();
+        const bool scores = warp == 4 * SETS + 1;
         bool go = true;
         const uint64_t k0 = sdesc_k_sw128(smem_u32(sK)), q0 = sdesc_k_sw128(smem_u32(sQ));
         const uint64_t v0 = sdesc_mn_sw128(smem_u32(sV), HD == 128 ? ATOM : 0), p0 = sdesc_mn_sw128(smem_u32(sP), ATOM);
@@ -517,7 +520,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) rows_kernel(const __grid_const
                     *abort_flag = 1;
                     go = false;
                 }
-                go = go && wait_all(&M.q_full[n & 1], (n >> 1) & 1);
+                go = go && wait_all(&M.q_full[n % SETS], (n / SETS) & 1);
             }
             for (int i = 0; go && i < ntiles; ++i, ++t) {
                 const uint32_t b = t & 1, use = t >> 1, stage = t % STAGES, parity = (t / STAGES) & 1;
@@ -531,7 +534,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) rows_kernel(const __grid_const
                     if (elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < HD / 16; ++kk)
-                            umma_bf16(tmem_base + TM_S + 64 * b, k + step_k<ATOM>(kk), q0 + (n & 1) * (L::Q / 16) + step_k<L::Q_HALF>(kk), idesc, kk != 0);
+                            umma_bf16(tmem_base + TM_S + 64 * b, k + step_k<ATOM>(kk), q0 + (n % SETS) * (L::Q / 16) + step_k<L::Q_HALF>(kk), idesc, kk != 0);
                         umma_commit(&M.s_full[b]);
                         umma_commit(&M.k_empty[stage]);
                     }
@@ -541,18 +544,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) rows_kernel(const __grid_const
                     go = go && wait_all(&M.p_full[b], use & 1);
                     if (!go) break;
                     tc_fence_after();
-                    const uint64_t v = v0 + stage * (L::TILE / 16), p = p0 + (t % L::BUFFERS) * (L::WEIGHTS / 16);
+                    const uint64_t v = v0 + stage * (L::TILE / 16), p = p0 + b * (L::WEIGHTS / 16);
                     if (elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < TK / 16; ++kk)
-                            umma_bf16(tmem_base + TM_O + 128 * (n & 1), v + kk * (16 * 128 / 16), p + kk * (16 * 128 / 16), idesc, (i | kk) != 0);
+                            umma_bf16(tmem_base + TM_O + 128 * (n % SETS), v + kk * (16 * 128 / 16), p + kk * (16 * 128 / 16), idesc, (i | kk) != 0);
                         umma_commit(&M.v_empty[stage]);
                         umma_commit(&M.pv_done[b]);
                     }
                 }
                 __syncwarp();
             }
-            if (go && !scores && elect_one()) umma_commit(&M.o_full[n & 1]);  // the piece's outputs are complete
+            if (go && !scores && elect_one()) umma_commit(&M.o_full[n % SETS]);  // the piece's outputs are complete
             __syncwarp();
         }
         if (elect_one()) {
@@ -564,7 +567,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) rows_kernel(const __grid_const
 
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == 4 * SETS + 1) {
         __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem_base, TM_COLUMNS);
@@ -596,7 +599,7 @@ cudaError_t launch(const AttnParams& P, const AttnPlan& p, cudaStream_t s, std::
     }
     cudaError_t e = cudaFuncSetAttribute(rows_kernel<HD, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<HD, NR>::BYTES);
     if (e != cudaSuccess) return e;
-    rows_kernel<HD, NR><<<p.ctas, NUM_THREADS, Layout<HD, NR>::BYTES, s>>>(maps, P);
+    rows_kernel<HD, NR><<<p.ctas, threads_of(NR), Layout<HD, NR>::BYTES, s>>>(maps, P);
     return cudaGetLastError();
 }
 
