@@ -404,10 +404,12 @@ def test_many_rows(kvb, d, page, H, g, n, lens, layout):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
-@pytest.mark.parametrize("d,g,n", [(128, 8, 1), (64, 4, 1), (128, 4, 4), (32, 3, 9), (64, 8, 8), (128, 8, 5)])
-def test_long_cache_split_over_ctas_joins_and_repeats_bit_for_bit(kvb, d, g, n, dtype):
-    P = Pool(kvb, 1, 1, d, 64, 3, 9000, dtype, seed=5)
-    lens = np.asarray([9000, 4097, 8191])
+@pytest.mark.parametrize("d,g,n,lens", [(128, 8, 1, [9000, 4097, 8191]), (64, 4, 1, [9000, 4097, 8191]), (128, 4, 4, [9000, 4097, 8191]),
+                                        (32, 3, 9, [9000, 4097, 8191]), (64, 8, 8, [9000, 4097, 8191]), (128, 8, 5, [9000, 4097, 8191]),
+                                        (128, 8, 5, [2500, 40, 1300]), (64, 5, 5, [9000, 64, 128]), (128, 20, 3, [600, 601, 8])])
+def test_long_cache_split_over_ctas_joins_and_repeats_bit_for_bit(kvb, d, g, n, lens, dtype):
+    lens = np.asarray(lens)
+    P = Pool(kvb, 1, 1, d, 64, 3, int(lens.max()), dtype, seed=5)
     P.fill(lens)
     q = P.rows(1, g, 3 * n, sigma=1.5)
     off, pos = offsets([n] * 3), lens - n
