@@ -35,7 +35,7 @@ kvb_status check_rows(const kvb_rows* r, const char* name, const char* what, int
     for (Axis& a : axis) {
         if (a.size <= 1) a.stride = 0;  // one index: the stride means nothing
         if (a.stride % unit) return fail(KVB_ERR_INVALID_ARG, w + " has a stride that is not a multiple of 16 bytes");
-        if (a.stride < 0 || static_cast<double>(a.stride) * static_cast<double>(a.size) > 4e18)
+        if (a.stride < 0 || static_cast<double>(a.stride) * static_cast<double>(a.size) > 1e18)  // three of them, in bytes, in 64 bits
             return fail(KVB_ERR_INVALID_ARG, w + " has a stride that is negative or too large");
     }
     out->data = r->data;

@@ -519,6 +519,7 @@ __device__ __forceinline__ void attend(const AttnParams& P, const RowBlock& B, i
     // the part that is asked for while part m is used is m + DEPTH - 1, in the place of part m - 1
     constexpr int NEXT_K = (R::DEPTH - 1) % 2, NEXT_V = R::DEPTH % 2;
     int stage = 0;
+    bool odd = false;  // values that are not finite have been taken out
     for (int n = 0; n < feed.steps; ++n) {
         copies_wait<R::DEPTH - 2>();
         const bool absent = (feed.absent >> stage) & 1;
@@ -531,13 +532,28 @@ __device__ __forceinline__ void attend(const AttnParams& P, const RowBlock& B, i
         copies_wait<R::DEPTH - 2>();
         __syncwarp();
         feed.template ask<NEXT_V>(P, n + R::DEPTH / 2);
+        if (j + STEP - 1 > B.pos_lo && B.pos_lo + 1 < k1) {  // some rows see keys of it that others do not
+#pragma unroll 1
+            for (int i = (threadIdx.x & 31) + max(B.pos_lo + 1 - j, 0) * R::CH; i < STEP * R::CH; i += 32) odd |= make_finite<T>(reinterpret_cast<uint4*>(mine + stage * R::PART)[i]);
+            __syncwarp();
+        }
         math.values(feed.ring + stage * R::PART, shared);
         stage = stage + 1 == R::DEPTH ? 0 : stage + 1;
     }
     copies_wait<0>();
     __syncwarp();
     math.finish(reinterpret_cast<float*>(mine), reinterpret_cast<float2*>(smem + S::STAT) + warp * S::ROWS);
-    __syncthreads();
+    if (__syncthreads_or(odd)) {
+#pragma unroll 1
+        for (int i = threadIdx.x; i < B.nrows * D; i += 32 * NW) {  // row 0 .. of warp 0's outputs
+            const int row = i / D, pos = B.pos + (B.row0 + row) / P.g;
+            for (int j = max(k0, B.pos_lo + 1); j < k1 && j <= pos; ++j) {
+                const float v = value_of<T>(P, s, l, h, j, i % D);
+                if (not_finite(v)) reinterpret_cast<float*>(smem)[i] += v;
+            }
+        }
+        __syncthreads();
+    }
 }
 
 // Four columns of a row over a CTA's warps.

@@ -41,6 +41,35 @@ struct Joined {
     __device__ __forceinline__ float lse() const { return sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.693147180559945f; }
 };
 
+// Keys that some rows of a block see and others do not (the last of several new tokens) may have values
+// that are not finite: 0 times them is NaN, for rows that do not see them too.  Such values become 0 where
+// they lie in shared memory, and are added afterwards to the rows that see them: any weight of them is the same.
+__device__ __forceinline__ bool not_finite(float x) { return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u; }
+template <typename T>
+__device__ __forceinline__ uint32_t finite_or_0(uint32_t w) {  // an fp32 number, or two of bf16
+    if constexpr (sizeof(T) == 4) return (w & 0x7f800000u) == 0x7f800000u ? 0u : w;
+    else return w & (((w & 0x7f80u) == 0x7f80u ? 0u : 0xffffu) | ((w & 0x7f800000u) == 0x7f800000u ? 0u : 0xffff0000u));
+}
+template <typename T>
+__device__ __forceinline__ bool make_finite(uint4& v) {  // whether it was not
+    const uint4 x = make_uint4(finite_or_0<T>(v.x), finite_or_0<T>(v.y), finite_or_0<T>(v.z), finite_or_0<T>(v.w));
+    const bool odd = ((v.x ^ x.x) | (v.y ^ x.y) | (v.z ^ x.z) | (v.w ^ x.w)) != 0;
+    if (odd) v = x;
+    return odd;
+}
+// Element `dim` of the value of key j, 0 if its page is not there.
+template <typename T>
+__device__ __forceinline__ float value_of(const AttnParams& P, int s, int l, int h, int j, int dim) {
+    const int p = j >> P.c.page_log2;
+    if (p >= P.q.max_pages || !c8::table_in_bounds(P.q, P.err, s, p)) return 0.f;
+    const int pid = __ldg(P.q.page_table + static_cast<int64_t>(s) * P.q.max_pages + p);
+    const int64_t blocks = (static_cast<int64_t>(P.c.l_begin) + P.c.n_layers) * P.c.n_pages * P.c.H;
+    const int64_t block = ((static_cast<int64_t>(P.c.l_begin) + l) * P.c.n_pages + pid) * P.c.H + h;
+    if (pid < 0 || pid >= P.c.n_pages || !KVB_IN_BOUNDS(P.err, block, 1, blocks)) return 0.f;
+    const int64_t at = (((block << P.c.page_log2) + (j & (P.c.page - 1))) << P.c.d_log2) + dim;
+    return static_cast<float>(static_cast<const T*>(P.c.kv[1])[at]);
+}
+
 // Row `row` of a unit, in rows with strides and in [n_layers][Hq][T].
 struct RowPlace {
     int head, token;

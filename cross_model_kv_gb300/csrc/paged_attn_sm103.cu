@@ -56,6 +56,7 @@ struct Rows {
     alignas(16) float by[64];        // factors of a raise; 1 / sum of a piece
     alignas(16) float part[4][64];   // of a warp
     int pos[64];                     // positions of the rows
+    int odd;                         // values that are not finite have been taken out of the products
     int64_t to[64];                  // element of P.out that their outputs begin at
     int last;
 };
@@ -248,9 +249,10 @@ __global__ void __launch_bounds__(threads_of(NR), 1) rows_kernel(const __grid_co
                     *reinterpret_cast<uint4*>(myQ + (c >> 3) * L::Q_HALF + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = u[i];
                 }
             }
+            if (key == 0) N.odd = 0;
             if (key < NR) {
                 N.ref[key] = key < G.B.nrows ? LOWEST : 0.f;  // rows that do not exist: weights of 1, never raised
-                N.pos[key] = key < G.B.nrows ? G.B.pos + (G.B.row0 + key) / P.g : INT32_MAX;
+                N.pos[key] = key < G.B.nrows ? G.B.pos + (G.B.row0 + key) / P.g : INT32_MAX - 1;
             }
             fence_proxy_async_smem();
             mbar_arrive(&M.q_full[half]);
@@ -267,20 +269,21 @@ __global__ void __launch_bounds__(threads_of(NR), 1) rows_kernel(const __grid_co
                 ok = ok && wait_all(&M.s_full[b], use & 1);
                 const int j = G.k0 + i * TK + key;
                 uint32_t sv[NR];
-                bool above = false, dead = false;
+                bool above = false, special = false;  // special: not every row sees the key
+                auto dead = [&] { return j >= G.k1 || !((M.present[t % 8] >> (key / 16)) & 1u); };  // nothing sees it
                 if (ok) {
                     tc_fence_after();
 #pragma unroll
                     for (int c = 0; c < NR; c += 16) tmem_ld16(tl + TM_S + 64 * b + c, *reinterpret_cast<uint32_t(*)[16]>(sv + c));
-                    const uint32_t present = M.present[t % 8];
-                    dead = j >= G.k1 || !((present >> (key / 16)) & 1u);  // nothing sees the key
+                    special = dead() || j > G.B.pos_lo;
                     tmem_ld_wait();
                     tc_fence_before();
                     mbar_arrive(&M.s_empty[b]);
-                    if (!__all_sync(0xffffffffu, !dead && j <= G.B.pos_lo)) {
+                    if (__any_sync(0xffffffffu, special)) {
+                        const int from = dead() ? INT32_MAX : j;
 #pragma unroll
                         for (int n = 0; n < NR; ++n)
-                            if (dead || j > N.pos[n]) sv[n] = 0xff800000u;  // -inf
+                            if (from > N.pos[n]) sv[n] = 0xff800000u;  // -inf
                     }
                     float top = -INFINITY;
 #pragma unroll
@@ -330,7 +333,7 @@ __global__ void __launch_bounds__(threads_of(NR), 1) rows_kernel(const __grid_co
                 }
                 // the weights' buffer is free when its products are done
                 if (ok && use > 0) ok = wait_all(&M.pv_done[b], (use - 1) & 1);
-                if (ok && __any_sync(0xffffffffu, dead)) ok = wait_all(&M.v_full[stage], (t / STAGES) & 1);
+                if (ok && __any_sync(0xffffffffu, special)) ok = wait_all(&M.v_full[stage], (t / STAGES) & 1);
                 if (!ok) continue;  // to the next vote
                 uint8_t* mine = sP + b * L::WEIGHTS + key * 128;
 #pragma unroll
@@ -350,10 +353,15 @@ __global__ void __launch_bounds__(threads_of(NR), 1) rows_kernel(const __grid_co
                     *reinterpret_cast<uint4*>(mine + (c >> 3) * ATOM + (((c & 7) ^ (key & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                     *reinterpret_cast<uint4*>(mine + ((LO + c) >> 3) * ATOM + ((((LO + c) & 7) ^ (key & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
-                if (dead) {  // slots that nothing sees may hold anything: their value rows are zeros
-                    uint8_t* row = sV + stage * L::TILE + key * 128;
-#pragma unroll
-                    for (int c = 0; c < HD / 8; ++c) *reinterpret_cast<uint4*>(row + (c >> 3) * ATOM + 16 * (c & 7)) = make_uint4(0, 0, 0, 0);
+                if (special) {  // slots that nothing sees may hold anything: their value rows are zeros
+                    uint4* row = reinterpret_cast<uint4*>(sV + stage * L::TILE + key * 128);
+                    const bool none = dead();
+#pragma unroll 4
+                    for (int c = 0; c < HD / 8; ++c) {
+                        uint4& v = row[(c >> 3) * (ATOM / 16) + (c & 7)];
+                        if (none) v = make_uint4(0, 0, 0, 0);
+                        else if (make_finite<__nv_bfloat16>(v)) N.odd = 1;
+                    }
                 }
                 fence_proxy_async_smem();
                 mbar_arrive(&M.p_full[b]);
@@ -409,6 +417,16 @@ __global__ void __launch_bounds__(threads_of(NR), 1) rows_kernel(const __grid_co
                     float o[16];
 #pragma unroll
                     for (int n = 0; n < 16; ++n) o[n] = __uint_as_float(hi[n]) + __uint_as_float(lo[n]);
+                    if (have && N.odd) {
+#pragma unroll 1
+                        for (int j = max(G.k0, G.B.pos_lo + 1); j < G.k1; ++j) {
+                            const float v = value_of<__nv_bfloat16>(P, G.s, G.l, G.h, j, key);
+                            if (not_finite(v))
+#pragma unroll
+                                for (int n = 0; n < 16; ++n)
+                                    if (j <= N.pos[c + n]) o[n] += v;
+                        }
+                    }
                     if (alone) {
                         int64_t to[16];
                         float by[16];

@@ -488,8 +488,8 @@ kvb_status kvb_cache8_append(kvb_ctx* ctx, const kvb_cache8* cache, const kvb_se
 
 /*
  * Attention of new tokens over the cache: for one token a sequence, or the few of a
- * draft that is checked (any number is right; keys are read once for 32 query rows, a
- * head's tokens times n_q_heads / H, of bf16 and once for 8 of fp32):
+ * draft that is checked (any number is right; keys are read once for up to 64 query rows,
+ * a head's tokens times n_q_heads / H, of bf16, 32 where d is below 64, and for 8 of fp32):
  *     out_i = sum over visible j of softmax_j(scale * q_i . k_j) v_j,
  *     lse_i = log sum over visible j of exp(scale * q_i . k_j),
  * with seqs, visibility, n_q_heads, scale and lse as for kvb_cache8_attention; q and out
@@ -497,13 +497,14 @@ kvb_status kvb_cache8_append(kvb_ctx* ctx, const kvb_cache8* cache, const kvb_se
  * that sees nothing is 0 with lse -infinity; rows of tokens that no sequence owns are
  * left as they are.  Products of bf16 numbers are exact and summed in fp32; bf16 calls
  * carry a weight as a bf16 pair (16 bits) into its product with v, fp32 calls as fp32.
- * Statistics and sums are fp32.  What slots past kv_len or the query's position hold is
- * never used, and a page outside [0, n_pages) counts as absent and is recorded.
- * The result does not depend on timing.
+ * Statistics and sums are fp32.  What slots past kv_len or a query's position hold never
+ * reaches it, infinities and NaN included; a visible value that is not finite makes its
+ * element of the output infinite or NaN.  A page outside [0, n_pages) counts as absent and
+ * is recorded.  The result does not depend on timing.
  *
  * Workspace: the context's attention workspace, with the rules of kvb_cache8_attention:
  * attention calls on one context, of both kinds of cache, never overlap on the GPU; make a
- * call once before capturing it.
+ * call once before capturing it.  (A call with few keys and few rows needs none of it.)
  */
 kvb_status kvb_paged_attention(kvb_ctx* ctx, const kvb_paged_cache* cache, const kvb_seqs* seqs, int32_t l_begin,
                                int32_t n_layers, const kvb_rows* q, int32_t n_q_heads, int64_t T, double scale,

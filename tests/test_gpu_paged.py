@@ -512,6 +512,44 @@ def test_a_query_that_is_not_finite_stays_in_its_row(kvb, bad, dtype, g):
     assert torch.isnan(out[0, 3, 1]).any() or torch.isinf(lse[0, 3, 1])
 
 
+@pytest.mark.parametrize("dtype,H,d,page,g,n", [(BF, 1, 128, 64, 2, 5), (BF, 2, 64, 16, 1, 3), (BF, 1, 32, 32, 3, 9), (BF, 160, 16, 16, 3, 4), (F32, 1, 64, 64, 1, 7),
+                                                (F32, 2, 128, 16, 2, 4), (F32, 160, 16, 32, 3, 4), (BF, 2, 128, 64, 8, 5), (BF, 1, 64, 16, 16, 4), (BF, 2, 64, 128, 4, 8),
+                                                (BF, 1, 128, 16, 9, 40), (F32, 1, 128, 64, 9, 40), (BF, 1, 32, 64, 9, 40)])
+def test_new_tokens_that_are_not_finite_stay_hidden_from_earlier_ones(kvb, dtype, H, d, page, g, n):
+    lens = np.array([130, n, 2500, 64 + n // 2])
+    P = Pool(kvb, 1, H, d, page, 4, 2500, dtype)
+    P.fill(lens)
+    pos, off = lens - n, offsets([n] * 4)
+    q = P.rows(1, H * g, 4 * n)
+    good, z = attend(P, q, off, pos)
+
+    def put(x, token, dim, value):  # in every sequence and head
+        for s in range(4):
+            at = int(pos[s]) + token
+            x[:, P.table[s, at // page], :, at % page, dim] = value
+
+    inf, nan = float("inf"), float("nan")
+    put(P.cache.v, 2, 0, nan), put(P.cache.v, 2, 1, inf), put(P.cache.v, n - 1, 1, -inf if n > 3 else nan), put(P.cache.v, n - 1, d - 1, inf)
+    want = good.clone().view(1, H * g, 4, n, d)
+    want[..., 2:, 0] = nan
+    want[..., 2:, 1] = inf
+    want[..., n - 1, 1] = nan
+    want[..., n - 1, d - 1] = inf
+    for _ in range(2):
+        out, lse = attend(P, q, off, pos)
+        assert torch.equal(lse, z)
+        # infinite or NaN: a weight w goes into its product as hi + lo with lo = bf16(w - hi), which is 0 or negative for
+        # half of all w, so that hi * inf + lo * inf = inf + NaN or inf - inf where the block sees all of the keys
+        assert torch.equal(torch.isfinite(out), torch.isfinite(want.view_as(out)))
+        assert torch.equal(out.nan_to_num(0, 0, 0), want.view_as(out).nan_to_num(0, 0, 0))
+    put(P.cache.k, n - 1, 3, nan)
+    out, lse = (x.view(1, H * g, 4, n, -1) for x in attend(P, q, off, pos))
+    assert torch.isnan(out[..., n - 1, :]).all() and torch.isnan(lse[..., n - 1, :]).all()
+    out, want = out[..., :n - 1, :], want[..., :n - 1, :]
+    assert torch.equal(torch.isfinite(out), torch.isfinite(want)) and torch.equal(out.nan_to_num(0, 0, 0), want.nan_to_num(0, 0, 0))
+    kvb.kvb_ctx_check(P.ctx)
+
+
 @pytest.mark.parametrize("dtype,g", [(BF, 4), (F32, 4), (BF, 20)])
 def test_a_bad_page_is_absent_and_reported(kvb, dtype, g):
     P = Pool(kvb, 1, 2, 64, 16, 3, 200, dtype)
