@@ -1,17 +1,19 @@
 #!/usr/bin/env python
-"""Decode from a mapped cache kept in 8 bits.
+"""Decode from a mapped cache.
 
-A source model's prefilled cache is mapped to the target model (kvb_map_apply)
-and stored in the paged 8-bit cache (kvb_cache8_write).  Then the target decodes:
-for every new token and layer its key and value are written into the cache and
-its queries attend over it (kvb_cache8_attention).  At the end the 8-bit cache is
-read back (kvb_cache8_read) and its attention outputs are compared with those of
-the bf16 cache (kvb_attention_cosine).
+A source model's prefilled cache is mapped to the target model (kvb_map_apply) and
+stored in a paged cache: in 8 bits (kvb_cache8_write) or, with --cache model, in the
+model's own type (kvb_paged_append).  Then the target decodes: for every new token and
+layer its projection's output, q, k and v heads in one row and no RoPE yet, is appended
+with the rotation on the way (kvb_cache8_append, kvb_paged_append) and its rotated
+queries attend over the cache (kvb_cache8_attention, kvb_paged_attention).  At the end
+the cache is read back and its attention outputs are compared with those of a plain bf16
+cache that torch has rotated (kvb_attention_cosine).
 
 Synthetic data of the given shapes stands in for the two models: the queries, keys
 and values that a model would compute for each new token are random draws.
 
-    python examples/decode_mapped_cache.py [--layers-src 8 --layers-tgt 12 --prefix 4096 --tokens 64]
+    python examples/decode_mapped_cache.py [--cache model --layers-src 8 --layers-tgt 12 --prefix 4096 --tokens 64]
 """
 import argparse
 import os
@@ -25,6 +27,18 @@ import cross_model_kv_gb300 as kvb  # noqa: E402
 import synth  # noqa: E402
 
 
+THETA = 1e6
+
+
+def rotated(x, pos):
+    """x [..., T, d] with RoPE of the positions, rotate-half, in fp32."""
+    d = x.shape[-1]
+    angle = pos.double()[:, None] * THETA ** (-torch.arange(0, d, 2, device=x.device).double() / d)
+    c, s = angle.cos().float(), angle.sin().float()
+    lo, hi = x.float().split(d // 2, dim=-1)
+    return torch.cat([lo * c - hi * s, hi * c + lo * s], dim=-1).to(x.dtype)
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--layers-src", type=int, default=8)
@@ -34,10 +48,11 @@ def main(argv=None):
     ap.add_argument("--prefix", type=int, default=4096)
     ap.add_argument("--tokens", type=int, default=64)
     ap.add_argument("--page", type=int, default=64)
+    ap.add_argument("--cache", choices=["8bit", "model"], default="8bit", help="what the paged cache holds")
     a = ap.parse_args(argv)
     L_s, L_t, H, Hq, d, k, T = a.layers_src, a.layers_tgt, a.kv_heads, a.q_heads, 128, 4, a.prefix
     dev, bf = "cuda", torch.bfloat16
-    spec = lambda n: {"n_layers": n, "n_kv_heads": H, "head_dim": d, "rope_theta": 1e6}
+    spec = lambda n: {"n_layers": n, "n_kv_heads": H, "head_dim": d, "rope_theta": THETA}
     total = T + a.tokens
     ctx = kvb.kvb_ctx_create(spec(L_s), spec(L_t), k, total)
 
@@ -49,31 +64,37 @@ def main(argv=None):
     map_k, map_v = (torch.empty((L_t, H, T, d), dtype=bf, device=dev) for _ in range(2))
     kvb.kvb_map_apply(ctx, src_k, src_v, pos, sel, sel, W_k, W_v, b_k, b_v, map_k, map_v)
 
-    # stored in 8 bits: one sequence, its pages in any order
+    # stored in pages: one sequence, its pages in any order
+    eight = a.cache == "8bit"
     n_pages = -(-total // a.page)
-    cache = kvb.kvb_cache8_create(ctx, n_pages, a.page)
     i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=dev)
     table = torch.randperm(n_pages, device=dev).to(torch.int32)[None]
-    kvb.kvb_cache8_write(ctx, cache, kvb.Seqs(table, i32([0, T]), i32([0]), max_tokens=T), map_k, map_v)
+    prefix = kvb.Seqs(table, i32([0, T]), i32([0]), max_tokens=T)
+    if eight:
+        cache = kvb.kvb_cache8_create(ctx, n_pages, a.page)
+        kvb.kvb_cache8_write(ctx, cache, prefix, map_k, map_v)
+        append, attend = kvb.kvb_cache8_append, kvb.kvb_cache8_attention
+    else:
+        cache = kvb.kvb_paged_create(ctx, n_pages, a.page, bf)
+        kvb.kvb_paged_append(ctx, cache, prefix, map_k, map_v, rotate=False)
+        append, attend = kvb.kvb_paged_append, kvb.kvb_paged_attention
 
     # decoding: the call's tensors stay in place, only the position moves on
-    new_k, new_v = (synth.torch_content(s, L_t, H, a.tokens, d, 0.5, bf, dev) for s in (6, 7))
-    new_q = synth.torch_content(8, L_t, Hq, a.tokens, d, 0.5, bf, dev)
+    heads = synth.torch_content(6, L_t, Hq + 2 * H, a.tokens, d, 0.5, bf, dev)  # no RoPE
     at = i32([T])
     seqs = kvb.Seqs(table, i32([0, 1]), at, max_tokens=1, max_kv=total)
-    tok_k, tok_v = (torch.empty((1, H, 1, d), dtype=bf, device=dev) for _ in range(2))
-    tok_q = torch.empty((1, Hq, 1, d), dtype=bf, device=dev)
-    out = torch.empty((L_t, Hq, a.tokens, d), dtype=bf, device=dev)
-    o = torch.empty_like(tok_q)
+    row = torch.empty((1, Hq + 2 * H, 1, d), dtype=bf, device=dev)  # a token's projection
+    tok_q, tok_k, tok_v = row.split([Hq, H, H], dim=1)
+    rot_q, o = (torch.empty((1, Hq, 1, d), dtype=bf, device=dev) for _ in range(2))
+    out, all_q = (torch.empty((L_t, Hq, a.tokens, d), dtype=bf, device=dev) for _ in range(2))
 
     def token(i):
         for l in range(L_t):
-            tok_k.copy_(new_k[l:l + 1, :, i:i + 1])
-            tok_v.copy_(new_v[l:l + 1, :, i:i + 1])
-            tok_q.copy_(new_q[l:l + 1, :, i:i + 1])
-            kvb.kvb_cache8_write(ctx, cache, seqs, tok_k, tok_v, l_begin=l)
-            kvb.kvb_cache8_attention(ctx, cache, seqs, tok_q, o, l_begin=l)
+            row.copy_(heads[l:l + 1, :, i:i + 1])
+            append(ctx, cache, seqs, tok_k, tok_v, q=tok_q, q_out=rot_q, l_begin=l)
+            attend(ctx, cache, seqs, rot_q, o, l_begin=l)
             out[l, :, i].copy_(o[0, :, 0])
+            all_q[l, :, i].copy_(rot_q[0, :, 0])
         at.add_(1)
 
     t0, t1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
@@ -84,20 +105,24 @@ def main(argv=None):
     torch.cuda.synchronize()
     kvb.kvb_ctx_check(ctx)
 
-    # the 8-bit cache against the bf16 one, every decoded token a query
-    whole = kvb.Seqs(table, i32([0, total]), i32([0]), max_tokens=total)
-    back_k, back_v = (torch.empty((L_t, H, total, d), dtype=bf, device=dev) for _ in range(2))
-    kvb.kvb_cache8_read(ctx, cache, whole, back_k, back_v)
-    full_k, full_v = torch.cat([map_k, new_k], dim=2), torch.cat([map_v, new_v], dim=2)
-    cos = torch.empty((L_t, Hq, a.tokens), device=dev)
+    # the cache against a plain one, every decoded token a query
     where = torch.arange(total, dtype=torch.int32, device=dev)
-    kvb.kvb_attention_cosine(ctx, new_q, where[T:].contiguous(), back_k, back_v, full_k, full_v, where, cos)
+    back_k, back_v = (torch.empty((L_t, H, total, d), dtype=bf, device=dev) for _ in range(2))
+    if eight:
+        kvb.kvb_cache8_read(ctx, cache, kvb.Seqs(table, i32([0, total]), i32([0]), max_tokens=total), back_k, back_v)
+    else:
+        for x, back in ((cache.k, back_k), (cache.v, back_v)):
+            back.copy_(x[:, table[0].long()].transpose(1, 2).flatten(2, 3)[:, :, :total])
+    new_k, new_v = heads[:, Hq:Hq + H], heads[:, Hq + H:]
+    full_k, full_v = torch.cat([map_k, rotated(new_k, where[T:])], dim=2), torch.cat([map_v, new_v], dim=2)
+    cos = torch.empty((L_t, Hq, a.tokens), device=dev)
+    kvb.kvb_attention_cosine(ctx, all_q, where[T:].contiguous(), back_k, back_v, full_k, full_v, where, cos)
     torch.cuda.synchronize()
     kvb.kvb_ctx_check(ctx)
-    bits8, bits16 = (cache.k.numel() + cache.v.numel()) / 2 ** 20, 2 * (full_k.numel() + full_v.numel()) / 2 ** 20
-    print(f"{T} mapped + {a.tokens} decoded tokens, {L_t} layers: cache {bits8:.1f} MiB in 8 bits, {bits16:.1f} MiB in bf16")
-    print(f"{t0.elapsed_time(t1) / a.tokens:.3f} ms a token (write + attention, {L_t} layers)")
-    print(f"attention-output cosine, 8 bits against bf16: mean {cos.mean():.5f}, min {cos.min():.5f}")
+    mib = (cache.k.numel() + cache.v.numel()) * cache.k.element_size() / 2 ** 20
+    print(f"{T} mapped + {a.tokens} decoded tokens, {L_t} layers: cache {mib:.1f} MiB ({'8 bits' if eight else 'bf16'})")
+    print(f"{t0.elapsed_time(t1) / a.tokens:.3f} ms a token (append + attention, {L_t} layers)")
+    print(f"attention-output cosine against a plain bf16 cache: mean {cos.mean():.5f}, min {cos.min():.5f}")
     return {"cos_mean": float(cos.mean()), "cos_min": float(cos.min()), "out": out}
 
 

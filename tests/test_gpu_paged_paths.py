@@ -93,6 +93,19 @@ def test_many_sequences_of_every_length(kvb, dtype, g):  # noqa: F811
         check_attention(P, q, np.arange(m + 1), lens[:m] - 1, out, lse)
 
 
+def test_example_decodes_from_pages_of_the_models_type(kvb):  # noqa: F811
+    # the cache holds what the plain one does but for the sums and table that torch rounds otherwise: a key's
+    # element differs by a bf16 step, 2^-8 of it, now and then, and moves an output less than 2^-6 rad; cos 0.999 is 0.045
+    sys.path.insert(0, os.path.join(ROOT, "examples"))
+    try:
+        import decode_mapped_cache as ex
+    finally:
+        sys.path.pop(0)
+    r = ex.main(["--cache", "model", "--layers-src", "5", "--layers-tgt", "3", "--kv-heads", "2", "--q-heads", "8", "--prefix", "700",
+                 "--tokens", "9", "--page", "32"])
+    assert r["cos_min"] > 0.999 and torch.isfinite(r["out"]).all()
+
+
 def test_everything_on_the_checked_build():
     if not torch.cuda.is_available():
         pytest.skip("no CUDA device")
