@@ -26,12 +26,22 @@ namespace paged {
 
 namespace {
 
-constexpr int WARPS = 4;              // of a CTA of the line
+constexpr int WARPS = 4;              // of a CTA
 constexpr int STEP = 16;              // keys of a warp's step
-constexpr int TILE = STEP * WARPS;    // a tile of the line
-constexpr int MIN_TILES = 2;
-constexpr int MMA_ROWS = 16;           // bf16 rows up to which mma.sync keeps up (d 64, 128)
-constexpr int FEW_SHARES = 32;          // steps of a warp up to which a cluster takes a unit
+constexpr int TILE = STEP * WARPS;    // a tile
+constexpr int MIN_TILES = 2;          // 1 and 4 measure the same within 2 %
+// bf16 rows up to which mma.sync keeps up (d 64, 128).  16 rows, here / on tcgen05: 14.2 / 23.5 us for one
+// sequence of 4096 keys, 8 heads, 58.0 / 59.1 for 16 of 1024 to 8192; 24 rows, 16 of 8192: 126 / 92.
+constexpr int MMA_ROWS = 16;
+// A CTA for each unit, if there are more of them than SMs and they are short: up to SHORT tiles, or so many units
+// a tile that the last ones to finish do not count.  Against the line, 8 rows of d 128: 256 sequences of up to
+// 300 keys, 8 heads, 40 us and 54, 128 of up to 1000 50 and 64, 256 of up to 4000 327 and 344; but 64 of up to 8192 202
+// and 181, and 64 of 1000 each 53 and 48 (512 units on 608 places).
+constexpr int SHORT = 16;
+// Steps of a warp up to which a cluster takes a unit where there are no more units than SMs.  One row block of 8,
+// 8 heads, cluster / line: 4096 keys 10 / 14 us, 32768 34 / 41; 8 sequences of 8192 45 / 53, 16 of 1024 to 8192
+// 57.9 / 55.7 (64 steps would take the clusters there).
+constexpr int FEW_SHARES = 32;
 
 // A step's K or V rows in shared memory: 16-byte chunks, chunk c of row r at c ^ swizzle(r), so that
 // eight rows' chunks of one number, and a row's chunks, lie in different banks.
@@ -50,8 +60,10 @@ template <typename T, int D>
 struct Ring {
     static constexpr int CH = D * sizeof(T) / 16;       // 16-byte chunks of a row
     static constexpr int PART = STEP * D * sizeof(T);   // bytes
-    static constexpr int FIT = 24576 / PART;            // four warps' rings twice on an SM
-    static constexpr int DEPTH = FIT > 16 ? 16 : FIT;   // d 128: 6 parts in bf16, 3 in fp32
+    // Four warps' rings fit an SM four times in bf16, twice in fp32.  Twice in bf16, 6 parts of d 128: 16 x 32768 keys
+    // 313 us against 303, 64 x 1024..8192 185 against 181, one sequence of 32768 31.6 against 34.3.
+    static constexpr int FIT = (sizeof(T) == 2 ? 12288 : 24576) / PART;
+    static constexpr int DEPTH = FIT > 16 ? 16 : FIT;   // d 128: 3 parts
     static constexpr int BYTES = DEPTH * PART;
 };
 
@@ -645,7 +657,7 @@ __device__ __forceinline__ void hand2(uint32_t p, float2 v) {
 
 // Few keys: a cluster of CTAs for each unit, an even share of its keys each.  Every CTA hands each of
 // the others its part of the columns that the other joins, through distributed shared memory: no
-// global scratch, no atomics.
+// global scratch, no atomics.  And many short units: a CTA for each, which waits for no other.
 template <typename T, int D, int NB>
 __global__ void __launch_bounds__(32 * WARPS) cluster_kernel(const __grid_constant__ AttnParams P) {
     constexpr int NT = 32 * WARPS;
@@ -830,6 +842,11 @@ AttnPlan plan_attention(const Pages& c, const Seqs& q, kvb_dtype dtype, int g, i
         p.ctas = static_cast<int>(p.units) * p.cluster;
         if (p.units <= most_of[0] && shares <= static_cast<int64_t>(FEW_SHARES) * p.cluster) return p;
         p.cluster = 0;
+    }
+    if (!p.tensor && p.units > num_sms && (shares <= SHORT || p.units > SHORT * shares)) {
+        p.cluster = 1;  // a CTA for each unit
+        p.ctas = static_cast<int>(p.units);
+        return p;
     }
     int fit = 1;
     if (!p.tensor) pick(dtype, c.d, p, nullptr, nullptr, &fit);
