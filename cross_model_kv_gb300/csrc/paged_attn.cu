@@ -33,6 +33,11 @@ constexpr int MIN_TILES = 2;          // 1 and 4 measure the same within 2 %
 // bf16 rows up to which mma.sync keeps up (d 64, 128).  16 rows, here / on tcgen05: 14.2 / 23.5 us for one
 // sequence of 4096 keys, 8 heads, 58.0 / 59.1 for 16 of 1024 to 8192; 24 rows, 16 of 8192: 126 / 92.
 constexpr int MMA_ROWS = 16;
+// Tiles an SM, of 16 rows each, up to which clusters take more rows, if all are resident at once: the tcgen05 kernel joins
+// many pieces of few units slowly.  8 heads, clusters / tcgen05: 40 rows of one sequence of 300, 4096, 8192 keys 10.7,
+// 18.2, 26.9 / 16.6, 34.9, 37.1 us, four of 1024 16.8 / 18.9, of 2048 (36 tiles an SM, which tcgen05 takes) 22.3 / 21.0;
+// 128 rows of one of 4096 27.1 / 24.1.
+constexpr int FEW_TILES = 24;
 // A CTA for each unit, if there are more of them than SMs and they are short: up to SHORT tiles, or so many units
 // a tile that the last ones to finish do not count.  Against the line, 8 rows of d 128: 256 sequences of up to
 // 300 keys, 8 heads, 40 us and 54, 128 of up to 1000 50 and 64, 256 of up to 4000 327 and 344; but 64 of up to 8192 202
@@ -821,7 +826,10 @@ AttnPlan plan_attention(const Pages& c, const Seqs& q, kvb_dtype dtype, int g, i
     const int64_t most = static_cast<int64_t>(q.max_tokens) * g;  // rows of one sequence and head
     const int64_t max_kv = q.max_kv > 0 ? q.max_kv : 1;
     const double all_blocks = (static_cast<double>(c.l_begin) + c.n_layers) * c.n_pages * c.H;
-    p.tensor = dtype == KVB_BF16 && c.d >= 64 && most > MMA_ROWS && c.n_pages > 0 && all_blocks < 2147483648.0;  // (blocks are TMA coordinates)
+    const int64_t shares = (max_kv + TILE - 1) / TILE;  // tiles of a unit
+    const double units16 = static_cast<double>((most + 15) / 16) * c.n_layers * q.n_seq * c.H;  // of 16 rows
+    const bool small = units16 <= num_sms && units16 * shares <= static_cast<double>(FEW_TILES) * num_sms;
+    p.tensor = dtype == KVB_BF16 && c.d >= 64 && most > MMA_ROWS && !small && c.n_pages > 0 && all_blocks < 2147483648.0;  // (blocks are TMA coordinates)
     // blocks of up to 64 rows in the tcgen05 kernel, as small as their number allows
     const int64_t few = (most + 63) / 64, each = few > 0 ? (most + few - 1) / few : 1;
     p.rows = p.tensor ? (each <= 32 ? 32 : each <= 48 ? 48 : 64) : dtype == KVB_F32 ? (most <= 4 ? 4 : 8) : most <= 8 ? 8 : most <= 16 || c.d >= 64 ? 16 : 32;
@@ -831,7 +839,6 @@ AttnPlan plan_attention(const Pages& c, const Seqs& q, kvb_dtype dtype, int g, i
     if (p.tiles > static_cast<double>(1 << 30)) return p;  // refused
     p.row_blocks = static_cast<int>(blocks);
     p.units = static_cast<int64_t>(units);
-    const int64_t shares = (max_kv + TILE - 1) / TILE;  // steps of a unit, by a CTA
     if (!p.tensor && p.units <= num_sms && shares <= FEW_SHARES * 16) {
         int most_of[5] = {};
         p.cluster = 1;

@@ -9,7 +9,9 @@ import numpy as np
 import pytest
 
 from cases import spec
+
 from test_gpu_paged import BF, F32, THETA, Pool, attend, check_attention, i32, kvb, offsets, status_of  # noqa: F401  (kvb: the fixture)
+from test_gpu_paged_long import widen
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -22,6 +24,7 @@ TIMEOUT = 7
 def test_a_limit_of_no_time_runs_out_every_time(kvb, d, g, monkeypatch):  # noqa: F811
     # every role gives up, what it holds is released, and the units' counters are left as the next call needs them
     P = Pool(kvb, 1, 2, d, 16, 3, 9000, BF)
+    widen(P)  # rows over keys that may be many: the kernel that waits
     lens = np.array([9000, 1, 700])
     P.fill(lens)
     q, one = P.rows(1, 2 * g, 3), P.rows(1, 4, 3)
@@ -112,7 +115,7 @@ def test_everything_on_the_checked_build():
     from cross_model_kv_gb300 import build
     build.build(checked=True)
     r = subprocess.run([sys.executable, "-m", "pytest", "-q", "-x", "-m", "gpu", "-p", "no:cacheprovider", "tests/test_gpu_paged.py",
-                        "tests/test_gpu_paged_paths.py", "-k", "not checked_build"],
+                        "tests/test_gpu_paged_long.py", "tests/test_gpu_paged_paths.py", "-k", "not checked_build"],
                        cwd=ROOT, env=dict(os.environ, KVB_LIBRARY="checked"), capture_output=True, text=True, timeout=900)
     if r.returncode != 0 or " passed" not in r.stdout:
         pytest.fail(r.stdout[-6000:] + r.stderr[-2000:])
