@@ -72,10 +72,11 @@ __device__ __forceinline__ RowBlock row_block(const Params& P, int s, int rb, in
     return B;
 }
 
-// Tiles of TILE keys of a unit: one at least, so that rows that see nothing are written.
-template <int TILE>
+// Tiles of TILE keys of a unit: one at least, so that rows that see nothing are written; EXTRA: in front of them,
+// those that the unit itself counts as.
+template <int TILE, int EXTRA = 0>
 __device__ __forceinline__ int unit_tiles(const RowBlock& B) {
-    return B.nrows == 0 ? 0 : max(1, (B.kv_end + TILE - 1) / TILE);
+    return B.nrows == 0 ? 0 : EXTRA + max(1, (B.kv_end + TILE - 1) / TILE);
 }
 
 // Inclusive scan / sum over the CTA's NTHREADS threads (scratch: one value a warp).
@@ -110,11 +111,11 @@ struct LineStart {
 // The units' tiles form one line: layer, then entry (sequence, row block), then
 // head.  This CTA takes tiles [at, stop) of it, the first of them tile `first` of unit
 // (l, e, h); share is every CTA's number.  false: nothing is left for this CTA.
-template <int ROWS, int TILE, int NTHREADS, class Params>
+template <int ROWS, int TILE, int NTHREADS, int EXTRA = 0, class Params>
 __device__ __forceinline__ bool line_start(const Params& P, int* scratch, LineStart* found, int& at, int& stop, int& share,
                                            int& l, int& e, int& h, int& first) {
     const int entries = P.q.n_seq * P.row_blocks;
-    auto tiles_of = [&](int i) { return unit_tiles<TILE>(row_block(P, i / P.row_blocks, i % P.row_blocks, ROWS)); };
+    auto tiles_of = [&](int i) { return unit_tiles<TILE, EXTRA>(row_block(P, i / P.row_blocks, i % P.row_blocks, ROWS)); };
     int before = 0, want;  // tiles of the entries before e, times H; and up to this CTA's first
     auto place = [&](int per_layer) {
         const int all = per_layer * P.c.n_layers;

@@ -172,10 +172,11 @@ kvb_status kvb_paged_attention(kvb_ctx* c, const kvb_paged_cache* cache, const k
         constexpr double most = 1 << 30;
         if (static_cast<double>(p.units) > most || p.tiles > most || static_cast<double>(a.q.max_tokens) * a.g > most)
             return fail(KVB_ERR_UNSUPPORTED, "kvb_paged_attention: more query rows, sequences, layers or keys than one call takes (2^30 tiles of 64 keys)");
-        if (!p.cluster && (st = c8::ensure_attn_ws(c, p.counter_bytes, p.partial_bytes, what, s)) != KVB_OK) return st;
+        if (!p.cluster && (st = c8::ensure_attn_ws(c, p.counter_bytes, p.partial_bytes + p.shared_bytes, what, s)) != KVB_OK) return st;
         a.counters = static_cast<int*>(c->attn_counters);
         a.partial = static_cast<float*>(c->attn_parts);
         a.part_stat = reinterpret_cast<float2*>(a.partial + static_cast<size_t>(p.slots) * p.rows * c->d);
+        a.shared = reinterpret_cast<int4*>(static_cast<char*>(c->attn_parts) + p.partial_bytes);
         a.units = p.units;
         a.slots = p.slots;
         a.row_blocks = p.row_blocks;

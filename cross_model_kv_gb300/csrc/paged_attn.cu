@@ -33,11 +33,11 @@ constexpr int MIN_TILES = 2;          // 1 and 4 measure the same within 2 %
 // bf16 rows up to which mma.sync keeps up (d 64, 128).  16 rows, here / on tcgen05: 14.2 / 23.5 us for one
 // sequence of 4096 keys, 8 heads, 58.0 / 59.1 for 16 of 1024 to 8192; 24 rows, 16 of 8192: 126 / 92.
 constexpr int MMA_ROWS = 16;
-// Tiles an SM, of 16 rows each, up to which clusters take more rows, if all are resident at once: the tcgen05 kernel joins
-// many pieces of few units slowly.  8 heads, clusters / tcgen05: 40 rows of one sequence of 300, 4096, 8192 keys 10.7,
-// 18.2, 26.9 / 16.6, 34.9, 37.1 us, four of 1024 16.8 / 18.9, of 2048 (36 tiles an SM, which tcgen05 takes) 22.3 / 21.0;
-// 128 rows of one of 4096 27.1 / 24.1.
-constexpr int FEW_TILES = 24;
+// More rows stay here, in blocks of 16, where keys are few: up to FEW_TILES tiles of a row block an SM, and up to 128 rows over
+// SHORT_KEYS / d tiles.  8 heads of 128, here / tcgen05, 40 rows: one sequence of 300, 4096, 8192 keys 10.5, 18.1, 26.5 /
+// 15.6, 19.2, 21.9 us, four of 1024, 2048 16.8, 22.4 / 18.5, 20.4; 64 of up to 250, 500, 2000 26, 34, 87 / 39, 45, 70; of 500
+// each 65 / 56.  20 rows of d 64: 64 of up to 1000 24 / 39.
+constexpr int FEW_TILES = 16, SHORT_KEYS = 1024;
 // A CTA for each unit, if there are more of them than SMs and they are short: up to SHORT tiles, or so many units
 // a tile that the last ones to finish do not count.  Against the line, 8 rows of d 128: 256 sequences of up to
 // 300 keys, 8 heads, 40 us and 54, 128 of up to 1000 50 and 64, 256 of up to 4000 327 and 344; but 64 of up to 8192 202
@@ -828,14 +828,14 @@ AttnPlan plan_attention(const Pages& c, const Seqs& q, kvb_dtype dtype, int g, i
     const double all_blocks = (static_cast<double>(c.l_begin) + c.n_layers) * c.n_pages * c.H;
     const int64_t shares = (max_kv + TILE - 1) / TILE;  // tiles of a unit
     const double units16 = static_cast<double>((most + 15) / 16) * c.n_layers * q.n_seq * c.H;  // of 16 rows
-    const bool small = units16 <= num_sms && units16 * shares <= static_cast<double>(FEW_TILES) * num_sms;
+    const bool small = units16 * shares <= static_cast<double>(FEW_TILES) * num_sms || (most <= 128 && shares * c.d <= SHORT_KEYS);
     p.tensor = dtype == KVB_BF16 && c.d >= 64 && most > MMA_ROWS && !small && c.n_pages > 0 && all_blocks < 2147483648.0;  // (blocks are TMA coordinates)
     // blocks of up to 64 rows in the tcgen05 kernel, as small as their number allows
     const int64_t few = (most + 63) / 64, each = few > 0 ? (most + few - 1) / few : 1;
     p.rows = p.tensor ? (each <= 32 ? 32 : each <= 48 ? 48 : 64) : dtype == KVB_F32 ? (most <= 4 ? 4 : 8) : most <= 8 ? 8 : most <= 16 || c.d >= 64 ? 16 : 32;
     const double blocks = static_cast<double>((most + p.rows - 1) / p.rows);
     const double units = blocks * c.n_layers * q.n_seq * c.H;
-    p.tiles = units * ((max_kv + TILE - 1) / TILE);  // of 64 keys; the tcgen05 kernel's have 128
+    p.tiles = units * (shares + (p.tensor ? unit_tiles_of(p.rows) : 0));  // of 64 keys; the tcgen05 kernel's have 128
     if (p.tiles > static_cast<double>(1 << 30)) return p;  // refused
     p.row_blocks = static_cast<int>(blocks);
     p.units = static_cast<int64_t>(units);
@@ -859,12 +859,13 @@ AttnPlan plan_attention(const Pages& c, const Seqs& q, kvb_dtype dtype, int g, i
     if (!p.tensor) pick(dtype, c.d, p, nullptr, nullptr, &fit);
     // the CTAs that fit the GPU, no more than the keys give the least share to
     p.min_tiles = p.tensor ? 1 : MIN_TILES;
-    const double need = p.tensor ? units * ((max_kv + 127) / 128) : (p.tiles + p.min_tiles - 1) / p.min_tiles;
+    const double need = p.tensor ? units * ((max_kv + 127) / 128 + unit_tiles_of(p.rows)) : (p.tiles + p.min_tiles - 1) / p.min_tiles;
     p.ctas = even_share(p.units, num_sms * (fit > 0 ? fit : 1), p.tensor);
     if (need < p.ctas) p.ctas = static_cast<int>(need) < 1 ? 1 : static_cast<int>(need);
     p.slots = 2 * static_cast<int64_t>(p.ctas);
-    p.counter_bytes = (static_cast<size_t>(p.units) * sizeof(int) + 255) / 256 * 256;
-    p.partial_bytes = static_cast<size_t>(p.slots) * p.rows * (c.d + 2) * sizeof(float);
+    p.counter_bytes = p.tensor ? 0 : (static_cast<size_t>(p.units) * sizeof(int) + 255) / 256 * 256;
+    p.partial_bytes = static_cast<size_t>(p.slots) * p.rows * (c.d + 2) * sizeof(float);  // slots are even: a multiple of 16
+    p.shared_bytes = p.tensor ? static_cast<size_t>(p.ctas) * 2 * sizeof(int4) : 0;
     return p;
 }
 

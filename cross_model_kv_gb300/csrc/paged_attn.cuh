@@ -92,12 +92,12 @@ __device__ __forceinline__ void write_row(const AttnParams& P, int l, RowPlace a
 
 // After a piece of a unit is written: the last CTA of the unit to arrive joins the pieces, in
 // order.  All pieces' statistics go to shared memory (`buf`, `cap` floats, free) and become their weights,
-// then each thread adds its columns, with the loads of each part in flight together.
-// meet(): the NT threads, numbered from 0 by tid, meet.
-template <typename T, int D, int ROWS, int NT, class Meet>
+// then each of the NT threads adds its columns, with the loads of each part in flight together.
+template <typename T, int D, int ROWS, int NT>
 __device__ __forceinline__ void join_pieces(const AttnParams& P, const RowBlock& B, const Pieces& pieces, int64_t unit, int l, int h,
-                                            int* s_last, float* buf, int cap, int tid, Meet meet) {
-    meet();
+                                            int* s_last, float* buf, int cap) {
+    const int tid = threadIdx.x;
+    __syncthreads();
     if (tid == 0) {  // its fences, with the barriers, order what all threads wrote and will read
         *s_last = false;
         __threadfence();
@@ -108,7 +108,7 @@ __device__ __forceinline__ void join_pieces(const AttnParams& P, const RowBlock&
         }
         __threadfence();
     }
-    meet();
+    __syncthreads();
     if (!*s_last) return;
     const int n = pieces.n, lane = tid & 31;
     float2* whole = reinterpret_cast<float2*>(buf);              // [ROWS] reference, 1 / sum
@@ -130,7 +130,7 @@ __device__ __forceinline__ void join_pieces(const AttnParams& P, const RowBlock&
     if (listed) {
 #pragma unroll 4
         for (int i = tid; i < B.nrows * n; i += NT) part[i] = stat(i / n, i % n);
-        meet();
+        __syncthreads();
     }
     if (listed && n <= 8) {  // a thread a row
         for (int row = tid; row < B.nrows; row += NT) {
@@ -167,7 +167,7 @@ __device__ __forceinline__ void join_pieces(const AttnParams& P, const RowBlock&
                 for (int i = lane; i < n; i += 32) part[row * n + i].x *= by;
         }
     }
-    meet();
+    __syncthreads();
     // a thread's items side by side, AT_ONCE loads and more in flight: one after another they took 1000
     // cycles each
     constexpr int AT_ONCE = 8;

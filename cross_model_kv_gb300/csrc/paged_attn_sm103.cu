@@ -11,23 +11,23 @@
 // (Query rows as M, 128 of them whatever their number, 64 keys a tile: 122 us for 16 sequences of
 // 8192 keys, 8 heads, 32 rows each, 1860 cycles a tile, of which HBM takes 1400; the products' warps
 // took 900 to 1000 cycles to issue eight of 128 x 64 x 16 or 128 x 128 x 16.)
-//   warps 0..3, 4..7  softmax of every other piece of a unit (64 rows: one set, of every piece), a key a thread: scores from TMEM to
-//               registers, the weights of its key to shared memory, every row's sum in registers until the
+//   warps 0..3, 4..7  softmax of every other piece of a unit (64 rows: one set, of every piece), a key a
+//               thread: scores from TMEM to registers, the weights of its key to shared memory, every row's sum in registers until the
 //               piece ends.  No thread knows a row's maximum: they vote whether some score passes its
-//               reference by 2^8, and only then reduce, and rescale O in TMEM.  They load the rows, write
-//               the outputs and join the pieces of shared units, 10000 cycles and more for each piece,
-//               while the other four warps are in the next one;
+//               reference by 2^8, and only then reduce, and rescale O in TMEM.  They load the rows and write
+//               the outputs while the other four warps are in the next piece;
 //   warp 8      page numbers, and TMA loads of K and V into rings of tiles, 128-byte swizzle, key
 //               rows: K-major for S, MN-major for O, as they lie in the pages;
 //   warp 9      one lane issues S^T = K Q^T;
 //   warp 10     and O^T += V^T P^T.
 // At head_dim 64 O^T has 64 rows and M is 128 all the same: the upper 64 are the lower ones again.
 // TMEM: score buffer b at 64 b, O's high part at 128 (and 256, odd pieces), its low part NR columns on.
-// HBM bounds it.  Every role finds the CTA's pieces by itself, so that the rings are filled while the
-// softmax goes from one unit to the next.
-// Every wait is bounded; after one gives up, the softmax still arrives at the units that it shares,
-// so that their counters are left as the next call needs them, the loads and products that
-// were issued are waited for, and TMEM is freed.
+// HBM bounds it where keys are many (16 sequences of 1024 to 8192 keys, 8 heads, 40 rows: 63 us, 0.66 of the copy rate; of
+// 8192 each 97 us, 0.82); a unit's chain of hand-overs, 5 to 12 us of which two units overlap, where they are few.
+// Every role finds the CTA's pieces by itself, so that the rings are filled while the softmax goes from one
+// unit to the next.  A second kernel joins the units that several CTAs share.
+// Every wait is bounded; after one gives up, the loads and products that were issued are waited for, TMEM is
+// freed, and what the call still writes is marked as wrong by its status.
 #include "kvb_host.h"
 #include "paged_attn.cuh"
 
@@ -39,7 +39,7 @@ namespace {
 constexpr int TK = 128;          // keys of a tile, TMEM lanes
 constexpr int SOFT = 128;        // threads of the softmax of a piece
 // Two sets of softmax warps where their registers suffice: 64 rows take more than 200 a thread (16 x 8192 keys:
-// 99 us with one set, 121 with two).
+// 99 us with one set, 121 with two; 40 rows, 16 x 1024..8192 keys: 73 and 63.5).
 constexpr int sets_of(int NR) { return NR <= 48 ? 2 : 1; }
 constexpr int threads_of(int NR) { return sets_of(NR) * SOFT + 128; }  // the last warp only makes up a warpgroup
 // Registers a thread: 168 at launch, then by role.  256 * 192 + 128 * 96 = 61440 of the launch's 384 * 168 = 64512.
@@ -58,7 +58,6 @@ struct Rows {
     int pos[64];                     // positions of the rows
     int odd;                         // values that are not finite have been taken out of the products
     int64_t to[64];                  // element of P.out that their outputs begin at
-    int last;
 };
 struct Smem {
     uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
@@ -91,7 +90,7 @@ struct Segment {
     RowBlock B;
     int s, l, h;
     int k0, k1;  // keys [k0, k1)
-    int64_t unit, slot;
+    int64_t slot;
     Pieces pieces;
     __device__ __forceinline__ int tiles() const { return (k1 - k0 + TK - 1) / TK; }
 };
@@ -99,48 +98,51 @@ struct Segment {
 // The CTA's place in the line of tiles.
 template <int NR>
 struct Walk {
+    static constexpr int UNIT_TILES = unit_tiles_of(NR);
     int at, stop, share, l, e, h, first;
     RowBlock B;
-    int tiles;  // of unit (l, e, h); 0 before the first
+    int tiles;  // of unit (l, e, h), UNIT_TILES without keys first; 0 before the first
 
     __device__ __forceinline__ RowBlock entry(const AttnParams& P) const {
         return c8::row_block(P, e / P.row_blocks, e % P.row_blocks, NR);
     }
-    // The next piece, if there is one.
+    // The next piece with keys, if there is one.
     __device__ __forceinline__ bool next(const AttnParams& P, Segment& g) {
-        if (at >= stop) return false;
         const int entries = P.q.n_seq * P.row_blocks;
-        if (tiles == 0) {
-            B = entry(P);
-            tiles = c8::unit_tiles<TK>(B);
-            if (tiles == 0) return false;  // not reached while the call's arrays stay as they are, here and below
-        } else {
-            first = 0;
-            if (++h == P.c.H) {
-                h = 0;
-                do {
-                    if (++e == entries) {
-                        e = 0;
-                        if (++l == P.c.n_layers) return false;
-                    }
-                    B = entry(P);
-                    tiles = c8::unit_tiles<TK>(B);
-                } while (tiles == 0);
+        for (;;) {
+            if (at >= stop) return false;
+            if (tiles == 0) {
+                B = entry(P);
+                tiles = c8::unit_tiles<TK, UNIT_TILES>(B);
+                if (tiles == 0) return false;  // not reached while the call's arrays stay as they are, here and below
+            } else {
+                first = 0;
+                if (++h == P.c.H) {
+                    h = 0;
+                    do {
+                        if (++e == entries) {
+                            e = 0;
+                            if (++l == P.c.n_layers) return false;
+                        }
+                        B = entry(P);
+                        tiles = c8::unit_tiles<TK, UNIT_TILES>(B);
+                    } while (tiles == 0);
+                }
             }
+            const int last = min(tiles, first + (stop - at));
+            const int u0 = at - first, c0 = (u0 + UNIT_TILES) / share;  // the CTA of its first keys
+            at += last - first;
+            if (last <= UNIT_TILES) continue;
+            g.B = B;
+            g.s = e / P.row_blocks;
+            g.l = l;
+            g.h = h;
+            g.k0 = max(first - UNIT_TILES, 0) * TK;
+            g.k1 = max(g.k0, min(B.kv_end, (last - UNIT_TILES) * TK));
+            g.pieces = Pieces{(u0 + tiles - 1) / share - c0 + 1, c0};
+            g.slot = 2 * static_cast<int64_t>(blockIdx.x) + (first <= UNIT_TILES);
+            return true;
         }
-        const int last = min(tiles, first + (stop - at));
-        const int u0 = at - first, c0 = u0 / share;
-        g.B = B;
-        g.s = e / P.row_blocks;
-        g.l = l;
-        g.h = h;
-        g.k0 = first * TK;
-        g.k1 = max(g.k0, min(B.kv_end, last * TK));
-        g.unit = (static_cast<int64_t>(l) * entries + e) * P.c.H + h;
-        g.pieces = Pieces{(u0 + tiles - 1) / share - c0 + 1, c0};
-        g.slot = 2 * static_cast<int64_t>(blockIdx.x) + (first == 0);
-        at += last - first;
-        return true;
     }
 };
 
@@ -177,7 +179,9 @@ __global__ void __launch_bounds__(threads_of(NR), 1) rows_kernel(const __grid_co
 
     Walk<NR> W;
     W.tiles = 0;
-    if (!c8::line_start<NR, TK, NUM_THREADS>(P, M.scan, &M.start, W.at, W.stop, W.share, W.l, W.e, W.h, W.first)) return;
+    if (threadIdx.x == 0 && KVB_IN_BOUNDS(P.err, 2 * static_cast<int64_t>(blockIdx.x), 1, P.slots))
+        P.shared[2 * blockIdx.x] = make_int4(0, 0, 0, 0);  // (until it is known, after a barrier)
+    if (!c8::line_start<NR, TK, NUM_THREADS, Walk<NR>::UNIT_TILES>(P, M.scan, &M.start, W.at, W.stop, W.share, W.l, W.e, W.h, W.first)) return;
     if (threadIdx.x == 0) {
         for (int i = 0; i < STAGES; ++i) {
             mbar_init(&M.k_full[i], 1);
@@ -448,9 +452,10 @@ __global__ void __launch_bounds__(threads_of(NR), 1) rows_kernel(const __grid_co
                 }
             }
             tc_fence_before();
-            if (!alone)
-                join_pieces<__nv_bfloat16, HD, NR, SOFT>(P, G.B, G.pieces, G.unit, G.l, G.h, &N.last, reinterpret_cast<float*>(myQ), L::Q / 4,
-                                                         key, [&] { named_bar_sync(id, SOFT); });
+            if (key == 0 && !alone && G.k0 == 0 && KVB_IN_BOUNDS(P.err, G.slot, 1, P.slots)) {  // at most one of a CTA's pieces
+                P.shared[2 * blockIdx.x + 1] = make_int4(G.l, G.h, 0, 0);
+                P.shared[2 * blockIdx.x] = make_int4(G.pieces.n, G.B.nrows, G.B.row0, G.B.tok0);
+            }
         }
     } else if (warp == 4 * SETS) {
         // ------------------------------------------------------- pages and loads
@@ -593,6 +598,29 @@ __global__ void __launch_bounds__(threads_of(NR), 1) rows_kernel(const __grid_co
     if (threadIdx.x == 0 && *abort_flag) *reinterpret_cast<volatile int*>(P.err.mirror) = DEV_ERR_TIMEOUT;
 }
 
+// The units that several CTAs share, in the order of their pieces: a thread takes four columns of a row.  A kernel of
+// its own: the last CTA to arrive took 1 us for each piece of a unit, and 8 to 19 pieces where there are few units.
+constexpr int JOIN_THREADS = 256;
+template <int HD, int NR>
+__global__ void __launch_bounds__(JOIN_THREADS) join_rows_kernel(const __grid_constant__ AttnParams P) {
+    const int4 who = P.shared[2 * blockIdx.x], where = P.shared[2 * blockIdx.x + 1];
+    const int row = (blockIdx.y * JOIN_THREADS + threadIdx.x) / (HD / 4), d4 = threadIdx.x % (HD / 4);
+    const Pieces pieces{who.x, static_cast<int>(blockIdx.x)};
+    if (row >= who.y || pieces.n < 2 || !c8::pieces_in_bounds(P, pieces)) return;
+    Joined z;
+#pragma unroll 8
+    for (int i = 0; i < pieces.n; ++i) z.reference(P.part_stat[pieces.slot(i) * NR + row]);
+#pragma unroll 8
+    for (int i = 0; i < pieces.n; ++i) {
+        const int64_t at = pieces.slot(i) * NR + row;
+        z.add(P.part_stat[at], reinterpret_cast<const float4*>(P.partial)[at * (HD / 4) + d4]);
+    }
+    RowBlock B{};
+    B.row0 = who.z;
+    B.tok0 = who.w;
+    write_row<__nv_bfloat16>(P, where.x, place_of(P, B, where.y, row), d4, z);
+}
+
 template <int HD, int NR>
 cudaError_t launch(const AttnParams& P, const AttnPlan& p, cudaStream_t s, std::string* why) {
     EncodeTiledFn enc = get_encode_tiled();
@@ -618,6 +646,7 @@ cudaError_t launch(const AttnParams& P, const AttnPlan& p, cudaStream_t s, std::
     cudaError_t e = cudaFuncSetAttribute(rows_kernel<HD, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<HD, NR>::BYTES);
     if (e != cudaSuccess) return e;
     rows_kernel<HD, NR><<<p.ctas, threads_of(NR), Layout<HD, NR>::BYTES, s>>>(maps, P);
+    join_rows_kernel<HD, NR><<<dim3(static_cast<unsigned>(p.ctas), NR * (HD / 4) / JOIN_THREADS), JOIN_THREADS, 0, s>>>(P);
     return cudaGetLastError();
 }
 
