@@ -16,9 +16,10 @@
 //                  as a bf16 pair (hi, lo): 16 bits of a weight, for twice the products.
 // fp32: CUDA cores, two products an instruction (f32x2).
 //
-// The keys of all units (layer, sequence, row block, head) form one line of 64-key tiles that the
-// CTAs which fit the GPU share evenly; the last CTA to arrive at a unit that several share joins
-// its pieces in order, so results do not depend on timing.
+// Three ways to cut a call: the keys of all units (layer, sequence, row block, head) form one line of
+// 64-key tiles that the CTAs which fit the GPU share evenly, and the last CTA to arrive at a unit that
+// several share joins its pieces in order; a cluster takes a unit, where units are few and short; a CTA
+// takes a unit, where they are many and short.  Results do not depend on timing.
 #include "paged_attn.cuh"
 
 namespace kvb {
@@ -624,8 +625,7 @@ __global__ void __launch_bounds__(32 * WARPS) line_kernel(const __grid_constant_
             }
         }
         if (pieces > 1)
-            join_pieces<T, D, ROWS, NT>(P, B, Pieces{pieces, c0}, unit, l, h, &s_last, reinterpret_cast<float*>(smem), S::MORE / 4,
-                                        threadIdx.x, [] { __syncthreads(); });
+            join_pieces<T, D, ROWS, NT>(P, B, Pieces{pieces, c0}, unit, l, h, &s_last, reinterpret_cast<float*>(smem), S::MORE / 4);
 
         at += last - first;
         if (at >= stop) return;
@@ -809,7 +809,7 @@ cudaError_t pick(kvb_dtype dtype, int d, const AttnPlan& p, const AttnParams* P,
 }
 
 // CTAs, at most `most`: where units of one length leave no CTA with parts of two, and not too few CTAs
-// with the others' keys too, that many.  With 304 CTAs of this file's kernel, 16 x 8192 / 16 x 32768 keys of one length
+// with the others' keys too, that many.  With two CTAs an SM of this file's kernel, 16 x 8192 / 16 x 32768 keys of one length
 // take 86 / 310 us so and 90 / 321 on all of them, unequal ones (16 x 1024 .. 8192) 54 either way; more
 // units than CTAs, unequal ones, 186 and 184.  The tcgen05 kernel
 // has 152 and longer ways from one unit to the next: 128 of them 86 and 152 93 us, but unequal lengths 94 and 78.
