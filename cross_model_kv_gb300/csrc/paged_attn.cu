@@ -41,8 +41,8 @@ constexpr int MMA_ROWS = 16;
 constexpr int FEW_TILES = 16, SHORT_KEYS = 1024;
 // A CTA for each unit, if there are more of them than SMs and they are short: up to SHORT tiles, or so many units
 // a tile that the last ones to finish do not count.  Against the line, 8 rows of d 128: 256 sequences of up to
-// 300 keys, 8 heads, 40 us and 54, 128 of up to 1000 50 and 64, 256 of up to 4000 327 and 344; but 64 of up to 8192 202
-// and 181, and 64 of 1000 each 53 and 48 (512 units on 608 places).
+// 300 keys, 8 heads, 35 us and 54, 128 of up to 1000 50 and 64, 64 of 1000 each 42 and 48, 256 of up to 4000 327 and 344;
+// but 64 of up to 8192 202 and 181.
 constexpr int SHORT = 16;
 // Steps of a warp up to which a cluster takes a unit where there are no more units than SMs.  One row block of 8,
 // 8 heads, cluster / line: 4096 keys 10 / 14 us, 32768 34 / 41; 8 sequences of 8192 45 / 53, 16 of 1024 to 8192
@@ -67,7 +67,9 @@ struct Ring {
     static constexpr int CH = D * sizeof(T) / 16;       // 16-byte chunks of a row
     static constexpr int PART = STEP * D * sizeof(T);   // bytes
     // Four warps' rings fit an SM four times in bf16, twice in fp32.  Twice in bf16, 6 parts of d 128: 16 x 32768 keys
-    // 313 us against 303, 64 x 1024..8192 185 against 181, one sequence of 32768 31.6 against 34.3.
+    // 313 us against 303, 64 x 1024..8192 185 against 181, one sequence of 32768 31.6 against 34.3.  Registers for four
+    // CTAs, 128 a thread, where they suffice (8 rows; three CTAs with 164): 16 x 8192 keys 82 against 86 us, 64 of 1000
+    // 42 against 53, 128 of up to 4000 176 against 173.
     static constexpr int FIT = (sizeof(T) == 2 ? 12288 : 24576) / PART;
     static constexpr int DEPTH = FIT > 16 ? 16 : FIT;   // d 128: 3 parts
     static constexpr int BYTES = DEPTH * PART;
@@ -589,7 +591,7 @@ __device__ __forceinline__ Joined join_warps(const uint8_t* smem, int row, int d
 
 // Many keys: the line of tiles, shared evenly by the CTAs that fit the GPU.
 template <typename T, int D, int NB>
-__global__ void __launch_bounds__(32 * WARPS) line_kernel(const __grid_constant__ AttnParams P) {
+__global__ void __launch_bounds__(32 * WARPS, sizeof(T) == 2 && NB == 1 ? 4 : 1) line_kernel(const __grid_constant__ AttnParams P) {
     constexpr int NT = 32 * WARPS;
     using S = Shared<T, D, NB, WARPS>;
     constexpr int ROWS = S::ROWS;
@@ -664,7 +666,7 @@ __device__ __forceinline__ void hand2(uint32_t p, float2 v) {
 // the others its part of the columns that the other joins, through distributed shared memory: no
 // global scratch, no atomics.  And many short units: a CTA for each, which waits for no other.
 template <typename T, int D, int NB>
-__global__ void __launch_bounds__(32 * WARPS) cluster_kernel(const __grid_constant__ AttnParams P) {
+__global__ void __launch_bounds__(32 * WARPS, sizeof(T) == 2 && NB == 1 ? 4 : 1) cluster_kernel(const __grid_constant__ AttnParams P) {
     constexpr int NT = 32 * WARPS;
     using S = Shared<T, D, NB, WARPS>;
     constexpr int ROWS = S::ROWS;
