@@ -157,6 +157,7 @@ kvb_status kvb_paged_attention(kvb_ctx* c, const kvb_paged_cache* cache, const k
         if (c8::empty_call(a.q, n_layers)) return KVB_OK;
         if ((st = check_rows(q, "q", what, n_layers, n_q_heads, T, c->d, cache->dtype, false, &a.query)) != KVB_OK) return st;
         if ((st = check_rows(out, "out", what, n_layers, n_q_heads, T, c->d, cache->dtype, true, &a.out)) != KVB_OK) return st;
+        if (out->data == q->data) return fail(KVB_ERR_INVALID_ARG, "kvb_paged_attention: out in the place of q");
         if (reinterpret_cast<uintptr_t>(lse) & 3u)
             return fail(KVB_ERR_INVALID_ARG, "kvb_paged_attention: lse not 4-byte aligned");
         DeviceGuard g(c->device);

@@ -92,7 +92,9 @@ struct Segment {
     int k0, k1;  // keys [k0, k1)
     int64_t slot;
     Pieces pieces;
-    __device__ __forceinline__ int tiles() const { return (k1 - k0 + TK - 1) / TK; }
+    // One at least: of a unit without keys a tile that nothing sees.  Every piece passes every barrier of the
+    // roles then, so that none gets two phases ahead of a wait.
+    __device__ __forceinline__ int tiles() const { return max(1, (k1 - k0 + TK - 1) / TK); }
 };
 
 // The CTA's place in the line of tiles.
@@ -373,8 +375,7 @@ __global__ void __launch_bounds__(threads_of(NR), 1) rows_kernel(const __grid_co
             if (SETS == 2) mbar_arrive(&M.handed[half]);
             // (a barrier of its own: those of the tiles go on with the next piece)
             ok = ok && wait_all(&M.o_full[half], (piece / SETS) & 1);
-            const bool have = ok && ntiles > 0;
-            if (have) tc_fence_after();
+            if (ok) tc_fence_after();
             // the rows' sums, and where their outputs go
 #pragma unroll
             for (int n0 = 0; n0 < NR; n0 += 16) {  // 16 rows: a lane keeps half of them at each exchange
@@ -396,7 +397,7 @@ __global__ void __launch_bounds__(threads_of(NR), 1) rows_kernel(const __grid_co
             const int64_t part0 = G.slot * NR;
             if (key < NR && key >= G.B.nrows) N.to[key] = -1;
             if (key < G.B.nrows) {
-                const float total = have ? (N.part[0][key] + N.part[1][key]) + (N.part[2][key] + N.part[3][key]) : 0.f, m = N.ref[key];
+                const float total = ok ? (N.part[0][key] + N.part[1][key]) + (N.part[2][key] + N.part[3][key]) : 0.f, m = N.ref[key];
                 const RowPlace at = place_of(P, G.B, G.h, key);
                 const int64_t lse_row = (static_cast<int64_t>(G.l) * P.c.H * P.g + at.head) * P.q.T + at.token;
                 const bool inside = KVB_IN_BOUNDS(P.err, lse_row, 1, c8::rows_of(P)) && KVB_IN_BOUNDS(P.err, G.slot, 1, P.slots);
@@ -410,7 +411,7 @@ __global__ void __launch_bounds__(threads_of(NR), 1) rows_kernel(const __grid_co
 #pragma unroll 1
                 for (int c = 0; c < G.B.nrows; c += 16) {
                     uint32_t hi[16], lo[16];
-                    if (have) {
+                    if (ok) {
                         tmem_ld16(tO + c, hi);
                         tmem_ld16(tO + NR + c, lo);
                         tmem_ld_wait();
@@ -421,7 +422,7 @@ __global__ void __launch_bounds__(threads_of(NR), 1) rows_kernel(const __grid_co
                     float o[16];
 #pragma unroll
                     for (int n = 0; n < 16; ++n) o[n] = __uint_as_float(hi[n]) + __uint_as_float(lo[n]);
-                    if (have && N.odd) {
+                    if (ok && N.odd) {
 #pragma unroll 1
                         for (int j = max(G.k0, G.B.pos_lo + 1); j < G.k1; ++j) {
                             const float v = value_of<__nv_bfloat16>(P, G.s, G.l, G.h, j, key);
@@ -536,7 +537,7 @@ __global__ void __launch_bounds__(threads_of(NR), 1) rows_kernel(const __grid_co
         const uint64_t v0 = sdesc_mn_sw128(smem_u32(sV), HD == 128 ? ATOM : 0), p0 = sdesc_mn_sw128(smem_u32(sP), ATOM);
         for (int n = 0; go && W.next(P, G); ++n) {
             const int ntiles = G.tiles();
-            if (scores && ntiles > 0) {
+            if (scores) {
                 // A limit of 0 leaves no time to wait: a timeout, whatever the wait would have found.
                 if (derr.timeout_ns == 0) {
                     dev_err_set(derr, DEV_ERR_TIMEOUT);
@@ -605,7 +606,7 @@ template <int HD, int NR>
 __global__ void __launch_bounds__(JOIN_THREADS) join_rows_kernel(const __grid_constant__ AttnParams P) {
     const int4 who = P.shared[2 * blockIdx.x], where = P.shared[2 * blockIdx.x + 1];
     const int row = (blockIdx.y * JOIN_THREADS + threadIdx.x) / (HD / 4), d4 = threadIdx.x % (HD / 4);
-    const Pieces pieces{who.x, static_cast<int>(blockIdx.x)};
+    const Pieces pieces{min(who.x, static_cast<int>(gridDim.x - blockIdx.x)), static_cast<int>(blockIdx.x)};
     if (row >= who.y || pieces.n < 2 || !c8::pieces_in_bounds(P, pieces)) return;
     Joined z;
 #pragma unroll 8

@@ -488,8 +488,9 @@ kvb_status kvb_cache8_append(kvb_ctx* ctx, const kvb_cache8* cache, const kvb_se
 
 /*
  * Attention of new tokens over the cache: for one token a sequence, or the few of a
- * draft that is checked (any number is right; keys are read once for up to 64 query rows,
- * a head's tokens times n_q_heads / H, of bf16, 32 where d is below 64, and for 8 of fp32):
+ * draft that is checked (any number is right; a head's query rows are its tokens times
+ * n_q_heads / H, and keys are read once for up to 64 of them in bf16, 16 where keys are few,
+ * 32 where d is below 64, and for 8 in fp32):
  *     out_i = sum over visible j of softmax_j(scale * q_i . k_j) v_j,
  *     lse_i = log sum over visible j of exp(scale * q_i . k_j),
  * with seqs, visibility, n_q_heads, scale and lse as for kvb_cache8_attention; q and out

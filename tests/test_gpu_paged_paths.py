@@ -109,6 +109,32 @@ def test_example_decodes_from_pages_of_the_models_type(kvb):  # noqa: F811
     assert r["cos_min"] > 0.999 and torch.isfinite(r["out"]).all()
 
 
+@pytest.mark.parametrize("d,g", [(64, 10), (128, 20), (64, 32)])
+def test_sequences_without_keys_among_others(kvb, d, g):  # noqa: F811
+    # several units of a CTA, of which some see nothing: the next one's rows are still its own
+    n = 300
+    P = Pool(kvb, 1, 2, d, 16, n, 100, BF)
+    widen(P)
+    P.fill([100] * n)
+    q = P.rows(1, 2 * g, 2 * n)
+    off, pos = offsets([2] * n), P.rng.integers(0, 98, n)
+    for empty in (2, 3, 1):
+        lens = np.where(np.arange(n) % 4 < empty, 0, P.rng.integers(1, 100, n))
+        out, lse = attend(P, q, off, pos, kv_len=i32(lens))
+        kvb.kvb_ctx_check(P.ctx)
+        check_attention(P, q, off, pos, out, lse, kv_len=lens)
+        for _ in range(5):
+            again, z = attend(P, q, off, pos, kv_len=i32(lens))
+            assert torch.equal(out, again) and torch.equal(lse, z)
+
+
+def test_outputs_in_the_place_of_the_queries_are_refused(kvb):  # noqa: F811
+    P = Pool(kvb, 1, 1, 64, 16, 1, 20, BF)
+    P.fill([20])
+    q = P.rows(1, 2, 1)
+    assert status_of(kvb, lambda: kvb.kvb_paged_attention(P.ctx, P.cache, P.seqs([0, 1], [19]), q, q)) == 1
+
+
 def test_everything_on_the_checked_build():
     if not torch.cuda.is_available():
         pytest.skip("no CUDA device")
