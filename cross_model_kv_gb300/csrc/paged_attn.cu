@@ -32,6 +32,9 @@ namespace {
 constexpr int WARPS = 4;              // of a CTA
 constexpr int STEP = 16;              // keys of a warp's step
 constexpr int TILE = STEP * WARPS;    // a tile
+// Tiles that a unit itself counts as in the line.  0 / 4: 64 sequences of up to 4000 keys, 16 rows, 108 / 99 us, 24 of up to 2000, 8
+// rows, 24.9 / 23.4; 16 of 8192 each 81 either way.
+constexpr int LINE_UNIT_TILES = 4;
 constexpr int MIN_TILES = 2;          // 1 and 4 measure the same within 2 %
 // bf16 rows up to which mma.sync keeps up (d 64, 128).  16 rows, here / on tcgen05: 14.2 / 23.5 us for one
 // sequence of 4096 keys, 8 heads, 58.0 / 59.1 for 16 of 1024 to 8192; 24 rows, 16 of 8192: 126 / 92.
@@ -41,6 +44,9 @@ constexpr int MMA_ROWS = 16;
 // 15.6, 19.2, 21.9 us, four of 1024, 2048 16.8, 22.4 / 18.5, 20.4; 64 of up to 250, 500, 2000 26, 34, 87 / 39, 45, 70; of 500
 // each 65 / 56.  20 rows of d 64: 64 of up to 1000 24 / 39.
 constexpr int FEW_TILES = 16, SHORT_KEYS = 1024;
+// Two CTAs an SM where more would cut a unit into more pieces than this, all of which one CTA joins: 8 units of 35000, 131072 keys
+// 36, 90 us with two and 42, 99 with four; 16 units of 35000 53 and 58.
+constexpr int MOST_PIECES = 36;
 // A CTA for each unit, if there are more of them than SMs and they are short: up to SHORT tiles, or so many units
 // a tile that the last ones to finish do not count.  Against the line, 8 rows of d 128: 256 sequences of up to
 // 300 keys, 8 heads, 35 us and 54, 128 of up to 1000 50 and 64, 64 of 1000 each 42 and 48, 256 of up to 4000 327 and 344;
@@ -603,33 +609,36 @@ __global__ void __launch_bounds__(32 * WARPS, sizeof(T) == 2 && NB == 1 ? 4 : 1)
     __shared__ int s_scan[WARPS];
 
     int at, stop, share, l, e, h, first;
-    if (!c8::line_start<ROWS, TILE, NT>(P, s_scan, &s_start, at, stop, share, l, e, h, first)) return;
+    if (!c8::line_start<ROWS, TILE, NT, LINE_UNIT_TILES>(P, s_scan, &s_start, at, stop, share, l, e, h, first)) return;
     const int entries = P.q.n_seq * P.row_blocks;
     auto entry = [&](int x) { return c8::row_block(P, x / P.row_blocks, x % P.row_blocks, ROWS); };
     RowBlock B = entry(e);
-    int tiles = c8::unit_tiles<TILE>(B);
+    int tiles = c8::unit_tiles<TILE, LINE_UNIT_TILES>(B);
 
     for (;;) {  // one unit, or a piece of one, after another
-        const int last = min(tiles, first + (stop - at));  // tiles [first, last)
-        const int64_t unit = (static_cast<int64_t>(l) * entries + e) * P.c.H + h;
-        attend<T, D, NB, WARPS>(P, B, e / P.row_blocks, l, h, first * TILE, min(B.kv_end, last * TILE), smem);
+        const int last = min(tiles, first + (stop - at));  // tiles [first, last), those without keys first
+        const int k0 = max(first - LINE_UNIT_TILES, 0) * TILE, k1 = min(B.kv_end, (last - LINE_UNIT_TILES) * TILE);
+        if (last > LINE_UNIT_TILES) {
+            const int64_t unit = (static_cast<int64_t>(l) * entries + e) * P.c.H + h;
+            attend<T, D, NB, WARPS>(P, B, e / P.row_blocks, l, h, k0, k1, smem);
 
-        // the CTAs that share this unit, and this one's slot
-        const int u0 = at - first, c0 = u0 / share;
-        const int pieces = (u0 + tiles - 1) / share - c0 + 1;
-        const int64_t part0 = (2 * static_cast<int64_t>(blockIdx.x) + (first == 0)) * ROWS;
-        for (int i = threadIdx.x; i < B.nrows * (D / 4); i += NT) {
-            const int row = i / (D / 4), d4 = i % (D / 4);
-            const Joined z = join_warps<T, D, NB, WARPS>(smem, row, d4);
-            if (pieces == 1) {
-                write_row<T>(P, l, place_of(P, B, h, row), d4, z);
-            } else if (KVB_IN_BOUNDS(P.err, part0 + row, 1, P.slots * ROWS)) {
-                reinterpret_cast<float4*>(P.partial + (part0 + row) * D)[d4] = z.acc;
-                if (d4 == 0) P.part_stat[part0 + row] = make_float2(z.m, z.sum);
+            // the CTAs that share this unit, and this one's slot
+            const int u0 = at - first, c0 = (u0 + LINE_UNIT_TILES) / share;
+            const int pieces = (u0 + tiles - 1) / share - c0 + 1;
+            const int64_t part0 = (2 * static_cast<int64_t>(blockIdx.x) + (first <= LINE_UNIT_TILES)) * ROWS;
+            for (int i = threadIdx.x; i < B.nrows * (D / 4); i += NT) {
+                const int row = i / (D / 4), d4 = i % (D / 4);
+                const Joined z = join_warps<T, D, NB, WARPS>(smem, row, d4);
+                if (pieces == 1) {
+                    write_row<T>(P, l, place_of(P, B, h, row), d4, z);
+                } else if (KVB_IN_BOUNDS(P.err, part0 + row, 1, P.slots * ROWS)) {
+                    reinterpret_cast<float4*>(P.partial + (part0 + row) * D)[d4] = z.acc;
+                    if (d4 == 0) P.part_stat[part0 + row] = make_float2(z.m, z.sum);
+                }
             }
+            if (pieces > 1)
+                join_pieces<T, D, ROWS, NT>(P, B, Pieces{pieces, c0}, unit, l, h, &s_last, reinterpret_cast<float*>(smem), S::MORE / 4);
         }
-        if (pieces > 1)
-            join_pieces<T, D, ROWS, NT>(P, B, Pieces{pieces, c0}, unit, l, h, &s_last, reinterpret_cast<float*>(smem), S::MORE / 4);
 
         at += last - first;
         if (at >= stop) return;
@@ -642,7 +651,7 @@ __global__ void __launch_bounds__(32 * WARPS, sizeof(T) == 2 && NB == 1 ? 4 : 1)
                     if (++l == P.c.n_layers) return;  // not reached while the call's arrays stay as they are
                 }
                 B = entry(e);
-                tiles = c8::unit_tiles<TILE>(B);
+                tiles = c8::unit_tiles<TILE, LINE_UNIT_TILES>(B);
             } while (tiles == 0);
         }
         __syncthreads();  // shared memory is free for the next unit
@@ -839,7 +848,7 @@ AttnPlan plan_attention(const Pages& c, const Seqs& q, kvb_dtype dtype, int g, i
     p.rows = p.tensor ? (each <= 32 ? 32 : each <= 48 ? 48 : 64) : dtype == KVB_F32 ? (most <= 4 ? 4 : 8) : most <= 8 ? 8 : most <= 16 || c.d >= 64 ? 16 : 32;
     const double blocks = static_cast<double>((most + p.rows - 1) / p.rows);
     const double units = blocks * c.n_layers * q.n_seq * c.H;
-    p.tiles = units * (shares + (p.tensor ? unit_tiles_of(p.rows) : 0));  // of 64 keys; the tcgen05 kernel's have 128
+    p.tiles = units * (shares + (p.tensor ? unit_tiles_of(p.rows) : LINE_UNIT_TILES));  // of 64 keys; the tcgen05 kernel's have 128
     if (p.tiles > static_cast<double>(1 << 30)) return p;  // refused
     p.row_blocks = static_cast<int>(blocks);
     p.units = static_cast<int64_t>(units);
@@ -861,6 +870,7 @@ AttnPlan plan_attention(const Pages& c, const Seqs& q, kvb_dtype dtype, int g, i
     }
     int fit = 1;
     if (!p.tensor) pick(dtype, c.d, p, nullptr, nullptr, &fit);
+    if (fit > 2 && p.units * MOST_PIECES < static_cast<int64_t>(num_sms) * fit) fit = 2;
     // the CTAs that fit the GPU, no more than the keys give the least share to
     p.min_tiles = p.tensor ? 1 : MIN_TILES;
     const double need = p.tensor ? units * ((max_kv + 127) / 128 + unit_tiles_of(p.rows)) : (p.tiles + p.min_tiles - 1) / p.min_tiles;
