@@ -4,7 +4,7 @@
 //     s_rj = scale * q_r . k_j,  p_rj = 2^(s_rj log2(e) - m_r),
 //     o_r = sum_j p_rj v_j / sum_j p_rj,  lse_r = (m_r + log2 sum_j p_rj) ln 2
 // in one pass over the keys, with a reference m_r that is raised when a score passes it by 2^8.
-// One token of 64 query heads over 8 KV heads of 128, bf16: 16 x 32768 keys 303 us (7.1 TB/s, above the copy rate), 64 of
+// One token of 64 query heads over 8 KV heads of 128, bf16: 16 x 32768 keys 299 us (7.2 TB/s, above the copy rate), 64 of
 // 1024 to 8192 181 (0.97 of it), one of 4096 9.8.
 // Every key is read once for 4 d g flops per 2 d elements (8 flop/byte at g = 8 and bf16), so HBM
 // bounds it and what counts is that enough of it is on its way: each warp has a ring of its own
@@ -870,6 +870,9 @@ AttnPlan plan_attention(const Pages& c, const Seqs& q, kvb_dtype dtype, int g, i
     }
     int fit = 1;
     if (!p.tensor) pick(dtype, c.d, p, nullptr, nullptr, &fit);
+    // three CTAs an SM at most, although four fit: 16 x 32768 keys 299 us and 305, 32 of 1024 to 16384 176 and 181, 8 x 20000
+    // 103 and 106 (64 x 8192 312 and 302)
+    if (fit > 3) fit = 3;
     if (fit > 2 && p.units * MOST_PIECES < static_cast<int64_t>(num_sms) * fit) fit = 2;
     // the CTAs that fit the GPU, no more than the keys give the least share to
     p.min_tiles = p.tensor ? 1 : MIN_TILES;
