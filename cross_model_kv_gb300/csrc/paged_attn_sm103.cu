@@ -464,6 +464,7 @@ __global__ void __launch_bounds__(threads_of(NR), 1) rows_kernel(const __grid_co
         constexpr int HALVES = HD / 64;
         const int rows = min(P.c.page, TK), per = TK / rows;  // keys of a load; loads of a tile, of 64 dims
         bool go = true;
+        uint32_t asked[2] = {0, 0};  // tiles of K, and of V, whose barrier has been armed
         while (go && W.next(P, G)) {
             const int ntiles = G.tiles();
             const int64_t block0 = (static_cast<int64_t>(P.c.l_begin) + G.l) * P.c.n_pages * P.c.H + G.h;
@@ -508,6 +509,7 @@ __global__ void __launch_bounds__(threads_of(NR), 1) rows_kernel(const __grid_co
                     uint64_t* full = kv ? &M.v_full[stage] : &M.k_full[stage];
                     if (go) go = wait_all(kv ? &M.v_empty[stage] : &M.k_empty[stage], (round & 1) ^ 1);
                     if (!go) break;
+                    asked[kv] = t + 1;
                     if (elect_one()) {
                         if (bytes) mbar_arrive_expect_tx(full, bytes);
                         else mbar_arrive(full);
@@ -519,13 +521,12 @@ __global__ void __launch_bounds__(threads_of(NR), 1) rows_kernel(const __grid_co
                 if (!go) break;
             }
         }
-        if (!go) {  // what was asked for arrives before the CTA ends (k of tile t may have been)
-            for (uint32_t u = t >= STAGES ? t - STAGES : 0; u <= t; ++u) {
-                const uint32_t stage = u % STAGES, parity = (u / STAGES) & 1;
-                mbar_wait_drain(&M.k_full[stage], parity, DRAIN_NS / 16);
-                mbar_wait_drain(&M.v_full[stage], parity, DRAIN_NS / 16);
-            }
-        }
+        // What was asked for arrives before the CTA ends, also where the other roles gave up before they looked at it
+        // and no wait of this warp did: the first STAGES tiles find their places empty.
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv)
+            for (uint32_t u = asked[kv] > STAGES ? asked[kv] - STAGES : 0; u < asked[kv]; ++u)
+                mbar_wait_drain(kv ? &M.v_full[u % STAGES] : &M.k_full[u % STAGES], (u / STAGES) & 1, DRAIN_NS);
     } else if (warp == 4 * SETS + 3) {
         if constexpr (SETS == 2) regs_down<REGS_OTHERS>();
     } else {
