@@ -464,9 +464,11 @@ typedef struct {
  *       x'_i = x_i c - x_(i+d/2) s,  x'_(i+d/2) = x_(i+d/2) c + x_i s
  * with c and s of position p from the context's fp32 table (reduced in float64).  Every
  * product and sum is rounded to fp32 by itself (no fused multiply-add) and the result
- * once to dtype, so elementary fp32 operations give the same bits.  A position outside
- * [0, max_pos) is recorded on the context (KVB_ERR_INVALID_ARG) and its rows, where they
- * have a place, are written as 0; a token without a page is recorded and not stored.
+ * once to dtype, so elementary fp32 operations give the same bits.  With rotate = 1 a
+ * position outside [0, max_pos) is recorded on the context (KVB_ERR_INVALID_ARG) and its
+ * rows, where they have a place, are written as 0; with rotate = 0 the table is not read and
+ * the page table alone bounds positions.  A token without a page (one below position 0
+ * among them) is recorded and not stored.
  * Values are not looked at: infinities and NaN are stored.  Several sequences of a call
  * may write to one page, not to one slot.
  */
@@ -476,9 +478,10 @@ kvb_status kvb_paged_append(kvb_ctx* ctx, const kvb_paged_cache* cache, const kv
 
 /*
  * The same into the 8-bit cache: blocks, scales and codes as kvb_cache8_write makes
- * them, of the keys rotated in fp32 (not rounded to dtype between).  Where the position
- * is outside [0, max_pos) keys and values count as 0; a value that is not finite, after
- * the rotation for keys, is stored as 0 and recorded as KVB_ERR_NUMERIC.  One call writes
+ * them, of the keys rotated in fp32 (not rounded to dtype between).  Where rotate is 1 and
+ * the position is max_pos or above, keys and values count as 0; a value that is not finite,
+ * after the rotation for keys, is stored as 0 and recorded as KVB_ERR_NUMERIC.  Of a
+ * sequence that begins below position 0 nothing is stored.  One call writes
  * to a page from one sequence only.  dtype is that of the rows.
  */
 kvb_status kvb_cache8_append(kvb_ctx* ctx, const kvb_cache8* cache, const kvb_seqs* seqs, int32_t l_begin,
