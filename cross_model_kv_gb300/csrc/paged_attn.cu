@@ -609,7 +609,7 @@ __global__ void __launch_bounds__(32 * WARPS, sizeof(T) == 2 && NB == 1 ? 4 : 1)
     __shared__ int s_scan[WARPS];
 
     int at, stop, share, l, e, h, first;
-    if (!c8::line_start<ROWS, TILE, NT, LINE_UNIT_TILES>(P, s_scan, &s_start, at, stop, share, l, e, h, first)) return;
+    if (!c8::line_start<ROWS, TILE, NT, LINE_UNIT_TILES, 4>(P, s_scan, &s_start, at, stop, share, l, e, h, first)) return;
     const int entries = P.q.n_seq * P.row_blocks;
     auto entry = [&](int x) { return c8::row_block(P, x / P.row_blocks, x % P.row_blocks, ROWS); };
     RowBlock B = entry(e);

@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(threads_of(NR), 1) rows_kernel(const __grid_co
     W.tiles = 0;
     if (threadIdx.x == 0 && KVB_IN_BOUNDS(P.err, 2 * static_cast<int64_t>(blockIdx.x), 1, P.slots))
         P.shared[2 * blockIdx.x] = make_int4(0, 0, 0, 0);  // (until it is known, after a barrier)
-    if (!c8::line_start<NR, TK, NUM_THREADS, Walk<NR>::UNIT_TILES>(P, M.scan, &M.start, W.at, W.stop, W.share, W.l, W.e, W.h, W.first)) return;
+    if (!c8::line_start<NR, TK, NUM_THREADS, Walk<NR>::UNIT_TILES, 4>(P, M.scan, &M.start, W.at, W.stop, W.share, W.l, W.e, W.h, W.first)) return;
     if (threadIdx.x == 0) {
         for (int i = 0; i < STAGES; ++i) {
             mbar_init(&M.k_full[i], 1);
