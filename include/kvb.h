@@ -504,7 +504,11 @@ kvb_status kvb_cache8_append(kvb_ctx* ctx, const kvb_cache8* cache, const kvb_se
  * Statistics and sums are fp32.  What slots past kv_len or a query's position hold never
  * reaches it, infinities and NaN included; a visible value that is not finite makes its
  * element of the output infinite or NaN.  A page outside [0, n_pages) counts as absent and
- * is recorded.  The result does not depend on timing.
+ * is recorded.  The result does not depend on timing.  Weights are at most 2^8 before
+ * they are divided by their sum, and fp32 has to hold the sum of their products with v: 2^8
+ * times the sum of |v| over the visible keys stays below 2^128.  A call is refused whose
+ * layers x sequences x KV heads x blocks of rows (4 or 8 in fp32, 8 to 64 in bf16) x tiles
+ * of 64 keys that a sequence may have (max_kv), and 4 to 8 more tiles each, are above 2^30.
  *
  * Workspace: the context's attention workspace, with the rules of kvb_cache8_attention:
  * attention calls on one context, of both kinds of cache, never overlap on the GPU; make a
