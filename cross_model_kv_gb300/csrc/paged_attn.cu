@@ -42,7 +42,9 @@ constexpr int MMA_ROWS = 16;
 // More rows stay here, in blocks of 16, where keys are few: up to FEW_TILES tiles of a row block an SM, and up to 128 rows over
 // SHORT_KEYS / d tiles.  8 heads of 128, here / tcgen05, 40 rows: one sequence of 300, 4096, 8192 keys 10.5, 18.1, 26.5 /
 // 15.6, 19.2, 21.9 us, four of 1024, 2048 16.8, 22.4 / 18.5, 20.4; 64 of up to 250, 500, 2000 26, 34, 87 / 39, 45, 70; of 500
-// each 65 / 56.  20 rows of d 64: 64 of up to 1000 24 / 39.
+// each 65 / 56.  20 rows of d 64: 64 of up to 1000 24 / 39.  The rules see the longest sequence and the most tokens alone, and
+// lose where all sequences have as many: 64 of 5 tokens (40 rows) and 250, 500 keys each 48, 68 / 37, 56, and 500 at most
+// 54 / 49; of 8 tokens 64, 88 / 55, 75 and 71 / 73 (the first figures are of 2 to 5 tokens each).
 constexpr int FEW_TILES = 16, SHORT_KEYS = 1024;
 // Two CTAs an SM where more would cut a unit into more pieces than this, all of which one CTA joins: 8 units of 35000, 131072 keys
 // 36, 90 us with two and 42, 99 with four; 16 units of 35000 53 and 58.
@@ -50,7 +52,8 @@ constexpr int MOST_PIECES = 36;
 // A CTA for each unit, if there are more of them than SMs and they are short: up to SHORT tiles, or so many units
 // a tile that the last ones to finish do not count.  Against the line, 8 rows of d 128: 256 sequences of up to
 // 300 keys, 8 heads, 35 us and 54, 128 of up to 1000 50 and 64, 64 of 1000 each 42 and 48, 256 of up to 4000 327 and 344;
-// but 64 of up to 8192 202 and 181.
+// but 64 of up to 8192 202 and 181.  Only the longest sequence is looked at: 256 of 200 keys 46 and 47, but 255 of them and
+// one of 4000 87 and 55 (70 and 54 where that one comes first).
 constexpr int SHORT = 16;
 // Steps of a warp up to which a cluster takes a unit where there are no more units than SMs.  One row block of 8,
 // 8 heads, cluster / line: 4096 keys 10 / 14 us, 32768 34 / 41; 8 sequences of 8192 45 / 53, 16 of 1024 to 8192
@@ -76,8 +79,8 @@ struct Ring {
     static constexpr int PART = STEP * D * sizeof(T);   // bytes
     // Four warps' rings fit an SM four times in bf16, twice in fp32.  Twice in bf16, 6 parts of d 128: 16 x 32768 keys
     // 313 us against 303, 64 x 1024..8192 185 against 181, one sequence of 32768 31.6 against 34.3.  Registers for four
-    // CTAs, 128 a thread, where they suffice (8 rows; three CTAs with 164): 16 x 8192 keys 82 against 86 us, 64 of 1000
-    // 42 against 53, 128 of up to 4000 176 against 173.
+    // CTAs, 128 a thread, where they suffice (8 rows; three CTAs with 164): 64 of 1000, a CTA each, 42 against 53 us.  The line,
+    // which runs three, takes the same time with either (16 x 32768 keys 299, 64 x 8192 312 and 311, 16 x 8192 81).
     static constexpr int FIT = (sizeof(T) == 2 ? 12288 : 24576) / PART;
     static constexpr int DEPTH = FIT > 16 ? 16 : FIT;   // d 128: 3 parts
     static constexpr int BYTES = DEPTH * PART;
@@ -870,8 +873,9 @@ AttnPlan plan_attention(const Pages& c, const Seqs& q, kvb_dtype dtype, int g, i
     }
     int fit = 1;
     if (!p.tensor) pick(dtype, c.d, p, nullptr, nullptr, &fit);
-    // three CTAs an SM at most, although four fit: 16 x 32768 keys 299 us and 305, 32 of 1024 to 16384 176 and 181, 8 x 20000
-    // 103 and 106 (64 x 8192 312 and 302)
+    // three CTAs an SM at most, although four fit: 16 x 32768 keys 299 us and 308, 64 of 1024 to 8192 177 and 185, 32 of 2048 to
+    // 16384 176 and 183, 8 x 20000 103 and 108, 8 x 35000 169 and 176; but 64 x 8192 312 and 304, which no size that the
+    // host knows tells from the others
     if (fit > 3) fit = 3;
     if (fit > 2 && p.units * MOST_PIECES < static_cast<int64_t>(num_sms) * fit) fit = 2;
     // the CTAs that fit the GPU, no more than the keys give the least share to
