@@ -39,6 +39,12 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
                  : "memory");
 }
 
+// Count `bytes` as arrived in the current phase: of copies that will not come.
+__device__ __forceinline__ void mbar_complete_tx(uint64_t* bar, uint32_t bytes) {
+    asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes)
+                 : "memory");
+}
+
 // Bulk copy global -> shared (16-byte aligned addresses, size a multiple of 16),
 // completing `bytes` transactions on `bar`.
 __device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -361,6 +367,19 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
 // 32-bit store into the shared memory of a CTA of the cluster (address from mapa_shared).
 __device__ __forceinline__ void st_shared_cluster_u32(uint32_t cluster_addr, uint32_t v) {
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
+}
+// The end of a CTA pair whose loads complete on rank 0's full barriers: rank 0 waits for all that both have asked
+// for, when neither asks any more.  own, partner: uses of the ring's stages that rank 0 armed, for its own `bytes` and
+// rank 1's, and that rank 1 asked loads for.  After a wait that gave up one of them may be ahead of the other.
+template <int STAGES>
+__device__ __forceinline__ void drain_pair(uint64_t* full, uint32_t own, uint32_t partner, uint32_t bytes, uint64_t limit_ns) {
+    const uint32_t all = own > partner ? own : partner;
+    for (uint32_t u = all > STAGES ? all - STAGES : 0; u < all; ++u) {
+        uint64_t* b = &full[u % STAGES];
+        if (u >= own) mbar_arrive_expect_tx(b, bytes);
+        else if (u >= partner) mbar_complete_tx(b, bytes);
+        mbar_wait_drain(b, (u / STAGES) & 1u, limit_ns);
+    }
 }
 // TMA load into this CTA's shared memory signalling an mbarrier of either CTA of the pair.
 __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* m, uint32_t mbar_cluster, int x, int y,

@@ -349,6 +349,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     volatile int* ring = reinterpret_cast<volatile int*>(sempty + PRING);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(const_cast<int*>(ring + PRING));
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    uint32_t* asked = tmem_slot + 2;  // [rank], on rank 0: stages that the producers asked loads for
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -406,8 +407,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             // ---------------------------------------------------- producer (both CTAs; rank 0 claims)
             int stage = 0;
             uint32_t phase = 0;
-            int issued_phase[PSTAGES];
-            for (int s = 0; s < PSTAGES; ++s) issued_phase[s] = -1;
+            uint32_t issued = 0;
             bool ok = true;
             while (ok) {
                 int t;
@@ -445,18 +445,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         kb = 0;
                         product_maps(M, job, P.nprod - 1 - seg, ma, mb);
                     }
-                    issued_phase[stage] = static_cast<int>(phase);
+                    ++issued;
                     if (++stage == PSTAGES) {
                         stage = 0;
                         phase ^= 1u;
                     }
                 }
             }
-            // the leader's full barriers count both CTAs' bytes: drain there
-            if (leader)
-                for (int s = 0; s < PSTAGES; ++s)
-                    if (issued_phase[s] >= 0)
-                        mbar_wait_drain(&full[s], static_cast<uint32_t>(issued_phase[s]), DRAIN_NS);
+            st_shared_cluster_u32(mapa_shared(smem_u32(asked + rank), 0), issued);
         }
     } else if (warp == 1) {
         if (lane == 0 && leader) {
@@ -529,6 +525,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
 
     tc_fence_before();
+    cluster_sync_all();  // neither CTA asks for loads any more
+    if (leader && threadIdx.x == 0) drain_pair<PSTAGES>(full, asked[0], asked[1], PSTAGE_BYTES, DRAIN_NS);
+    __syncwarp();
     cluster_sync_all();  // no CTA leaves while its pair may still read its shared memory or TMEM
     if (warp == 1) {
         __syncwarp();

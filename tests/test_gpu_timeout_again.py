@@ -1,0 +1,56 @@
+"""Maps whose waits give up, again and again, each followed at once by a call that has to be right: CTAs of a
+pair that give up at different stages wait for the loads of both."""
+import numpy as np
+import pytest
+
+from cases import TOL_BF16, TOL_F32, ApplyCase, rel_fro, spec
+from test_gpu_fit import kvb  # noqa: F401  (kvb: the fixture)
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+KVB_ERR_TIMEOUT = 7
+
+
+def outcome(kvb, ctx):  # noqa: F811
+    try:
+        kvb.kvb_ctx_check(ctx)
+        return 0
+    except kvb.KvbError as e:
+        return e.status
+
+
+@pytest.mark.parametrize("dtype,T,fused", [(torch.bfloat16, 300, "1"), (torch.bfloat16, 4096, "1"), (torch.bfloat16, 4096, "0"), (torch.float32, 700, "1")])
+def test_maps_that_give_up_leave_the_next_one_right(kvb, dtype, T, fused, monkeypatch):  # noqa: F811
+    # short maps may be through before a wait has looked at the clock; long ones are not
+    monkeypatch.setenv("KVB_MAP_FUSED_STRIP", fused)
+    c = ApplyCase(4, 6, 4, 128, 3, T, 1e6, 1e4, dtype, seed=T, host=False)
+    mk = lambda: kvb.kvb_ctx_create(spec(c.L_s, c.H, c.d, c.theta_s), spec(c.L_t, c.H, c.d, c.theta_t), c.k, T)
+    monkeypatch.setenv("KVB_WAIT_TIMEOUT_MS", "0")
+    ctx0 = mk()
+    monkeypatch.delenv("KVB_WAIT_TIMEOUT_MS")
+    ctx1 = mk()
+    c.run(kvb, ctx1)
+    kvb.kvb_ctx_check(ctx1)
+    want = c.out_k.clone(), c.out_v.clone()
+    tok = np.unique(np.concatenate([np.random.default_rng(0).choice(T, 64, replace=False), [0, T - 1]]))
+    ok, ov = c.oracle([0, 5], tok)
+    gk, gv = c.gpu([0, 5], tok)
+    tol = TOL_BF16 if dtype == torch.bfloat16 else TOL_F32
+    assert rel_fro(gk, ok) <= tol and rel_fro(gv, ov) <= tol
+    seen, times = set(), []
+    for _ in range(15):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        c.run(kvb, ctx0)
+        b.record()
+        c.run(kvb, ctx1)
+        seen.add(outcome(kvb, ctx0))
+        kvb.kvb_ctx_check(ctx1)
+        assert torch.equal(c.out_k, want[0]) and torch.equal(c.out_v, want[1])
+        times.append(a.elapsed_time(b))
+    assert seen <= {0, KVB_ERR_TIMEOUT}
+    # a wait for loads that the other CTA of a pair never asked for would run for 200 ms
+    assert min(times) < 200, times
+    if T == 4096:
+        assert KVB_ERR_TIMEOUT in seen
