@@ -151,7 +151,8 @@ __global__ void __launch_bounds__(GTHREADS, 1) gather_all_kernel(const __grid_co
         bool reg_rows = false, reg_pos = false;
         int tok0 = 0, p0 = 0;
         uint32_t te_par = 0;   // next phase of tab_empty to wait for
-        int issued = 0;
+        int issued = 0;        // items
+        uint32_t tables = 0;   // table runs whose copies were asked for
         bool ok = true;
         // the current matrix's parameters
         int pm = -1;
@@ -269,6 +270,7 @@ __global__ void __launch_bounds__(GTHREADS, 1) gather_all_kernel(const __grid_co
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(tab_full);
+                ++tables;
                 loaded = key;
             }
         }
@@ -286,6 +288,7 @@ __global__ void __launch_bounds__(GTHREADS, 1) gather_all_kernel(const __grid_co
             const uint64_t limit = err.timeout_ns + 1000000000ull;
             for (int j = issued - GSTAGES > 0 ? issued - GSTAGES : 0; j < issued; ++j)
                 mbar_wait_drain(full + j % GSTAGES, (j / GSTAGES) & 1, limit);
+            if (tables > 0) mbar_wait_drain(tab_full, (tables - 1) & 1, limit);  // the runs before it were used
         }
         return;
     }

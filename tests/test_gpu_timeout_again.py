@@ -1,10 +1,10 @@
-"""Maps whose waits give up, again and again, each followed at once by a call that has to be right: CTAs of a
-pair that give up at different stages wait for the loads of both."""
+"""Maps and statistics whose waits give up, again and again, each followed at once by a call that has to be right:
+CTAs of a pair that give up at different stages wait for the loads of both, the gather for its table's."""
 import numpy as np
 import pytest
 
-from cases import TOL_BF16, TOL_F32, ApplyCase, rel_fro, spec
-from test_gpu_fit import kvb  # noqa: F401  (kvb: the fixture)
+from cases import TOL_BF16, TOL_F32, ApplyCase, make_pair, rel_fro, round_pair, spec
+from test_gpu_fit import _accumulate, _check_stats, _ctx, kvb  # noqa: F401  (kvb: the fixture)
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -54,3 +54,21 @@ def test_maps_that_give_up_leave_the_next_one_right(kvb, dtype, T, fused, monkey
     assert min(times) < 200, times
     if T == 4096:
         assert KVB_ERR_TIMEOUT in seen
+
+
+def test_statistics_that_give_up_leave_the_next_ones_right(kvb, monkeypatch):  # noqa: F811
+    pair = round_pair(make_pair(21, 4, 3, 2, 128, 2, 1024, 4, 1e4, 1e6, noise=1e-2, sigma=1.0), torch.bfloat16)
+    monkeypatch.setenv("KVB_WAIT_TIMEOUT_MS", "0")
+    ctx0 = _ctx(kvb, pair, 1024)
+    monkeypatch.delenv("KVB_WAIT_TIMEOUT_MS")
+    ctx1 = _ctx(kvb, pair, 1024)
+    st0, seen = kvb.kvb_stats_create(ctx0, kvb.KVB_BF16, 1024), set()
+    for _ in range(4):
+        st1 = kvb.kvb_stats_create(ctx1, kvb.KVB_BF16, 1024)
+        for seq in pair["calib"]:
+            _accumulate(kvb, ctx0, st0, [seq], torch.bfloat16)
+            seen.add(outcome(kvb, ctx0))
+            _accumulate(kvb, ctx1, st1, [seq], torch.bfloat16)
+        kvb.kvb_ctx_check(ctx1)
+        _check_stats(kvb, st1, pair, 1e-4)
+    assert seen <= {0, KVB_ERR_TIMEOUT}
